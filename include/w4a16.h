@@ -449,6 +449,137 @@ w4a16_path_t w8a16_linear_choose_path(int64_t m, int64_t n, int64_t k);
  */
 const char* w4a16_status_string(w4a16_status_t status);
 
+/* ------------------------------------------------------------------------
+ * Serving operators around the layer's projections: keys and values in a
+ * paged 4-bit cache, attention over it, and low-rank adapters beside a shared
+ * projection.  They follow the conventions at the top of this file; page
+ * numbers, slots, positions, lengths and adapter indices are read on the
+ * device and checked there against the buffers, so a bad one gives the
+ * outcome stated at the argument and never an access outside them.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * Bytes of a cache of `pages` pages of `page_size` tokens (a multiple of 16,
+ * at most 4096) for kv_heads heads of head_dim channels (64, 128 or 256), or
+ * 0 for invalid sizes.  Keys and values are kept as the weights are: signed
+ * 4-bit codes with one FP32 scale per token, head and group of
+ * min(head_dim, 128) channels.  A page of one head is one contiguous region of
+ *   page_size * head_dim + 8 * page_size * (head_dim / min(head_dim, 128))
+ * bytes, [pages][kv_heads][region]; inside it is the library's own execution
+ * layout (write it with kv4_append, read it with kv4_read).  The buffer needs
+ * no initialisation: only stored tokens are read as values.
+ */
+size_t kv4_pool_bytes(int64_t pages, int64_t page_size, int64_t kv_heads, int64_t head_dim);
+
+/*
+ * Rotates, quantizes and stores the keys and values of `tokens` tokens, and
+ * rotates their queries.
+ *   qkv        device, [tokens][ldqkv] of dtype (BF16 or F16), rows
+ *              [heads | kv_heads | kv_heads] heads of head_dim: queries, keys,
+ *              values (a fused projection's output); 16-byte aligned, ldqkv a
+ *              multiple of 8.  heads may be 0 (q_out unused).
+ *   rope       device FP32 [rope_len][rot_dim], or NULL for no rotation: row p
+ *              holds the cosines, then the sines, of rot_dim / 2 angles at
+ *              position p; 4-byte aligned.  rot_dim is a multiple of 16, at
+ *              most head_dim; channels from rot_dim on are not rotated.
+ *              With interleaved == 0 channel i turns with i + rot_dim / 2,
+ *              else 2i with 2i + 1:  (a, b) -> (a c - b s, b c + a s), each
+ *              product, difference and sum one FP32 operation.
+ *   positions  device, [tokens] int32 (NULL exactly when rope is): a token
+ *              whose position is not in [0, rope_len) is not stored, and its
+ *              queries are NaN.
+ *   slots      device, [tokens] int64: page * page_size + token in page.  A
+ *              token whose slot is not in the pool (-1, say) is not stored.
+ *              Two tokens of a call must not share a slot.
+ *   pool       device, kv4_pool_bytes(...) bytes, 16-byte aligned.
+ *   q_out      device, [tokens][heads * head_dim] of dtype, 16-byte aligned.
+ * Keys (after the rotation, in FP32) and values are quantized round-to-nearest:
+ *   s = fl32(max|x| / 7), q = clamp(round_half_even(fl32(x / s)), -8, 7), 0 if s == 0.
+ * Returns W4A16_OK (also for tokens == 0), W4A16_EINVAL, W4A16_EUNSUPPORTED or W4A16_EHIP.
+ */
+w4a16_status_t kv4_append(const void* qkv, w4a16_dtype_t dtype, int64_t tokens, int64_t ldqkv, int64_t heads,
+                          int64_t kv_heads, int64_t head_dim, const float* rope, int64_t rope_len, int64_t rot_dim,
+                          int interleaved, const int32_t* positions, const int64_t* slots, void* pool, int64_t pages,
+                          int64_t page_size, void* q_out, void* stream);
+
+/*
+ * The stored values of `tokens` slots: k, v [tokens][kv_heads][head_dim] of
+ * out_dtype (F32, BF16 or F16; code * scale in FP32, rounded once), 16-byte
+ * aligned; zeros where a slot is not in the pool.
+ * Returns W4A16_OK (also for tokens == 0), W4A16_EINVAL, W4A16_EUNSUPPORTED or W4A16_EHIP.
+ */
+w4a16_status_t kv4_read(const void* pool, int64_t pages, int64_t page_size, int64_t kv_heads, int64_t head_dim,
+                        const int64_t* slots, int64_t tokens, w4a16_dtype_t out_dtype, void* k, void* v, void* stream);
+
+/*
+ * Workspace bytes of kv4_attention for these sizes (0: none needed, or
+ * invalid sizes).  ragged: whether cu_q is given.  The header rules of
+ * w4a16_linear's workspace hold, so one workspace serves both.
+ */
+size_t kv4_attention_workspace_bytes(int64_t tokens, int64_t batch, int64_t heads, int64_t kv_heads, int64_t head_dim,
+                                     int64_t table_width, int64_t page_size, int ragged, int causal, int64_t window);
+
+/*
+ * out = softmax(scale q k^T) v over the cache, for `batch` requests.
+ *   q          device, [tokens][ldq] of dtype (BF16 or F16), rows of heads *
+ *              head_dim; heads is a multiple of kv_heads, query head h reads
+ *              key head h / (heads / kv_heads); 16-byte aligned, ldq a
+ *              multiple of 8.
+ *   table      device, [batch][ldt] int32, ldt >= table_width: the pages of a
+ *              request's tokens in order.  Tokens on a page number outside the
+ *              pool are not seen.
+ *   kv_lens    device, [batch] int32: tokens of the request in the cache, its
+ *              query tokens among them (the last ones).  Taken as at least 0
+ *              and at most table_width * page_size.
+ *   cu_q       device, [batch + 1] int32: request b's query tokens are rows
+ *              cu_q[b] .. cu_q[b+1] - 1; cu_q[0] = 0, not decreasing,
+ *              cu_q[batch] = tokens (other rows are not written).  NULL: one
+ *              query token a request, tokens == batch.
+ *   causal     1: a query at position p = kv_len - (its distance from the
+ *              request's end) sees tokens <= p; 0: all of them.
+ *   window     > 0: a query sees only tokens nearer to it than window
+ *              (p - t < window, and t - p < window without causal); 0: none.
+ *   out        device, [tokens][ldo] of dtype, 16-byte aligned, ldo a
+ *              multiple of 8.  A query that sees nothing gives zeros.
+ *   workspace  as w4a16_linear's.
+ * Logits, softmax and sums are FP32; the probabilities enter the second
+ * product as f16.
+ * Returns W4A16_OK (also for tokens == 0), W4A16_EINVAL, W4A16_EUNSUPPORTED,
+ * W4A16_EWORKSPACE or W4A16_EHIP.
+ */
+w4a16_status_t kv4_attention(const void* q, w4a16_dtype_t dtype, int64_t tokens, int64_t ldq, int64_t heads,
+                             int64_t kv_heads, int64_t head_dim, const void* pool, int64_t pages, int64_t page_size,
+                             const int32_t* table, int64_t table_width, int64_t ldt, const int32_t* kv_lens,
+                             const int32_t* cu_q, int64_t batch, int causal, int64_t window, float scale, void* out,
+                             int64_t ldo, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of lora_add (0 for invalid or empty sizes); header rules as above. */
+size_t lora_add_workspace_bytes(int64_t m, int64_t n, int64_t k, int64_t adapters, int64_t rank);
+
+/*
+ * out[i] = y[i] + scales[l] * (x[i] A_l^T) B_l^T with l = index[i]: low-rank
+ * adapters of many requests beside a shared projection's output y.
+ *   x        device, [m][ldx] of dtype (BF16 or F16), k columns (a multiple of
+ *            8); 16-byte aligned, ldx a multiple of 8.
+ *   a, b     device, [adapters][rank][k] and [adapters][n][rank] of dtype,
+ *            16-byte aligned; rank a multiple of 8, at most 128 (pad a smaller
+ *            adapter with zeros).
+ *   index    device, [m] int32, in any order; a row whose index is not in
+ *            [0, adapters) (-1, say) gets out = y.
+ *   scales   device, [adapters] FP32, or NULL for 1.
+ *   y, out   device, [m][ldy] and [m][ldo] of dtype, n columns; out may be y
+ *            itself (same ld), else they must not overlap.
+ *   workspace  as w4a16_linear's.
+ * Sums are FP32; the product with A enters the second one with at least 16
+ * significant bits; one rounding, of out.
+ * Returns W4A16_OK (also for m == 0 or n == 0), W4A16_EINVAL,
+ * W4A16_EUNSUPPORTED, W4A16_EWORKSPACE or W4A16_EHIP.
+ */
+w4a16_status_t lora_add(const void* x, w4a16_dtype_t dtype, int64_t m, int64_t k, int64_t ldx, const void* a,
+                        const void* b, int64_t adapters, int64_t rank, int64_t n, const int32_t* index,
+                        const float* scales, const void* y, int64_t ldy, void* out, int64_t ldo, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,315 @@
+"""Serving operators around the layer's projections: keys and values in a
+paged 4-bit cache, attention over it, and low-rank adapters beside a shared
+projection (the kv4_* and lora_add entry points of include/w4a16.h).
+
+Argument marshalling and checks from metadata only, as in ``_binding``."""
+from __future__ import annotations
+
+import ctypes
+import math
+
+import torch
+
+from ._binding import _act_tag, _check, _w_tag, lib, workspace_for
+
+_declared = False
+
+
+def _lib():
+    global _declared
+    L = lib()
+    if not _declared:
+        i64, i32, vp, sz = ctypes.c_int64, ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t
+        L.kv4_pool_bytes.argtypes = [i64] * 4
+        L.kv4_pool_bytes.restype = sz
+        L.kv4_append.argtypes = [vp, i32, i64, i64, i64, i64, i64, vp, i64, i64, i32, vp, vp, vp, i64, i64, vp, vp]
+        L.kv4_append.restype = i32
+        L.kv4_read.argtypes = [vp, i64, i64, i64, i64, vp, i64, i32, vp, vp, vp]
+        L.kv4_read.restype = i32
+        L.kv4_attention_workspace_bytes.argtypes = [i64] * 7 + [i32, i32, i64]
+        L.kv4_attention_workspace_bytes.restype = sz
+        L.kv4_attention.argtypes = [vp, i32, i64, i64, i64, i64, i64, vp, i64, i64, vp, i64, i64, vp, vp, i64, i32, i64,
+                                    ctypes.c_float, vp, i64, vp, sz, vp]
+        L.kv4_attention.restype = i32
+        L.lora_add_workspace_bytes.argtypes = [i64] * 5
+        L.lora_add_workspace_bytes.restype = sz
+        L.lora_add.argtypes = [vp, i32, i64, i64, i64, vp, vp, i64, i64, i64, vp, vp, vp, i64, vp, i64, vp, sz, vp]
+        L.lora_add.restype = i32
+        _declared = True
+    return L
+
+
+def _workspace(workspace, need: int, device, stream: int):
+    """(pointer, bytes) of the caller's workspace, or of this stream's."""
+    if workspace is None:
+        if need == 0:
+            return None, 0
+        if torch.cuda.is_current_stream_capturing():
+            raise ValueError(f"this call needs a {need}-byte workspace: under graph capture pass a "
+                             "zero-filled workspace= allocated before the capture")
+        workspace = workspace_for(device, stream, need)
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _same_device(first, **others):
+    if not first.is_cuda:
+        raise ValueError("tensors must be on a GPU device")
+    for name, t in others.items():
+        if t is not None and t.device != first.device:
+            raise ValueError(f"{name} must be on {first.device}, got {t.device}")
+
+
+def _vector(t, dtype, n, what):
+    if t.dtype != dtype or t.dim() != 1 or t.shape[0] != n:
+        raise ValueError(f"{what} must be a [{n}] tensor of {dtype}, got {tuple(t.shape)} of {t.dtype}")
+    if n > 1 and t.stride(0) != 1:
+        raise ValueError(f"{what} must be contiguous")
+
+
+def _no_grad(**ts):
+    for name, t in ts.items():
+        if t is not None and t.requires_grad:
+            raise ValueError(f"inference only: {name} requires a gradient")
+
+
+# ---------------------------------------------------------------------------
+# the cache
+# ---------------------------------------------------------------------------
+
+
+def _region(page_size: int, head_dim: int) -> int:
+    return page_size * head_dim + 8 * page_size * (head_dim // min(head_dim, 128))
+
+
+def kv4_pool(pages: int, page_size: int, kv_heads: int, head_dim: int, device="cuda") -> torch.Tensor:
+    """A 4-bit cache of ``pages`` pages of ``page_size`` tokens: uint8
+    [pages, kv_heads, bytes of a page of one head].  page_size is a multiple
+    of 16 (at most 4096); head_dim is 64, 128 or 256."""
+    if _lib().kv4_pool_bytes(pages, page_size, kv_heads, head_dim) == 0:
+        raise ValueError(f"no such cache: pages={pages}, page_size={page_size} (a multiple of 16, at most 4096), "
+                         f"kv_heads={kv_heads}, head_dim={head_dim} (64, 128 or 256)")
+    return torch.zeros(pages, kv_heads, _region(page_size, head_dim), dtype=torch.uint8, device=device)
+
+
+def kv4_page_size(pool: torch.Tensor, head_dim: int) -> int:
+    """Tokens of a page of ``pool`` (from kv4_pool) with heads of head_dim channels."""
+    if head_dim not in (64, 128, 256):
+        raise ValueError(f"head_dim is 64, 128 or 256, got {head_dim}")
+    if pool.dtype != torch.uint8 or pool.dim() != 3 or not pool.is_contiguous():
+        raise ValueError("pool must be a contiguous uint8 [pages, kv_heads, region] tensor (kv4_pool)")
+    page, rest = divmod(pool.shape[2], head_dim + 8 * (head_dim // min(head_dim, 128)))
+    if rest or page % 16 or not 16 <= page <= 4096 or pool.shape[0] < 1 or pool.shape[1] < 1:
+        raise ValueError(f"pool of shape {tuple(pool.shape)} does not hold pages of heads of {head_dim} channels")
+    return page
+
+
+def rope_table(length: int, rot_dim: int, base: float = 10000.0, factor: float = 1.0, original_length: int | None = None,
+               low_turns: float = 1.0, high_turns: float = 32.0, magnitude: float = 1.0, device="cuda") -> torch.Tensor:
+    """Rotation table of kv4_append: FP32 [length, rot_dim], row p the cosines
+    then the sines of p * base^(-2i / rot_dim), i < rot_dim / 2, computed in 64
+    bits (FP32 angles lose far positions).
+
+    For contexts longer than a model was trained on, ``factor`` > 1 stretches
+    the angles: all of them by 1 / factor, or, with ``original_length`` given,
+    by wavelength: those that turn more than ``high_turns`` times over the
+    original length stay, those that turn less than ``low_turns`` are divided
+    by factor, with a linear ramp between.  ``magnitude`` multiplies the table
+    (a correction of the logits' temperature)."""
+    if length < 1 or rot_dim < 16 or rot_dim % 16:
+        raise ValueError(f"a table of at least one position and a multiple of 16 channels, got {length} x {rot_dim}")
+    if base <= 0 or factor < 1 or (original_length is not None and not 0 < low_turns < high_turns):
+        raise ValueError("base > 0, factor >= 1 and 0 < low_turns < high_turns are needed")
+    freq = float(base) ** (-torch.arange(0, rot_dim, 2, dtype=torch.float64, device=device) / rot_dim)
+    if original_length is None:
+        freq = freq / factor
+    else:
+        turns = original_length * freq / (2 * math.pi)
+        keep = ((turns - low_turns) / (high_turns - low_turns)).clamp(0, 1)
+        freq = freq * (keep + (1 - keep) / factor)
+    angle = torch.arange(length, dtype=torch.float64, device=device)[:, None] * freq
+    return torch.cat((angle.cos(), angle.sin()), 1).mul_(magnitude).float()
+
+
+def kv4_append(qkv: torch.Tensor, pool: torch.Tensor, slots: torch.Tensor, head_dim: int,
+               positions: torch.Tensor | None = None, rope: torch.Tensor | None = None, interleaved: bool = False,
+               q_out: torch.Tensor | None = None) -> torch.Tensor:
+    """Stores keys and values of ``qkv`` [tokens, (heads + 2 kv_heads) head_dim]
+    (bf16/f16, a fused projection's output) in ``pool`` at ``slots`` [tokens]
+    int64 (page * page_size + token; outside the pool, -1 say: not stored),
+    rotated by ``rope`` (rope_table) at ``positions`` [tokens] int32 and
+    quantized to 4 bits; returns the rotated queries [tokens, heads, head_dim].
+    See kv4_append in include/w4a16.h."""
+    page = kv4_page_size(pool, head_dim)
+    tag = _act_tag(qkv.dtype)
+    pages, kv_heads = pool.shape[0], pool.shape[1]
+    if qkv.dim() != 2 or qkv.stride(1) != 1 or (qkv.shape[0] > 1 and qkv.stride(0) % 8):
+        raise ValueError("qkv must be 2-D with contiguous rows and a row stride that is a multiple of 8")
+    tokens, width = qkv.shape
+    heads = width // head_dim - 2 * kv_heads
+    if width % head_dim or heads < 0:
+        raise ValueError(f"qkv rows of {width} do not hold 2 x {kv_heads} key and value heads of {head_dim}")
+    _vector(slots, torch.int64, tokens, "slots")
+    _no_grad(qkv=qkv)
+    if (rope is None) != (positions is None):
+        raise ValueError("rope and positions go together")
+    rope_len = rot = 0
+    if rope is not None:
+        if rope.dtype != torch.float32 or rope.dim() != 2 or not rope.is_contiguous():
+            raise ValueError("rope must be a contiguous float32 [positions, rot_dim] table (rope_table)")
+        rope_len, rot = rope.shape
+        if rot % 16 or not 16 <= rot <= head_dim or rope_len < 1:
+            raise ValueError(f"rope has {rope_len} x {rot}: rot_dim is a multiple of 16, at most head_dim")
+        _vector(positions, torch.int32, tokens, "positions")
+    _same_device(qkv, pool=pool, slots=slots, positions=positions, rope=rope, q_out=q_out)
+    if q_out is None:
+        q_out = torch.empty((tokens, heads, head_dim), dtype=qkv.dtype, device=qkv.device)
+    elif q_out.shape != (tokens, heads, head_dim) or q_out.dtype != qkv.dtype or not q_out.is_contiguous():
+        raise ValueError("q_out must be a contiguous [tokens, heads, head_dim] tensor of qkv's dtype")
+    st = _lib().kv4_append(qkv.data_ptr(), tag, tokens, qkv.stride(0) if tokens > 1 else (width + 7) // 8 * 8, heads, kv_heads,
+                           head_dim, None if rope is None else rope.data_ptr(), rope_len, rot, int(bool(interleaved)),
+                           None if rope is None else positions.data_ptr(), slots.data_ptr(), pool.data_ptr(), pages, page,
+                           q_out.data_ptr(), torch.cuda.current_stream(qkv.device).cuda_stream)
+    _check(st, "kv4_append")
+    return q_out
+
+
+def kv4_read(pool: torch.Tensor, slots: torch.Tensor, head_dim: int, dtype: torch.dtype = torch.bfloat16):
+    """The values stored at ``slots`` [tokens] int64: (k, v), each
+    [tokens, kv_heads, head_dim] of ``dtype`` (float32, bfloat16 or float16);
+    zeros where a slot is outside the pool."""
+    page = kv4_page_size(pool, head_dim)
+    tag = _w_tag(dtype)
+    if slots.dim() != 1:
+        raise ValueError("slots must be a 1-D int64 tensor")
+    tokens = slots.shape[0]
+    _vector(slots, torch.int64, tokens, "slots")
+    _same_device(pool, slots=slots)
+    pages, kv_heads = pool.shape[0], pool.shape[1]
+    k, v = torch.empty((2, tokens, kv_heads, head_dim), dtype=dtype, device=pool.device).unbind(0)
+    st = _lib().kv4_read(pool.data_ptr(), pages, page, kv_heads, head_dim, slots.data_ptr(), tokens, tag, k.data_ptr(),
+                         v.data_ptr(), torch.cuda.current_stream(pool.device).cuda_stream)
+    _check(st, "kv4_read")
+    return k, v
+
+
+def kv4_attention_workspace_bytes(tokens: int, batch: int, heads: int, kv_heads: int, head_dim: int, table_width: int,
+                                  page_size: int, ragged: bool = False, causal: bool = True, window: int = 0) -> int:
+    """Workspace kv4_attention needs for these sizes (``ragged``: cu_q is given)."""
+    return int(_lib().kv4_attention_workspace_bytes(tokens, batch, heads, kv_heads, head_dim, table_width, page_size,
+                                                    int(bool(ragged)), int(bool(causal)), window))
+
+
+def kv4_attention(q: torch.Tensor, pool: torch.Tensor, block_table: torch.Tensor, kv_lens: torch.Tensor,
+                  cu_q: torch.Tensor | None = None, causal: bool = True, window: int = 0, scale: float | None = None,
+                  out: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """softmax(scale q k^T) v over the 4-bit cache: q [tokens, heads, head_dim]
+    (bf16/f16) -> [tokens, heads, head_dim].  ``block_table`` [batch, width]
+    int32 holds each request's pages, ``kv_lens`` [batch] int32 its tokens in
+    the cache, the query tokens among them; ``cu_q`` [batch + 1] int32 where
+    each request's query tokens begin (None: one each).  ``scale`` defaults to
+    head_dim ** -0.5.  See kv4_attention in include/w4a16.h."""
+    if q.dim() != 3 or q.stride(2) != 1 or (q.shape[1] > 1 and q.stride(1) != q.shape[2]):
+        raise ValueError("q must be [tokens, heads, head_dim] with contiguous tokens")
+    tokens, heads, dim = q.shape
+    page = kv4_page_size(pool, dim)
+    tag = _act_tag(q.dtype)
+    pages, kv_heads = pool.shape[0], pool.shape[1]
+    if heads < 1 or heads % kv_heads:
+        raise ValueError(f"{heads} query heads do not share {kv_heads} key heads evenly")
+    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[1] < 1 or block_table.stride(1) != 1:
+        raise ValueError("block_table must be an int32 [batch, width] tensor with contiguous rows")
+    batch, width = block_table.shape
+    _vector(kv_lens, torch.int32, batch, "kv_lens")
+    if cu_q is not None:
+        _vector(cu_q, torch.int32, batch + 1, "cu_q")
+    elif tokens != batch:
+        raise ValueError(f"{tokens} query tokens for {batch} requests: pass cu_q")
+    if tokens and not batch:
+        raise ValueError("query tokens without a request")
+    window = int(window)
+    if window < 0:
+        raise ValueError("window is 0 (none) or positive")
+    ldq = q.stride(0) if tokens > 1 else heads * dim
+    _no_grad(q=q)
+    _same_device(q, pool=pool, block_table=block_table, kv_lens=kv_lens, cu_q=cu_q, out=out, workspace=workspace)
+    if out is None:
+        out = torch.empty((tokens, heads, dim), dtype=q.dtype, device=q.device)
+    elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
+        raise ValueError("out must be a contiguous tensor of q's shape and dtype")
+    L = _lib()
+    stream = torch.cuda.current_stream(q.device).cuda_stream
+    need = L.kv4_attention_workspace_bytes(tokens, batch, heads, kv_heads, dim, width, page, int(cu_q is not None),
+                                           int(bool(causal)), window)
+    ws, ws_bytes = _workspace(workspace, need, q.device, stream)
+    st = L.kv4_attention(q.data_ptr(), tag, tokens, ldq, heads, kv_heads, dim, pool.data_ptr(), pages, page,
+                         block_table.data_ptr(), width, block_table.stride(0) if batch > 1 else width, kv_lens.data_ptr(),
+                         None if cu_q is None else cu_q.data_ptr(), batch, int(bool(causal)), window,
+                         dim ** -0.5 if scale is None else float(scale), out.data_ptr(), heads * dim, ws, ws_bytes, stream)
+    _check(st, "kv4_attention")
+    return out
+
+
+# ---------------------------------------------------------------------------
+# adapters
+# ---------------------------------------------------------------------------
+
+
+def lora_add_workspace_bytes(m: int, n: int, k: int, adapters: int, rank: int) -> int:
+    """Workspace lora_add needs for these sizes."""
+    return int(_lib().lora_add_workspace_bytes(m, n, k, adapters, rank))
+
+
+def lora_add(y: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, index: torch.Tensor,
+             scales: torch.Tensor | None = None, out: torch.Tensor | None = None,
+             workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """y + scales[l] (x A_l^T) B_l^T with l = index[row]: low-rank adapters of
+    many requests beside a shared projection's output y [..., n] of x [..., k]
+    (bf16/f16).  ``a`` [adapters, rank, k] and ``b`` [adapters, n, rank], rank a
+    multiple of 8 up to 128; ``index`` [rows] int32, -1 (or any other number
+    that is no adapter) for none; ``scales`` [adapters] float32, default 1.
+    ``out=y`` adds in place."""
+    tag = _act_tag(x.dtype)
+    if a.dim() != 3 or b.dim() != 3 or not a.is_contiguous() or not b.is_contiguous():
+        raise ValueError("a [adapters, rank, k] and b [adapters, n, rank] must be contiguous 3-D tensors")
+    adapters, rank, k = a.shape
+    n = b.shape[1]
+    if b.shape != (adapters, n, rank) or adapters < 1:
+        raise ValueError(f"a {tuple(a.shape)} and b {tuple(b.shape)} are not [adapters, rank, k] and [adapters, n, rank]")
+    if rank % 8 or not 8 <= rank <= 128:
+        raise ValueError(f"rank is a multiple of 8, at most 128, got {rank}: pad the adapters with zeros")
+    if a.dtype != x.dtype or b.dtype != x.dtype or y.dtype != x.dtype:
+        raise ValueError(f"x, y, a and b must have one dtype, got {x.dtype}, {y.dtype}, {a.dtype}, {b.dtype}")
+    if k % 8 or x.shape[-1] != k or y.shape[-1] != n or x.shape[:-1] != y.shape[:-1]:
+        raise ValueError(f"x [..., {k}] (a multiple of 8) and y [..., {n}] are needed, got {tuple(x.shape)}, {tuple(y.shape)}")
+    _no_grad(x=x, y=y, a=a, b=b, scales=scales)
+    x2 = x if x.dim() == 2 else x.reshape(-1, k)
+    if x2.stride(1) != 1 or (x2.shape[0] > 1 and x2.stride(0) % 8):
+        x2 = x2.contiguous()
+    y2 = y if y.dim() == 2 else y.reshape(-1, n)
+    if n > 1 and y2.stride(1) != 1:
+        raise ValueError("y must have contiguous rows")
+    m = x2.shape[0]
+    _vector(index, torch.int32, m, "index")
+    if scales is not None:
+        _vector(scales, torch.float32, adapters, "scales")
+    _same_device(x, y=y, a=a, b=b, index=index, scales=scales, out=out, workspace=workspace)
+    if out is None:
+        out = torch.empty(y.shape, dtype=y.dtype, device=y.device)
+    elif out.shape != y.shape or out.dtype != y.dtype or (out is not y and not out.is_contiguous()):
+        raise ValueError("out must be y, or a contiguous tensor of y's shape and dtype")
+    elif out is y and y.dim() != 2 and not y.is_contiguous():
+        raise ValueError("y must be contiguous to be added to in place")
+    out2 = y2 if out is y else out.view(-1, n) if out.dim() != 2 else out
+    if m == 0 or n == 0:
+        return out
+    L = _lib()
+    stream = torch.cuda.current_stream(x.device).cuda_stream
+    need = L.lora_add_workspace_bytes(m, n, k, adapters, rank)
+    ws, ws_bytes = _workspace(workspace, need, x.device, stream)
+    st = L.lora_add(x2.data_ptr(), tag, m, k, x2.stride(0) if m > 1 else k, a.data_ptr(), b.data_ptr(), adapters, rank, n,
+                    index.data_ptr(), None if scales is None else scales.data_ptr(), y2.data_ptr(), y2.stride(0) if m > 1 else n,
+                    out2.data_ptr(), out2.stride(0) if m > 1 else n, ws, ws_bytes, stream)
+    _check(st, "lora_add")
+    return out
