@@ -140,6 +140,7 @@ def kv4_append(qkv: torch.Tensor, pool: torch.Tensor, slots: torch.Tensor, head_
     int64 (page * page_size + token; outside the pool, -1 say: not stored),
     rotated by ``rope`` (rope_table) at ``positions`` [tokens] int32 and
     quantized to 4 bits; returns the rotated queries [tokens, heads, head_dim].
+    Without ``rope`` nothing is rotated and positions are not read.
     See kv4_append in include/w4a16.h."""
     page = kv4_page_size(pool, head_dim)
     tag = _act_tag(qkv.dtype)
@@ -152,8 +153,8 @@ def kv4_append(qkv: torch.Tensor, pool: torch.Tensor, slots: torch.Tensor, head_
         raise ValueError(f"qkv rows of {width} do not hold 2 x {kv_heads} key and value heads of {head_dim}")
     _vector(slots, torch.int64, tokens, "slots")
     _no_grad(qkv=qkv)
-    if (rope is None) != (positions is None):
-        raise ValueError("rope and positions go together")
+    if rope is not None and positions is None:
+        raise ValueError("a rotation needs positions")
     rope_len = rot = 0
     if rope is not None:
         if rope.dtype != torch.float32 or rope.dim() != 2 or not rope.is_contiguous():
@@ -162,7 +163,7 @@ def kv4_append(qkv: torch.Tensor, pool: torch.Tensor, slots: torch.Tensor, head_
         if rot % 16 or not 16 <= rot <= head_dim or rope_len < 1:
             raise ValueError(f"rope has {rope_len} x {rot}: rot_dim is a multiple of 16, at most head_dim")
         _vector(positions, torch.int32, tokens, "positions")
-    _same_device(qkv, pool=pool, slots=slots, positions=positions, rope=rope, q_out=q_out)
+    _same_device(qkv, pool=pool, slots=slots, positions=positions if rope is not None else None, rope=rope, q_out=q_out)
     if q_out is None:
         q_out = torch.empty((tokens, heads, head_dim), dtype=qkv.dtype, device=qkv.device)
     elif q_out.shape != (tokens, heads, head_dim) or q_out.dtype != qkv.dtype or not q_out.is_contiguous():
