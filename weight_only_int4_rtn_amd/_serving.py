@@ -6,19 +6,20 @@ Argument marshalling and checks from metadata only, as in ``_binding``."""
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 
 import torch
 
 from ._binding import _act_tag, _check, _w_tag, lib, workspace_for
 
-_declared = False
+_loaded = None
 
 
 def _lib():
-    global _declared
-    L = lib()
-    if not _declared:
+    global _loaded
+    if _loaded is None:
+        L = lib()
         i64, i32, vp, sz = ctypes.c_int64, ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t
         L.kv4_pool_bytes.argtypes = [i64] * 4
         L.kv4_pool_bytes.restype = sz
@@ -35,8 +36,15 @@ def _lib():
         L.lora_add_workspace_bytes.restype = sz
         L.lora_add.argtypes = [vp, i32, i64, i64, i64, vp, vp, i64, i64, i64, vp, vp, vp, i64, vp, i64, vp, sz, vp]
         L.lora_add.restype = i32
-        _declared = True
-    return L
+        _loaded = L
+    return _loaded
+
+
+# One decoding step makes each of these calls once a layer, so their cost on the
+# host counts: the current stream's handle is taken directly (a Stream object
+# costs 2 us), workspace sizes are functions of sizes alone and are remembered,
+# and a tensor's metadata is read once.
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _workspace(workspace, need: int, device, stream: int):
@@ -53,12 +61,15 @@ def _workspace(workspace, need: int, device, stream: int):
     return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
-def _same_device(first, **others):
-    if not first.is_cuda:
+def _device_index(first, *others) -> int:
+    """The GPU that all of the tensors (or None) are on."""
+    index = first.get_device()
+    if index < 0:
         raise ValueError("tensors must be on a GPU device")
-    for name, t in others.items():
-        if t is not None and t.device != first.device:
-            raise ValueError(f"{name} must be on {first.device}, got {t.device}")
+    for t in others:
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"tensors must be on one device, got {first.device} and {t.device}")
+    return index
 
 
 def _vector(t, dtype, n, what):
@@ -68,10 +79,10 @@ def _vector(t, dtype, n, what):
         raise ValueError(f"{what} must be contiguous")
 
 
-def _no_grad(**ts):
-    for name, t in ts.items():
+def _no_grad(*ts):
+    for t in ts:
         if t is not None and t.requires_grad:
-            raise ValueError(f"inference only: {name} requires a gradient")
+            raise ValueError("inference only: autograd inputs are not supported")
 
 
 # ---------------------------------------------------------------------------
@@ -152,7 +163,7 @@ def kv4_append(qkv: torch.Tensor, pool: torch.Tensor, slots: torch.Tensor, head_
     if width % head_dim or heads < 0:
         raise ValueError(f"qkv rows of {width} do not hold 2 x {kv_heads} key and value heads of {head_dim}")
     _vector(slots, torch.int64, tokens, "slots")
-    _no_grad(qkv=qkv)
+    _no_grad(qkv)
     if rope is not None and positions is None:
         raise ValueError("a rotation needs positions")
     rope_len = rot = 0
@@ -163,16 +174,17 @@ def kv4_append(qkv: torch.Tensor, pool: torch.Tensor, slots: torch.Tensor, head_
         if rot % 16 or not 16 <= rot <= head_dim or rope_len < 1:
             raise ValueError(f"rope has {rope_len} x {rot}: rot_dim is a multiple of 16, at most head_dim")
         _vector(positions, torch.int32, tokens, "positions")
-    _same_device(qkv, pool=pool, slots=slots, positions=positions if rope is not None else None, rope=rope, q_out=q_out)
+    index = _device_index(qkv, pool, slots, positions if rope is not None else None, rope, q_out)
     if q_out is None:
-        q_out = torch.empty((tokens, heads, head_dim), dtype=qkv.dtype, device=qkv.device)
+        q_out = qkv.new_empty((tokens, heads, head_dim))
     elif q_out.shape != (tokens, heads, head_dim) or q_out.dtype != qkv.dtype or not q_out.is_contiguous():
         raise ValueError("q_out must be a contiguous [tokens, heads, head_dim] tensor of qkv's dtype")
     st = _lib().kv4_append(qkv.data_ptr(), tag, tokens, qkv.stride(0) if tokens > 1 else (width + 7) // 8 * 8, heads, kv_heads,
                            head_dim, None if rope is None else rope.data_ptr(), rope_len, rot, int(bool(interleaved)),
                            None if rope is None else positions.data_ptr(), slots.data_ptr(), pool.data_ptr(), pages, page,
-                           q_out.data_ptr(), torch.cuda.current_stream(qkv.device).cuda_stream)
-    _check(st, "kv4_append")
+                           q_out.data_ptr(), _raw_stream(index))
+    if st:
+        _check(st, "kv4_append")
     return q_out
 
 
@@ -186,20 +198,31 @@ def kv4_read(pool: torch.Tensor, slots: torch.Tensor, head_dim: int, dtype: torc
         raise ValueError("slots must be a 1-D int64 tensor")
     tokens = slots.shape[0]
     _vector(slots, torch.int64, tokens, "slots")
-    _same_device(pool, slots=slots)
+    index = _device_index(pool, slots)
     pages, kv_heads = pool.shape[0], pool.shape[1]
-    k, v = torch.empty((2, tokens, kv_heads, head_dim), dtype=dtype, device=pool.device).unbind(0)
+    k, v = pool.new_empty((2, tokens, kv_heads, head_dim), dtype=dtype).unbind(0)
     st = _lib().kv4_read(pool.data_ptr(), pages, page, kv_heads, head_dim, slots.data_ptr(), tokens, tag, k.data_ptr(),
-                         v.data_ptr(), torch.cuda.current_stream(pool.device).cuda_stream)
-    _check(st, "kv4_read")
+                         v.data_ptr(), _raw_stream(index))
+    if st:
+        _check(st, "kv4_read")
     return k, v
+
+
+@functools.lru_cache(maxsize=4096)
+def _attention_need(*sizes) -> int:
+    return int(_lib().kv4_attention_workspace_bytes(*sizes))
+
+
+@functools.lru_cache(maxsize=4096)
+def _lora_need(*sizes) -> int:
+    return int(_lib().lora_add_workspace_bytes(*sizes))
 
 
 def kv4_attention_workspace_bytes(tokens: int, batch: int, heads: int, kv_heads: int, head_dim: int, table_width: int,
                                   page_size: int, ragged: bool = False, causal: bool = True, window: int = 0) -> int:
     """Workspace kv4_attention needs for these sizes (``ragged``: cu_q is given)."""
-    return int(_lib().kv4_attention_workspace_bytes(tokens, batch, heads, kv_heads, head_dim, table_width, page_size,
-                                                    int(bool(ragged)), int(bool(causal)), window))
+    return _attention_need(tokens, batch, heads, kv_heads, head_dim, table_width, page_size, int(bool(ragged)),
+                           int(bool(causal)), window)
 
 
 def kv4_attention(q: torch.Tensor, pool: torch.Tensor, block_table: torch.Tensor, kv_lens: torch.Tensor,
@@ -233,22 +256,22 @@ def kv4_attention(q: torch.Tensor, pool: torch.Tensor, block_table: torch.Tensor
     if window < 0:
         raise ValueError("window is 0 (none) or positive")
     ldq = q.stride(0) if tokens > 1 else heads * dim
-    _no_grad(q=q)
-    _same_device(q, pool=pool, block_table=block_table, kv_lens=kv_lens, cu_q=cu_q, out=out, workspace=workspace)
+    _no_grad(q)
+    index = _device_index(q, pool, block_table, kv_lens, cu_q, out, workspace)
     if out is None:
-        out = torch.empty((tokens, heads, dim), dtype=q.dtype, device=q.device)
+        out = q.new_empty((tokens, heads, dim))
     elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
         raise ValueError("out must be a contiguous tensor of q's shape and dtype")
-    L = _lib()
-    stream = torch.cuda.current_stream(q.device).cuda_stream
-    need = L.kv4_attention_workspace_bytes(tokens, batch, heads, kv_heads, dim, width, page, int(cu_q is not None),
-                                           int(bool(causal)), window)
+    stream = _raw_stream(index)
+    causal = 1 if causal else 0
+    need = _attention_need(tokens, batch, heads, kv_heads, dim, width, page, 0 if cu_q is None else 1, causal, window)
     ws, ws_bytes = _workspace(workspace, need, q.device, stream)
-    st = L.kv4_attention(q.data_ptr(), tag, tokens, ldq, heads, kv_heads, dim, pool.data_ptr(), pages, page,
-                         block_table.data_ptr(), width, block_table.stride(0) if batch > 1 else width, kv_lens.data_ptr(),
-                         None if cu_q is None else cu_q.data_ptr(), batch, int(bool(causal)), window,
-                         dim ** -0.5 if scale is None else float(scale), out.data_ptr(), heads * dim, ws, ws_bytes, stream)
-    _check(st, "kv4_attention")
+    st = _lib().kv4_attention(q.data_ptr(), tag, tokens, ldq, heads, kv_heads, dim, pool.data_ptr(), pages, page,
+                              block_table.data_ptr(), width, block_table.stride(0) if batch > 1 else width, kv_lens.data_ptr(),
+                              None if cu_q is None else cu_q.data_ptr(), batch, causal, window,
+                              dim ** -0.5 if scale is None else float(scale), out.data_ptr(), heads * dim, ws, ws_bytes, stream)
+    if st:
+        _check(st, "kv4_attention")
     return out
 
 
@@ -259,7 +282,7 @@ def kv4_attention(q: torch.Tensor, pool: torch.Tensor, block_table: torch.Tensor
 
 def lora_add_workspace_bytes(m: int, n: int, k: int, adapters: int, rank: int) -> int:
     """Workspace lora_add needs for these sizes."""
-    return int(_lib().lora_add_workspace_bytes(m, n, k, adapters, rank))
+    return _lora_need(m, n, k, adapters, rank)
 
 
 def lora_add(y: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, index: torch.Tensor,
@@ -284,7 +307,7 @@ def lora_add(y: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor,
         raise ValueError(f"x, y, a and b must have one dtype, got {x.dtype}, {y.dtype}, {a.dtype}, {b.dtype}")
     if k % 8 or x.shape[-1] != k or y.shape[-1] != n or x.shape[:-1] != y.shape[:-1]:
         raise ValueError(f"x [..., {k}] (a multiple of 8) and y [..., {n}] are needed, got {tuple(x.shape)}, {tuple(y.shape)}")
-    _no_grad(x=x, y=y, a=a, b=b, scales=scales)
+    _no_grad(x, y, a, b, scales)
     x2 = x if x.dim() == 2 else x.reshape(-1, k)
     if x2.stride(1) != 1 or (x2.shape[0] > 1 and x2.stride(0) % 8):
         x2 = x2.contiguous()
@@ -295,9 +318,9 @@ def lora_add(y: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor,
     _vector(index, torch.int32, m, "index")
     if scales is not None:
         _vector(scales, torch.float32, adapters, "scales")
-    _same_device(x, y=y, a=a, b=b, index=index, scales=scales, out=out, workspace=workspace)
+    device = _device_index(x, y, a, b, index, scales, out, workspace)
     if out is None:
-        out = torch.empty(y.shape, dtype=y.dtype, device=y.device)
+        out = y.new_empty(y.shape)
     elif out.shape != y.shape or out.dtype != y.dtype or (out is not y and not out.is_contiguous()):
         raise ValueError("out must be y, or a contiguous tensor of y's shape and dtype")
     elif out is y and y.dim() != 2 and not y.is_contiguous():
@@ -305,12 +328,12 @@ def lora_add(y: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor,
     out2 = y2 if out is y else out.view(-1, n) if out.dim() != 2 else out
     if m == 0 or n == 0:
         return out
-    L = _lib()
-    stream = torch.cuda.current_stream(x.device).cuda_stream
-    need = L.lora_add_workspace_bytes(m, n, k, adapters, rank)
+    stream = _raw_stream(device)
+    need = _lora_need(m, n, k, adapters, rank)
     ws, ws_bytes = _workspace(workspace, need, x.device, stream)
-    st = L.lora_add(x2.data_ptr(), tag, m, k, x2.stride(0) if m > 1 else k, a.data_ptr(), b.data_ptr(), adapters, rank, n,
-                    index.data_ptr(), None if scales is None else scales.data_ptr(), y2.data_ptr(), y2.stride(0) if m > 1 else n,
-                    out2.data_ptr(), out2.stride(0) if m > 1 else n, ws, ws_bytes, stream)
-    _check(st, "lora_add")
+    st = _lib().lora_add(x2.data_ptr(), tag, m, k, x2.stride(0) if m > 1 else k, a.data_ptr(), b.data_ptr(), adapters, rank, n,
+                         index.data_ptr(), None if scales is None else scales.data_ptr(), y2.data_ptr(),
+                         y2.stride(0) if m > 1 else n, out2.data_ptr(), out2.stride(0) if m > 1 else n, ws, ws_bytes, stream)
+    if st:
+        _check(st, "lora_add")
     return out
