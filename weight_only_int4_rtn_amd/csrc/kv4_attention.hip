@@ -92,54 +92,60 @@ __device__ inline bool find_tile(const Kv4AttentionArgs& a, int64_t x, Tile& t) 
     return true;
 }
 
-// Chunks of 16 tokens -> their place in the pool.
-struct Pages {
-    const int32_t* row;
-    int width, per;      // pages a row holds, chunks per page
-    uint32_t magic;      // floor(c / per) = (c magic) >> 32 for c < 2^24, per <= 256
-    int64_t pages;
-    const uint8_t* pool; // of this key head
-    int64_t stride;      // bytes between pages
-    __device__ const uint8_t* region(int chunk, int end, int& in_page, bool& ok) const {
-        const int p = per == 1 ? chunk : int(__umulhi(uint32_t(chunk), magic));
-        in_page = chunk - p * per;
+// Where the 16-token chunks of a wave's steps lie, for 32 steps at a time: lane
+// L holds chunk L % 2 of step L / 2, so a step finds its chunks with scalar
+// reads of lanes instead of a page lookup (a scalar load and its wait) each.
+// Offsets are in units of 128 bytes (codes) and 64 bytes (scales): 32 bits
+// reach every pool that fits a GPU.
+struct Chunks {
+    uint32_t code, scale;
+    uint64_t there;  // bit L: lane L's chunk is on a page of the pool
+    // stride: chunks between a wave's steps; end: tokens
+    __device__ void find(const Kv4AttentionArgs& a, uint32_t magic, const int32_t* row, int64_t region, int chunk_bytes,
+                         int first, int stride, int end, int lane) {
+        const int c = first + lane / 2 * stride + lane % 2;
+        const int per = a.page / 16;
+        const int p = per == 1 ? c : int(__umulhi(uint32_t(c), magic));
+        const int in = c - p * per;
         int id = -1;
-        if (chunk * 16 < end && p < width) id = row[p];
-        ok = id >= 0 && id < pages;
-        return pool + (ok ? int64_t(id) * stride : 0);
+        if (c * 16 < end && p < int(a.table_width)) id = row[p];
+        const bool ok = id >= 0 && id < a.pages;
+        const uint64_t at = uint64_t(ok ? id : 0) * uint64_t(a.kv_heads * region);
+        code = ok ? uint32_t((at + uint64_t(in) * chunk_bytes) >> 7) : 0;
+        scale = ok ? uint32_t((at + uint64_t(a.page) * a.dim + in * 64) >> 6) : 0;
+        there = __ballot(ok);
     }
+    __device__ uint64_t code_at(int i) const { return uint64_t(uint32_t(__builtin_amdgcn_readlane(int(code), i))) << 7; }
+    __device__ uint64_t scale_at(int i) const { return uint64_t(uint32_t(__builtin_amdgcn_readlane(int(scale), i))) << 6; }
 };
 
-// 32 tokens of one key head, as loaded.
+// One side (keys or values) of 32 tokens of one key head, as loaded.
 template <int D>
-struct Step {
+struct Side {
     static constexpr int W = kv4_width(D), NB = kv4_blocks(D);
-    uint32_t k[2][NB][W / 32], v[2][NB][W / 32];
-    float4 ks[2][NB], vs[2][NB];
-    bool ok[2];
+    uint32_t w[2][NB][W / 32];
+    float4 s[2][NB];
 
     __device__ static void words(const uint8_t* p, uint32_t (&w)[W / 32]) {
         if constexpr (W == 128) {
-            const uint4 x = *reinterpret_cast<const uint4*>(p);
+            const uint4 x = load_stream16(p);
             w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
         } else {
-            const uint2 x = *reinterpret_cast<const uint2*>(p);
+            typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+            const u32x2 x = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(p));
             w[0] = x.x; w[1] = x.y;
         }
     }
-    __device__ void load(const Pages& pg, int token, int end, int page, int lane) {
+    // codes, scales: this head's region of page 0, at the side
+    __device__ void load(const uint8_t* codes, const uint8_t* scales, const Chunks& ch, int step, int page, int lane) {
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-            int in_page;
-            const uint8_t* r = pg.region(token / 16 + c, end, in_page, ok[c]);
-            const float* sc = reinterpret_cast<const float*>(r + page * D) + in_page * 16 + 4 * (lane / 16);
+            const uint8_t* p = codes + ch.code_at(2 * step + c);
+            const uint8_t* q = scales + ch.scale_at(2 * step + c);
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
-                const uint8_t* p = r + (in_page * NB + b) * (8 * W) + lane * (W / 8);
-                words(p, k[c][b]);
-                words(p + page * (D / 2), v[c][b]);
-                ks[c][b] = *reinterpret_cast<const float4*>(sc + b * page);
-                vs[c][b] = *reinterpret_cast<const float4*>(sc + (NB + b) * page);
+                words(p + b * (8 * W) + uint32_t(lane * (W / 8)), w[c][b]);
+                s[c][b] = *reinterpret_cast<const float4*>(q + b * page * 4 + uint32_t(lane / 16 * 16));
             }
         }
     }
@@ -150,12 +156,90 @@ struct Step {
 template <int D>
 constexpr int64_t partial_floats() { return 16 * D + 32; }
 
+// One row's queries as f16, scaled by 2^e; what undoes it in the logits' base-2
+// exponent; and -24 sum(q) per block.
+template <int ACT, int D>
+__device__ inline float load_queries(const uint16_t* src, float scale, uint4 (&q)[kv4_blocks(D)][kv4_width(D) / 32],
+                                     float (&offset)[kv4_blocks(D)]) {
+    constexpr int W = kv4_width(D), NB = kv4_blocks(D);
+    uint4 raw[NB][W / 32];
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int s = 0; s < W / 32; ++s) raw[b][s] = *reinterpret_cast<const uint4*>(src + W * b + 32 * s);
+    float big = 0.0f;
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int s = 0; s < W / 32; ++s) {
+            const uint32_t w[4] = {raw[b][s].x, raw[b][s].y, raw[b][s].z, raw[b][s].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                big = fmaxf(big, fmaxf(fabsf(to_f32<ACT>(uint16_t(w[i]))), fabsf(to_f32<ACT>(uint16_t(w[i] >> 16)))));
+        }
+    big = row_max(big);
+    const int e = big > 0.0f && big < 3e38f ? 10 - (int(__float_as_uint(big) >> 23) - 127) : 0;
+    const float sign = scale < 0.0f ? -1.0f : 1.0f;  // the logits' factor is positive
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int s = 0; s < W / 32; ++s) {
+            const uint32_t w[4] = {raw[b][s].x, raw[b][s].y, raw[b][s].z, raw[b][s].w};
+            uint32_t o[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                o[i] = pack_f16(sign * ldexpf(to_f32<ACT>(uint16_t(w[i])), e), sign * ldexpf(to_f32<ACT>(uint16_t(w[i] >> 16)), e));
+            q[b][s] = make_uint4(o[0], o[1], o[2], o[3]);
+            sum += sum8<kActF16>(q[b][s]);
+        }
+        offset[b] = -kKvOffset * row_sum(sum);
+    }
+    // never 0, which would make a masked logit (-inf) NaN
+    return fmaxf(ldexpf(fabsf(scale) * kLog2e, -e), 1e-37f);
+}
+
+// A row's running softmax over some of its tokens.
+struct Running {
+    float top = -INFINITY;  // largest logit (before the factor)
+    float vlim = 0.0f;      // power of two above the value scales so far
+    float ref = -INFINITY;  // what the probabilities are relative to: top's exponent + log2(vlim)
+    float sum = 0.0f;       // this lane's part of the row's sum
+    // new references for logits up to z and value scales up to v (this row's largest); returns what
+    // the sums so far are to be multiplied by
+    __device__ float raise(float z, float v, float zf) {
+        top = fmaxf(top, z);
+        // never below 2^-60, so that the probabilities' sum stays in range
+        const int e = max(int(__float_as_uint(v) >> 23) - 126, -60);
+        vlim = fmaxf(vlim, ldexpf(1.0f, e));
+        const float now = top == -INFINITY ? -INFINITY : top * zf + __builtin_amdgcn_logf(vlim);
+        const float f = ref == -INFINITY ? 0.0f : exp2_fast(ref - now);
+        ref = now;
+        sum *= f;
+        return f;
+    }
+};
+
+// The probability operands of one step: weights p vs as f16.
+template <int D>
+__device__ inline uint4 weights(const float (&p)[2][4], const float (&vs)[2][kv4_blocks(D)][4], int b) {
+    return make_uint4(pack_f16(p[0][0] * vs[0][b][0], p[0][1] * vs[0][b][1]), pack_f16(p[0][2] * vs[0][b][2], p[0][3] * vs[0][b][3]),
+                      pack_f16(p[1][0] * vs[1][b][0], p[1][1] * vs[1][b][1]), pack_f16(p[1][2] * vs[1][b][2], p[1][3] * vs[1][b][3]));
+}
+
+constexpr uint32_t kOnes = 0x3C003C00u;  // two f16 ones
+
 // One workgroup: 16 rows of one key head over one split of the tokens.  Its
 // four waves take steps of 32 tokens in turn, each with its own running
-// maximum, and meet in LDS at the end.
+// softmax, and meet in LDS at the end.  The next step's keys are loaded as soon
+// as this step's have been used, and the values likewise, so each side has one
+// set of registers and half a step or more of work to arrive behind, and four
+// waves fit a SIMD (two for D = 256).  Splits are joined by the last of a
+// tile's workgroups to finish, in split order.
 template <int ACT, int D>
-__global__ __launch_bounds__(256) void kv4_attention_kernel(Kv4AttentionArgs a, int span, int splits, uint32_t magic,
-                                                            float* partials) {
+__global__ __launch_bounds__(256, D == 256 ? 2 : 4) void kv4_attention_kernel(Kv4AttentionArgs a, int span, int splits,
+                                                                              uint32_t magic, unsigned* counters,
+                                                                              float* partials) {
     constexpr int W = kv4_width(D), NB = kv4_blocks(D), CH = W / 16;
     constexpr int WAVES = 4;
     __shared__ float lds[WAVES / 2][NB * CH * 4 + 2][64];
@@ -169,67 +253,32 @@ __global__ __launch_bounds__(256) void kv4_attention_kernel(Kv4AttentionArgs a, 
     const int last = min(t.r0 + 15, t.rows - 1);
     const int p_first = t.position(t.r0 / share), p_last = t.position(last / share);
     const int begin = view.lo(p_first) / 32 * 32, end = view.hi(p_last, t.kv);
+    const int live = max(1, min(splits, (end - begin + span - 1) / span));  // splits with tokens
+    if (int(blockIdx.z) >= live) return;
     const int s0 = begin + int(blockIdx.z) * span, s1 = min(end, s0 + span);
-    if (splits > 1 && s0 >= end) return;
     // every row of the tile sees [all_lo, all_hi)
-    const int all_lo = view.lo(p_last), all_hi = view.hi(p_first, t.kv);
+    const int all_lo = view.lo(p_last), all_hi = min(view.hi(p_first, t.kv), s1);
+
+    const int64_t region = kv4_region(a.page, D);
+    const uint8_t* pool = a.pool + kh * region;
+    const int32_t* row = a.table + int64_t(t.b) * a.ldt;
+    const int first = s0 + 32 * wave, steps = max(0, (s1 - first + 32 * WAVES - 1) / (32 * WAVES));
+    Chunks ch;
+    ch.find(a, magic, row, region, NB * 8 * W, first / 16, 2 * WAVES, s1, lane);
+    Side<D> k, v;
+    if (steps > 0) {
+        k.load(pool, pool, ch, 0, a.page, lane);
+        v.load(pool + a.page * (D / 2), pool + NB * a.page * 4, ch, 0, a.page, lane);
+    }
 
     // columns past the last row repeat it, and are dropped at the end
     const int r = min(t.r0 + col, last);
     const int qi = r / share, hd = kh * share + r % share;
     const int pos = t.position(qi);
-    const int lo = view.lo(pos), hi = view.hi(pos, t.kv);
-
-    // queries: f16, scaled by 2^(10 - e), and -24 sum(q) per block
+    const int lo = view.lo(pos), hi = min(view.hi(pos, t.kv), s1);
     uint4 q[NB][W / 32];
-    f32x4_t init[NB];
-    float zf;
-    {
-        const uint16_t* src = a.q + (t.q0 + qi) * a.ldq + int64_t(hd) * D + 8 * kq;
-        uint4 raw[NB][W / 32];
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-#pragma unroll
-            for (int s = 0; s < W / 32; ++s) raw[b][s] = *reinterpret_cast<const uint4*>(src + W * b + 32 * s);
-        float big = 0.0f;
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-#pragma unroll
-            for (int s = 0; s < W / 32; ++s) {
-                const uint32_t w[4] = {raw[b][s].x, raw[b][s].y, raw[b][s].z, raw[b][s].w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    big = fmaxf(big, fmaxf(fabsf(to_f32<ACT>(uint16_t(w[i]))), fabsf(to_f32<ACT>(uint16_t(w[i] >> 16)))));
-            }
-        big = row_max(big);
-        const int e = big > 0.0f && big < 3e38f ? 10 - (int(__float_as_uint(big) >> 23) - 127) : 0;
-        zf = ldexpf(a.scale * kLog2e, -e);
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-            float sum = 0.0f;
-#pragma unroll
-            for (int s = 0; s < W / 32; ++s) {
-                const uint32_t w[4] = {raw[b][s].x, raw[b][s].y, raw[b][s].z, raw[b][s].w};
-                uint32_t o[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    o[i] = pack_f16(ldexpf(to_f32<ACT>(uint16_t(w[i])), e), ldexpf(to_f32<ACT>(uint16_t(w[i] >> 16)), e));
-                q[b][s] = make_uint4(o[0], o[1], o[2], o[3]);
-                sum += sum8<kActF16>(q[b][s]);
-            }
-            sum = -kKvOffset * row_sum(sum);
-            init[b] = f32x4_t{sum, sum, sum, sum};
-        }
-    }
-
-    Pages pg;
-    pg.row = a.table + int64_t(t.b) * a.ldt;
-    pg.width = int(a.table_width);
-    pg.per = a.page / 16;
-    pg.magic = magic;
-    pg.pages = a.pages;
-    pg.stride = a.kv_heads * kv4_region(a.page, D);
-    pg.pool = a.pool + kh * kv4_region(a.page, D);
+    float offset[NB];
+    const float zf = load_queries<ACT, D>(a.q + (t.q0 + qi) * a.ldq + int64_t(hd) * D + 8 * kq, a.scale, q, offset);
 
     f32x4_t acc[NB][CH], ps[NB];
 #pragma unroll
@@ -238,46 +287,48 @@ __global__ __launch_bounds__(256) void kv4_attention_kernel(Kv4AttentionArgs a, 
 #pragma unroll
         for (int i = 0; i < CH; ++i) acc[b][i] = f32x4_t{0, 0, 0, 0};
     }
-    float top = -INFINITY;   // running maximum of the row's logits (base 2)
-    int vexp = -60;          // exponent of the largest value scale so far (never below 2^-60)
-    float ref = -INFINITY;   // top + vexp: what the probabilities are relative to
-    float sum = 0.0f;        // this lane's part of the row's sum
+    Running run;
 
-    Step<D> cur, next;
-    int tok = s0 + 32 * wave;
-    if (tok < s1) cur.load(pg, tok, s1, a.page, lane);
-    for (; tok < s1; tok += 32 * WAVES) {
-        if (tok + 32 * WAVES < s1) next.load(pg, tok + 32 * WAVES, s1, a.page, lane);
-        float z[2][4], vs[2][NB][4];
+    for (int step = 0; step < steps; ++step) {
+        const int tok = first + step * 32 * WAVES;
+        const uint32_t there = uint32_t(ch.there >> (2 * (step % 32))) & 3;
+        float z[2][4];
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) z[c][i] = 0.0f;
-#pragma unroll
             for (int b = 0; b < NB; ++b) {
-                f32x4_t s = init[b];
+                f32x4_t s = {offset[b], offset[b], offset[b], offset[b]};
 #pragma unroll
                 for (int ks = 0; ks < W / 32; ++ks) {
-                    const uint32_t w = cur.k[c][b][ks];
+                    const uint32_t w = k.w[c][b][ks];
                     s = mfma(make_uint4(kv4_pair<0>(w), kv4_pair<1>(w), kv4_pair<2>(w), kv4_pair<3>(w)), q[b][ks], s);
                 }
-                const float4 kf = cur.ks[c][b], vf = cur.vs[c][b];
-                z[c][0] += s[0] * kf.x; z[c][1] += s[1] * kf.y; z[c][2] += s[2] * kf.z; z[c][3] += s[3] * kf.w;
-                vs[c][b][0] = vf.x; vs[c][b][1] = vf.y; vs[c][b][2] = vf.z; vs[c][b][3] = vf.w;
+                const float4 f = k.s[c][b];
+                const float y[4] = {s[0] * f.x, s[1] * f.y, s[2] * f.z, s[3] * f.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) z[c][i] = b == 0 ? y[i] : z[c][i] + y[i];
             }
         }
-        const bool whole = tok >= all_lo && tok + 32 <= all_hi && tok + 32 <= s1 && cur.ok[0] && cur.ok[1];
+        const bool more = step + 1 < steps;
+        if (more) {
+            if ((step + 1) % 32 == 0)
+                ch.find(a, magic, row, region, NB * 8 * W, (tok + 32 * WAVES) / 16, 2 * WAVES, s1, lane);
+            k.load(pool, pool, ch, (step + 1) % 32, a.page, lane);
+        }
+        float vs[2][NB][4];
 #pragma unroll
         for (int c = 0; c < 2; ++c)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) z[c][i] *= zf;
-        if (!whole) {
+            for (int b = 0; b < NB; ++b) {
+                vs[c][b][0] = v.s[c][b].x; vs[c][b][1] = v.s[c][b].y; vs[c][b][2] = v.s[c][b].z; vs[c][b][3] = v.s[c][b].w;
+            }
+        if (!(tok >= all_lo && tok + 32 <= all_hi && there == 3)) {
 #pragma unroll
             for (int c = 0; c < 2; ++c)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int at = tok + 16 * c + 4 * kq + i;
-                    const bool seen = cur.ok[c] && at >= lo && at < min(hi, s1);
+                    const bool seen = (there >> c & 1) && at >= lo && at < hi;
                     z[c][i] = seen ? z[c][i] : -INFINITY;
 #pragma unroll
                     for (int b = 0; b < NB; ++b) vs[c][b][i] = seen ? vs[c][b][i] : 0.0f;
@@ -293,14 +344,8 @@ __global__ __launch_bounds__(256) void kv4_attention_kernel(Kv4AttentionArgs a, 
 #pragma unroll
                 for (int b = 0; b < NB; ++b) vm = fmaxf(vm, vs[c][b][i]);
             }
-        if (__any(zm > top || vm > ldexpf(1.0f, vexp))) {
-            top = fmaxf(top, row_max(zm));
-            vm = row_max(vm);
-            vexp = max(vexp, int(__float_as_uint(vm) >> 23) - 126);
-            const float now = top + float(vexp);
-            const float f = ref == -INFINITY ? 0.0f : exp2_fast(ref - now);
-            ref = now;
-            sum *= f;
+        if (__any(zm > run.top || vm > run.vlim)) {
+            const float f = run.raise(row_max(zm), row_max(vm), zf);
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
                 ps[b] *= f;
@@ -308,30 +353,27 @@ __global__ __launch_bounds__(256) void kv4_attention_kernel(Kv4AttentionArgs a, 
                 for (int i = 0; i < CH; ++i) acc[b][i] *= f;
             }
         }
-        const float base = ref == -INFINITY ? 0.0f : ref;
+        const float base = run.ref == -INFINITY ? 0.0f : run.ref;
         float p[2][4];
 #pragma unroll
         for (int c = 0; c < 2; ++c)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                p[c][i] = exp2_fast(z[c][i] - base);
-                sum += p[c][i];
+                p[c][i] = exp2_fast(fmaf(z[c][i], zf, -base));
+                run.sum += p[c][i];
             }
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-            const uint4 pw = make_uint4(pack_f16(p[0][0] * vs[0][b][0], p[0][1] * vs[0][b][1]),
-                                        pack_f16(p[0][2] * vs[0][b][2], p[0][3] * vs[0][b][3]),
-                                        pack_f16(p[1][0] * vs[1][b][0], p[1][1] * vs[1][b][1]),
-                                        pack_f16(p[1][2] * vs[1][b][2], p[1][3] * vs[1][b][3]));
-            ps[b] = mfma(make_uint4(0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u), pw, ps[b]);
+            const uint4 pw = weights<D>(p, vs, b);
+            ps[b] = mfma(make_uint4(kOnes, kOnes, kOnes, kOnes), pw, ps[b]);
             static_for<0, CH>([&](auto ic) {
                 constexpr int i = ic, h = i / 4, ii = i % 4;
-                acc[b][i] = mfma(make_uint4(kv4_pair<ii>(cur.v[0][b][2 * h]), kv4_pair<ii>(cur.v[0][b][2 * h + 1]),
-                                            kv4_pair<ii>(cur.v[1][b][2 * h]), kv4_pair<ii>(cur.v[1][b][2 * h + 1])),
+                acc[b][i] = mfma(make_uint4(kv4_pair<ii>(v.w[0][b][2 * h]), kv4_pair<ii>(v.w[0][b][2 * h + 1]),
+                                            kv4_pair<ii>(v.w[1][b][2 * h]), kv4_pair<ii>(v.w[1][b][2 * h + 1])),
                                  pw, acc[b][i]);
             });
         }
-        cur = next;
+        if (more) v.load(pool + a.page * (D / 2), pool + NB * a.page * 4, ch, (step + 1) % 32, a.page, lane);
     }
 
     // take the offset out, then join the waves two and two
@@ -339,6 +381,7 @@ __global__ __launch_bounds__(256) void kv4_attention_kernel(Kv4AttentionArgs a, 
     for (int b = 0; b < NB; ++b)
 #pragma unroll
         for (int i = 0; i < CH; ++i) acc[b][i] -= kKvOffset * ps[b];
+    float ref = run.ref, sum = run.sum;
 #pragma unroll
     for (int half = WAVES / 2; half > 0; half /= 2) {
         if (wave >= half && wave < 2 * half) {
@@ -370,101 +413,122 @@ __global__ __launch_bounds__(256) void kv4_attention_kernel(Kv4AttentionArgs a, 
         }
         __syncthreads();
     }
-    if (wave != 0) return;
-    sum = row_sum(sum);
-    if (splits > 1) {
-        float* o = partials + ((int64_t(blockIdx.x) * a.kv_heads + kh) * splits + blockIdx.z) * partial_floats<D>();
+    uint16_t* dst = a.out + (t.q0 + qi) * a.ldo + int64_t(hd) * D;
+    if (live == 1) {
+        if (wave != 0 || t.r0 + col > last) return;
+        sum = row_sum(sum);
+        const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint32_t w[CH / 2];
+#pragma unroll
+                for (int i = 0; i < CH / 2; ++i)
+                    w[i] = uint32_t(from_f32<ACT>(acc[b][2 * i][j] * inv)) | (uint32_t(from_f32<ACT>(acc[b][2 * i + 1][j] * inv)) << 16);
+                uint16_t* to = dst + W * b + CH * (4 * kq + j);
+                if constexpr (CH == 8) *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
+                else *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[1]);
+            }
+        return;
+    }
+
+    // A split stores its sums past the L2 (SC1: the XCDs' L2s are not coherent)
+    // and counts itself; the one that completes the count joins them all and
+    // clears the counter for the next call.  Nobody waits.
+    const int64_t tile = int64_t(blockIdx.x) * a.kv_heads + kh;
+    typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+    constexpr int kSlot = int(partial_floats<D>() * 4), kRefs = 16 * D * 4;
+    const __amdgpu_buffer_rsrc_t slots = buffer_rsrc(partials + tile * splits * partial_floats<D>(), int64_t(splits) * kSlot);
+    int* last_one = reinterpret_cast<int*>(&lds[1][0][0]);  // the second join round read lds[0] only
+    if (wave == 0) {
+        sum = row_sum(sum);
+        const int at = int(blockIdx.z) * kSlot;
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
             for (int i = 0; i < CH; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) o[((b * CH + i) * 4 + j) * 64 + lane] = acc[b][i][j];
+                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc[b][i]), slots,
+                                                       at + ((b * CH + i) * 64 + lane) * 16, 0, kCoherent);
         if (kq == 0) {
-            o[16 * D + col] = ref;
-            o[16 * D + 16 + col] = sum;
+            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(ref), slots, at + kRefs + col * 4, 0, kCoherent);
+            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(sum), slots, at + kRefs + 64 + col * 4, 0, kCoherent);
         }
-        return;
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        if (lane == 0) {
+            const unsigned before = __hip_atomic_fetch_add(counters + tile, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            *last_one = before == unsigned(live - 1);
+            if (*last_one) __hip_atomic_store(counters + tile, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+    }
+    __syncthreads();
+    if (!*last_one) return;
+    // wave w joins the accumulators i = PER w .. PER w + PER - 1 of each block
+    constexpr int PER = CH / WAVES;
+    float total = 0.0f;
+    ref = -INFINITY;
+    f32x4_t out[NB][PER];
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int i = 0; i < PER; ++i) out[b][i] = f32x4_t{0, 0, 0, 0};
+    constexpr int BATCH = 4;
+    for (int sp = 0; sp < live; sp += BATCH) {
+        u32x4 part[BATCH][NB][PER];
+        float refs[BATCH], sums[BATCH];
+#pragma unroll
+        for (int g = 0; g < BATCH; ++g) {
+            const int at = min(sp + g, live - 1) * kSlot;
+            refs[g] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(slots, at + kRefs + col * 4, 0, kCoherent));
+            sums[g] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(slots, at + kRefs + 64 + col * 4, 0, kCoherent));
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int i = 0; i < PER; ++i)
+                    part[g][b][i] = __builtin_amdgcn_raw_buffer_load_b128(slots, at + ((b * CH + PER * wave + i) * 64 + lane) * 16, 0, kCoherent);
+        }
+        float now = ref;
+#pragma unroll
+        for (int g = 0; g < BATCH; ++g) now = fmaxf(now, refs[g]);
+        const float keep = ref == -INFINITY ? 0.0f : exp2_fast(ref - now);
+        ref = now;
+        total *= keep;
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int i = 0; i < PER; ++i) out[b][i] *= keep;
+#pragma unroll
+        for (int g = 0; g < BATCH; ++g) {
+            const float f = sp + g < live && refs[g] > -INFINITY ? exp2_fast(refs[g] - now) : 0.0f;
+            total += sums[g] * f;
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int i = 0; i < PER; ++i) out[b][i] += __builtin_bit_cast(f32x4_t, part[g][b][i]) * f;
+        }
     }
     if (t.r0 + col > last) return;
-    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-    uint16_t* dst = a.out + (t.q0 + qi) * a.ldo + int64_t(hd) * D;
+    const float inv = total > 0.0f ? 1.0f / total : 0.0f;
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            uint32_t w[CH / 2];
-#pragma unroll
-            for (int i = 0; i < CH / 2; ++i)
-                w[i] = uint32_t(from_f32<ACT>(acc[b][2 * i][j] * inv)) | (uint32_t(from_f32<ACT>(acc[b][2 * i + 1][j] * inv)) << 16);
-            uint16_t* to = dst + W * b + CH * (4 * kq + j);
-            if constexpr (CH == 8) *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
-            else *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[1]);
+            uint16_t* to = dst + W * b + CH * (4 * kq + j) + PER * wave;
+            if constexpr (PER == 2)
+                *reinterpret_cast<uint32_t*>(to) = uint32_t(from_f32<ACT>(out[b][0][j] * inv)) | (uint32_t(from_f32<ACT>(out[b][1][j] * inv)) << 16);
+            else
+                *to = from_f32<ACT>(out[b][0][j] * inv);
         }
-}
-
-// Joins the splits of one tile and key head: wave j takes the accumulators'
-// component j, which hold whole runs of CH channels of the output.
-template <int ACT, int D>
-__global__ __launch_bounds__(256) void kv4_join_kernel(Kv4AttentionArgs a, int span, int splits, const float* partials) {
-    constexpr int W = kv4_width(D), NB = kv4_blocks(D), CH = W / 16;
-    const int lane = threadIdx.x % 64, j = threadIdx.x / 64;
-    const int col = lane % 16, kq = lane / 16;
-    const int kh = blockIdx.y, share = a.heads / a.kv_heads;
-    Tile t;
-    if (!find_tile<16>(a, blockIdx.x, t)) return;
-    const View view{a.causal, int(a.window)};
-    const int last = min(t.r0 + 15, t.rows - 1);
-    const int begin = view.lo(t.position(t.r0 / share)) / 32 * 32, end = view.hi(t.position(last / share), t.kv);
-    const int live = min(splits, max(0, (end - begin + span - 1) / span));
-    const float* o = partials + (int64_t(blockIdx.x) * a.kv_heads + kh) * splits * partial_floats<D>();
-    float ref = -INFINITY;
-    for (int s = 0; s < live; ++s) ref = fmaxf(ref, o[s * partial_floats<D>() + 16 * D + col]);
-    float sum = 0.0f, acc[NB][CH];
-#pragma unroll
-    for (int b = 0; b < NB; ++b)
-#pragma unroll
-        for (int i = 0; i < CH; ++i) acc[b][i] = 0.0f;
-    if (ref > -INFINITY) {
-#pragma unroll 4
-        for (int s = 0; s < live; ++s) {
-            const float* p = o + s * partial_floats<D>();
-            const float f = exp2_fast(p[16 * D + col] - ref);
-            sum += p[16 * D + 16 + col] * f;
-#pragma unroll
-            for (int b = 0; b < NB; ++b)
-#pragma unroll
-                for (int i = 0; i < CH; ++i) acc[b][i] += p[((b * CH + i) * 4 + j) * 64 + lane] * f;
-        }
-    }
-    if (t.r0 + col > last) return;
-    const int r = t.r0 + col;
-    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-    uint16_t* dst = a.out + (t.q0 + r / share) * a.ldo + int64_t(kh * share + r % share) * D;
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-        uint32_t w[CH / 2];
-#pragma unroll
-        for (int i = 0; i < CH / 2; ++i)
-            w[i] = uint32_t(from_f32<ACT>(acc[b][2 * i] * inv)) | (uint32_t(from_f32<ACT>(acc[b][2 * i + 1] * inv)) << 16);
-        uint16_t* to = dst + W * b + CH * (4 * kq + j);
-        if constexpr (CH == 8) *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
-        else *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[1]);
-    }
 }
 
 template <int ACT, int D>
 hipError_t run(const Kv4AttentionArgs& a, const Kv4Plan& p, hipStream_t stream) {
     const int per = a.page / 16;
     const uint32_t magic = per == 1 ? 0 : uint32_t(((uint64_t(1) << 32) + per - 1) / per);
+    unsigned* counters = static_cast<unsigned*>(a.workspace);
     float* partials = p.splits > 1 ? reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + kSyncBytes) : nullptr;
     const dim3 grid(unsigned(p.tiles), unsigned(a.kv_heads), unsigned(p.splits));
-    kv4_attention_kernel<ACT, D><<<grid, dim3(256), 0, stream>>>(a, int(p.span), p.splits, magic, partials);
-    if (p.splits > 1) {
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
-        kv4_join_kernel<ACT, D><<<dim3(unsigned(p.tiles), unsigned(a.kv_heads)), dim3(256), 0, stream>>>(a, int(p.span), p.splits, partials);
-    }
+    kv4_attention_kernel<ACT, D><<<grid, dim3(256), 0, stream>>>(a, int(p.span), p.splits, magic, counters, partials);
     return hipGetLastError();
 }
 
@@ -492,7 +556,8 @@ Kv4Plan plan_kv4_attention(int64_t tokens, int64_t batch, int heads, int kv_head
         most = most < reach ? most : reach;
     }
     const int64_t base = p.tiles * kv_heads;
-    const int64_t want = ceil_div(2048, base > 0 ? base : 1);
+    // about four workgroups a CU and twice over; a tile's splits share a counter of the workspace's header
+    const int64_t want = base < int64_t(kSyncBytes / 4) ? ceil_div(2048, base > 0 ? base : 1) : 1;
     int64_t span = ceil_div(ceil_div(most, want), 128) * 128;
     if (span < 256) span = 256;
     p.span = span;
