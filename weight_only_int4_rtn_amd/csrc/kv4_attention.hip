@@ -233,11 +233,11 @@ constexpr uint32_t kOnes = 0x3C003C00u;  // two f16 ones
 // four waves take steps of 32 tokens in turn, each with its own running
 // softmax, and meet in LDS at the end.  The next step's keys are loaded as soon
 // as this step's have been used, and the values likewise, so each side has one
-// set of registers and half a step or more of work to arrive behind, and four
-// waves fit a SIMD (two for D = 256).  Splits are joined by the last of a
+// set of registers and half a step or more of work to arrive behind, and three
+// waves fit a SIMD (four for D = 64, two for D = 256).  Splits are joined by the last of a
 // tile's workgroups to finish, in split order.
 template <int ACT, int D>
-__global__ __launch_bounds__(256, D == 256 ? 2 : 4) void kv4_attention_kernel(Kv4AttentionArgs a, int span, int splits,
+__global__ __launch_bounds__(256, D == 256 ? 2 : D == 128 ? 3 : 4) void kv4_attention_kernel(Kv4AttentionArgs a, int span, int splits,
                                                                               uint32_t magic, unsigned* counters,
                                                                               float* partials) {
     constexpr int W = kv4_width(D), NB = kv4_blocks(D), CH = W / 16;
@@ -521,12 +521,390 @@ __global__ __launch_bounds__(256, D == 256 ? 2 : 4) void kv4_attention_kernel(Kv
         }
 }
 
+// ---------------------------------------------------------------------------
+// Many rows of a request (prompts, prompt pieces, action chunks).
+//
+// One workgroup: 64 CG rows of one key head over one split of the tokens; each
+// of the four waves owns 16 CG rows and all waves walk the same tokens, so the
+// codes become f16 once a workgroup: in turn each wave turns a quarter of the
+// next step's codes into matrix operands in LDS (in operand order: reads and
+// writes of 16 bytes a lane, no conflicts) while the step before is computed,
+// one barrier a step.  Raw codes are loaded two steps ahead.
+// ---------------------------------------------------------------------------
+template <int D>
+struct Stage {
+    static constexpr int W = kv4_width(D), NB = kv4_blocks(D), CH = W / 16;
+    static constexpr int SUB = D == 64 ? 2 : 1;       // 32-token parts of a step
+    static constexpr int KF = 2 * NB * (W / 32), VF = NB * CH;  // operands of a part, 1 KB each
+    uint4 k[SUB][KF][64], v[SUB][VF][64];
+    float ks[SUB][NB][32], vs[SUB][NB][32];
+};
+
+// A wave's quarter of a step: D >= 128: keys of chunk 0, of chunk 1, the values'
+// words 0 and 1 of both chunks, words 2 and 3.  D = 64 (two parts a step): keys
+// of part 0, of part 1, values of part 0, of part 1.
+template <int D>
+struct Quarter {
+    using S = Stage<D>;
+    static constexpr int W = S::W, NB = S::NB;
+    uint32_t w[NB][4];
+    float scale;
+
+    __device__ static uint2 load8(const uint8_t* p) {
+        typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+        const u32x2 x = *reinterpret_cast<const u32x2*>(p);
+        return make_uint2(x.x, x.y);
+    }
+    // c0: the step's first chunk in ch
+    __device__ void load(const uint8_t* pool, const Chunks& ch, int c0, int page, int wave, int lane) {
+        const bool values = wave >= 2;
+        const int u = wave & 1;
+        const uint8_t* codes = pool + (values ? page * (D / 2) : 0);
+        const uint8_t* scales = pool + (values ? NB * page * 4 : 0);
+        const int ca = c0 + (D == 64 ? 2 * u : 0), cb = ca + 1;
+        const uint64_t at0 = ch.code_at(ca), at1 = ch.code_at(cb), sc0 = ch.scale_at(ca), sc1 = ch.scale_at(cb);
+        if (D != 64 && !values) {
+            const uint8_t* p = codes + (u ? at1 : at0) + uint32_t(lane * 16);
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                const uint4 x = *reinterpret_cast<const uint4*>(p + b * (8 * W));
+                w[b][0] = x.x; w[b][1] = x.y; w[b][2] = x.z; w[b][3] = x.w;
+            }
+        } else {
+            const uint32_t in = uint32_t(lane * (W / 8) + (D == 64 ? 0 : 8 * u));
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                const uint2 x = load8(codes + at0 + b * (8 * W) + in), y = load8(codes + at1 + b * (8 * W) + in);
+                w[b][0] = x.x; w[b][1] = x.y; w[b][2] = y.x; w[b][3] = y.y;
+            }
+        }
+        // scales: 16 lanes a chunk and block
+        const int g = lane / 16;
+        const bool both = D == 64 || values;  // of both chunks, else of chunk u
+        const int c = both ? g & 1 : u, b = both ? g >> 1 : g;
+        if (b < NB && !(D != 64 && values && u))
+            scale = *reinterpret_cast<const float*>(scales + (c ? sc1 : sc0) + (b * page + lane % 16) * 4);
+    }
+    __device__ void store(S& st, int wave, int lane) const {
+        const bool values = wave >= 2;
+        const int u = wave & 1, part = D == 64 ? u : 0;
+        if (!values) {
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    // D = 64: words (chunk i / 2, k-step i % 2); else chunk u, k-step i
+                    const int f = D == 64 ? i : (u * NB + b) * 4 + i;
+                    st.k[part][f][lane] = make_uint4(kv4_pair<0>(w[b][i]), kv4_pair<1>(w[b][i]), kv4_pair<2>(w[b][i]), kv4_pair<3>(w[b][i]));
+                }
+        } else {
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+                static_for<0, 4>([&](auto ic) {
+                    constexpr int i = ic;
+                    const int f = D == 64 ? i : b * S::CH + 4 * u + i;
+                    st.v[part][f][lane] = make_uint4(kv4_pair<i>(w[b][0]), kv4_pair<i>(w[b][1]), kv4_pair<i>(w[b][2]), kv4_pair<i>(w[b][3]));
+                });
+        }
+        const int g = lane / 16;
+        const bool both = D == 64 || values;
+        const int c = both ? g & 1 : u, b = both ? g >> 1 : g;
+        if (b < NB && !(D != 64 && values && u)) (values ? st.vs : st.ks)[part][b][16 * c + lane % 16] = scale;
+    }
+};
+
+template <int ACT, int D, int CG>
+__global__ __launch_bounds__(256, 2) void kv4_rows_kernel(Kv4AttentionArgs a, int64_t tiles, int span, int splits, uint32_t magic,
+                                                          unsigned* counters, float* partials) {
+    using S = Stage<D>;
+    constexpr int W = S::W, NB = S::NB, CH = S::CH, SUB = S::SUB, ROWS = 64 * CG, STEP = 32 * SUB;
+    extern __shared__ uint4 lds_raw[];
+    S* const stage = reinterpret_cast<S*>(lds_raw);
+    __shared__ int last_one;
+    const int lane = threadIdx.x % 64, wave = uniform(threadIdx.x / 64);
+    const int col = lane % 16, kq = lane / 16;
+    // consecutive workgroups take the key heads of one tile (each XCD then keeps to few heads), the
+    // tiles from the last: under a causal mask those see most
+    const int kh = int(blockIdx.x % unsigned(a.kv_heads)), share = a.heads / a.kv_heads;
+    const int64_t x = tiles - 1 - int64_t(blockIdx.x / unsigned(a.kv_heads));
+
+    Tile t;
+    if (!find_tile<ROWS>(a, x, t)) return;
+    const View view{a.causal, int(a.window)};
+    const int last = min(t.r0 + ROWS - 1, t.rows - 1);
+    const int begin = view.lo(t.position(t.r0 / share)) / STEP * STEP, end = view.hi(t.position(last / share), t.kv);
+    const int live = max(1, min(splits, (end - begin + span - 1) / span));
+    if (int(blockIdx.y) >= live) return;
+    const int s0 = begin + int(blockIdx.y) * span, s1 = min(end, s0 + span);
+    const int steps = max(0, (s1 - s0 + STEP - 1) / STEP);
+
+    // this wave's rows
+    const int w0 = min(t.r0 + 16 * CG * wave, last), w1 = min(w0 + 16 * CG - 1, last);
+    const bool idle = t.r0 + 16 * CG * wave > last;
+    const int all_lo = view.lo(t.position(w1 / share)), all_hi = min(view.hi(t.position(w0 / share), t.kv), s1);
+    const int any_lo = view.lo(t.position(w0 / share)), any_hi = idle ? 0 : min(view.hi(t.position(w1 / share), t.kv), s1);
+
+    const int64_t region = kv4_region(a.page, D);
+    const uint8_t* pool = a.pool + kh * region;
+    const int32_t* table = a.table + int64_t(t.b) * a.ldt;
+    constexpr int PER = 64 / (2 * SUB);  // steps whose chunks the lanes hold
+    Chunks ch;
+    Quarter<D> raw;
+    uint32_t there[3] = {0, 0, 0};  // chunks on pages of the pool, of this step, the next and the one after
+    int loaded = 0;
+    auto load = [&]() {
+        const int at = loaded % PER;
+        if (at == 0) ch.find(a, magic, table, region, NB * 8 * W, s0 / 16 + loaded * 2 * SUB, 2, s1, lane);
+        raw.load(pool, ch, at * 2 * SUB, a.page, wave, lane);
+        const uint32_t on = uint32_t(ch.there >> (at * 2 * SUB)) & ((1u << (2 * SUB)) - 1);
+        ++loaded;
+        return on;
+    };
+    if (steps > 0) there[1] = load();
+
+    uint4 q[CG][NB][W / 32];
+    float offset[CG][NB], zf[CG];
+    int lo[CG], hi[CG];
+#pragma unroll
+    for (int g = 0; g < CG; ++g) {
+        const int r = min(t.r0 + 16 * (CG * wave + g) + col, last);
+        const int qi = r / share, hd = kh * share + r % share;
+        lo[g] = view.lo(t.position(qi));
+        hi[g] = min(view.hi(t.position(qi), t.kv), s1);
+        zf[g] = load_queries<ACT, D>(a.q + (t.q0 + qi) * a.ldq + int64_t(hd) * D + 8 * kq, a.scale, q[g], offset[g]);
+    }
+    f32x4_t acc[CG][NB][CH], ps[CG][NB];
+#pragma unroll
+    for (int g = 0; g < CG; ++g)
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            ps[g][b] = f32x4_t{0, 0, 0, 0};
+#pragma unroll
+            for (int i = 0; i < CH; ++i) acc[g][b][i] = f32x4_t{0, 0, 0, 0};
+        }
+    Running run[CG];
+
+    if (steps > 0) raw.store(stage[0], wave, lane);
+    if (steps > 1) there[2] = load();
+    for (int step = 0; step < steps; ++step) {
+        lds_barrier();  // this step's operands are there, and nobody reads the other buffer any more
+        there[0] = there[1];
+        there[1] = there[2];
+        if (step + 1 < steps) raw.store(stage[(step + 1) & 1], wave, lane);
+        if (step + 2 < steps) there[2] = load();
+        const S& st = stage[step & 1];
+#pragma unroll
+        for (int sub = 0; sub < SUB; ++sub) {
+            const int tok = s0 + step * STEP + 32 * sub;
+            if (tok + 32 <= any_lo || tok >= any_hi) continue;
+            const uint32_t on = there[0] >> (2 * sub) & 3;
+            float z[CG][2][4];
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+                    f32x4_t s[CG];
+#pragma unroll
+                    for (int g = 0; g < CG; ++g) s[g] = f32x4_t{offset[g][b], offset[g][b], offset[g][b], offset[g][b]};
+#pragma unroll
+                    for (int ks = 0; ks < W / 32; ++ks) {
+                        const uint4 kf = st.k[sub][(c * NB + b) * (W / 32) + ks][lane];
+#pragma unroll
+                        for (int g = 0; g < CG; ++g) s[g] = mfma(kf, q[g][b][ks], s[g]);
+                    }
+                    const float4 f = *reinterpret_cast<const float4*>(&st.ks[sub][b][16 * c + 4 * kq]);
+#pragma unroll
+                    for (int g = 0; g < CG; ++g) {
+                        const float y[4] = {s[g][0] * f.x, s[g][1] * f.y, s[g][2] * f.z, s[g][3] * f.w};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) z[g][c][i] = b == 0 ? y[i] : z[g][c][i] + y[i];
+                    }
+                }
+            float vs[2][NB][4];
+            float vm = 0.0f;
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+                    const float4 f = *reinterpret_cast<const float4*>(&st.vs[sub][b][16 * c + 4 * kq]);
+                    vs[c][b][0] = f.x; vs[c][b][1] = f.y; vs[c][b][2] = f.z; vs[c][b][3] = f.w;
+                }
+            if (!(tok >= all_lo && tok + 32 <= all_hi && on == 3)) {
+                // value scales of tokens that no row of the split may see are not numbers one can multiply by 0
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int at = tok + 16 * c + 4 * kq + i;
+                        const bool there_ = (on >> c & 1) && at >= any_lo && at < any_hi;
+#pragma unroll
+                        for (int b = 0; b < NB; ++b) vs[c][b][i] = there_ ? vs[c][b][i] : 0.0f;
+#pragma unroll
+                        for (int g = 0; g < CG; ++g) z[g][c][i] = there_ && at >= lo[g] && at < hi[g] ? z[g][c][i] : -INFINITY;
+                    }
+            }
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) vm = fmaxf(vm, vs[c][b][i]);
+            uint4 pw[CG][NB];
+#pragma unroll
+            for (int g = 0; g < CG; ++g) {
+                float zm = z[g][0][0];
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) zm = fmaxf(zm, z[g][c][i]);
+                if (__any(zm > run[g].top || vm > run[g].vlim)) {
+                    const float f = run[g].raise(row_max(zm), row_max(vm), zf[g]);
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) {
+                        ps[g][b] *= f;
+#pragma unroll
+                        for (int i = 0; i < CH; ++i) acc[g][b][i] *= f;
+                    }
+                }
+                const float base = run[g].ref == -INFINITY ? 0.0f : run[g].ref;
+                float p[2][4];
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        p[c][i] = exp2_fast(fmaf(z[g][c][i], zf[g], -base));
+                        run[g].sum += p[c][i];
+                    }
+#pragma unroll
+                for (int b = 0; b < NB; ++b) pw[g][b] = weights<D>(p, vs, b);
+            }
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+#pragma unroll
+                for (int g = 0; g < CG; ++g) ps[g][b] = mfma(make_uint4(kOnes, kOnes, kOnes, kOnes), pw[g][b], ps[g][b]);
+#pragma unroll
+                for (int i = 0; i < CH; ++i) {
+                    const uint4 vf = st.v[sub][b * CH + i][lane];
+#pragma unroll
+                    for (int g = 0; g < CG; ++g) acc[g][b][i] = mfma(vf, pw[g][b], acc[g][b][i]);
+                }
+            }
+        }
+    }
+
+    const int64_t tile = x * a.kv_heads + kh;
+    typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+    constexpr int kGroupBytes = int(partial_floats<D>() * 4), kSlot = kGroupBytes * (ROWS / 16), kRefs = 16 * D * 4;
+    const __amdgpu_buffer_rsrc_t slots =
+        buffer_rsrc(live > 1 ? partials + tile * splits * (kSlot / 4) : partials, live > 1 ? int64_t(splits) * kSlot : 0);
+#pragma unroll
+    for (int g = 0; g < CG; ++g) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int i = 0; i < CH; ++i) acc[g][b][i] -= kKvOffset * ps[g][b];
+        run[g].sum = row_sum(run[g].sum);
+    }
+    if (live > 1) {
+        // as in the kernel above: the last split to finish joins them all
+#pragma unroll
+        for (int g = 0; g < CG; ++g) {
+            const int at = int(blockIdx.y) * kSlot + (CG * wave + g) * kGroupBytes;
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int i = 0; i < CH; ++i)
+                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc[g][b][i]), slots,
+                                                           at + ((b * CH + i) * 64 + lane) * 16, 0, kCoherent);
+            if (kq == 0) {
+                __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(run[g].ref), slots, at + kRefs + col * 4, 0, kCoherent);
+                __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(run[g].sum), slots, at + kRefs + 64 + col * 4, 0, kCoherent);
+            }
+        }
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            const unsigned before = __hip_atomic_fetch_add(counters + tile, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            last_one = before == unsigned(live - 1);
+            if (last_one) __hip_atomic_store(counters + tile, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+        __syncthreads();
+        if (!last_one) return;
+#pragma unroll
+        for (int g = 0; g < CG; ++g) {
+            float ref = -INFINITY, sum = 0.0f;
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int i = 0; i < CH; ++i) acc[g][b][i] = f32x4_t{0, 0, 0, 0};
+            for (int sp = 0; sp < live; ++sp) {
+                const int at = sp * kSlot + (CG * wave + g) * kGroupBytes;
+                const float other = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(slots, at + kRefs + col * 4, 0, kCoherent));
+                const float more = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(slots, at + kRefs + 64 + col * 4, 0, kCoherent));
+                f32x4_t part[NB][CH];
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+#pragma unroll
+                    for (int i = 0; i < CH; ++i)
+                        part[b][i] = __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
+                                                                     slots, at + ((b * CH + i) * 64 + lane) * 16, 0, kCoherent));
+                const float now = fmaxf(ref, other);
+                const float f0 = ref == -INFINITY ? 0.0f : exp2_fast(ref - now);
+                const float f1 = other == -INFINITY ? 0.0f : exp2_fast(other - now);
+                ref = now;
+                sum = sum * f0 + more * f1;
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+#pragma unroll
+                    for (int i = 0; i < CH; ++i) acc[g][b][i] = acc[g][b][i] * f0 + part[b][i] * f1;
+            }
+            run[g].sum = sum;
+        }
+    }
+#pragma unroll
+    for (int g = 0; g < CG; ++g) {
+        const int r = t.r0 + 16 * (CG * wave + g) + col;
+        if (r > last) continue;
+        const float inv = run[g].sum > 0.0f ? 1.0f / run[g].sum : 0.0f;
+        uint16_t* dst = a.out + (t.q0 + r / share) * a.ldo + int64_t(kh * share + r % share) * D;
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint32_t w[CH / 2];
+#pragma unroll
+                for (int i = 0; i < CH / 2; ++i)
+                    w[i] = uint32_t(from_f32<ACT>(acc[g][b][2 * i][j] * inv)) | (uint32_t(from_f32<ACT>(acc[g][b][2 * i + 1][j] * inv)) << 16);
+                uint16_t* to = dst + W * b + CH * (4 * kq + j);
+                if constexpr (CH == 8) *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
+                else *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[1]);
+            }
+    }
+}
+
+// 16-row groups of a wave: two share each operand read, as far as the registers of two waves a SIMD go
+constexpr int row_groups(int d) { return d == 256 ? 1 : 2; }
+
+// Dynamic LDS beyond 64 KB has to be allowed for a kernel first.
+hipError_t allow_lds(const void* kernel, size_t bytes) {
+    return bytes <= 65536 ? hipSuccess : hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
+}
+
 template <int ACT, int D>
 hipError_t run(const Kv4AttentionArgs& a, const Kv4Plan& p, hipStream_t stream) {
     const int per = a.page / 16;
     const uint32_t magic = per == 1 ? 0 : uint32_t(((uint64_t(1) << 32) + per - 1) / per);
     unsigned* counters = static_cast<unsigned*>(a.workspace);
     float* partials = p.splits > 1 ? reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + kSyncBytes) : nullptr;
+    if (p.rows > 16) {
+        constexpr int CG = row_groups(D);
+        const dim3 grid(unsigned(p.tiles * a.kv_heads), unsigned(p.splits));
+        const size_t lds = 2 * sizeof(Stage<D>);
+        const hipError_t e = allow_lds(reinterpret_cast<const void*>(&kv4_rows_kernel<ACT, D, CG>), lds);
+        if (e != hipSuccess) return e;
+        kv4_rows_kernel<ACT, D, CG><<<grid, dim3(256), lds, stream>>>(a, p.tiles, int(p.span), p.splits, magic, counters, partials);
+        return hipGetLastError();
+    }
     const dim3 grid(unsigned(p.tiles), unsigned(a.kv_heads), unsigned(p.splits));
     kv4_attention_kernel<ACT, D><<<grid, dim3(256), 0, stream>>>(a, int(p.span), p.splits, magic, counters, partials);
     return hipGetLastError();
@@ -548,22 +926,27 @@ Kv4Plan plan_kv4_attention(int64_t tokens, int64_t batch, int heads, int kv_head
     Kv4Plan p{};
     const int64_t share = heads / kv_heads;
     p.rows = 16;
+    if (ragged && tokens * share > 32 * batch) p.rows = 64 * row_groups(dim);
     p.tiles = ragged ? tokens * share / p.rows + batch : batch * ceil_div(share, p.rows);
     // the tokens a tile can see: its window, the queries of its rows, an aligned begin
     int64_t most = capacity;
     if (window > 0) {
-        const int64_t reach = (causal ? window : 2 * window) + (ragged ? p.rows : 1) + 32;
+        const int64_t reach = (causal ? window : 2 * window) + (ragged ? p.rows : 1) + 64;
         most = most < reach ? most : reach;
     }
+    // Splits: with few tiles as many as fill the chip once (768 workgroups of D
+    // = 128; 4 x 131072 tokens: 111 us, twice as many 119, four times 131), else
+    // twice over, as lengths may differ (64 x 0..8192 tokens: 92 us, once 100,
+    // four times 94).  A tile's splits share a counter of the workspace's header.
     const int64_t base = p.tiles * kv_heads;
-    // about four workgroups a CU and twice over; a tile's splits share a counter of the workspace's header
-    const int64_t want = base < int64_t(kSyncBytes / 4) ? ceil_div(2048, base > 0 ? base : 1) : 1;
+    const int64_t room = 256 * (p.rows > 16 ? 2 : dim == 256 ? 2 : dim == 128 ? 3 : 4);
+    const int64_t want = base >= int64_t(kSyncBytes / 4) ? 1 : 4 * base <= room ? room / (base > 0 ? base : 1) : ceil_div(2 * room, base);
     int64_t span = ceil_div(ceil_div(most, want), 128) * 128;
     if (span < 256) span = 256;
     p.span = span;
     p.splits = int(ceil_div(most, span));
     if (p.splits < 1) p.splits = 1;
-    if (p.splits > 1) p.workspace = size_t(base) * size_t(p.splits) * size_t(16 * dim + 32) * 4;
+    if (p.splits > 1) p.workspace = size_t(base) * size_t(p.splits) * size_t(p.rows / 16) * size_t(16 * dim + 32) * 4;
     return p;
 }
 
