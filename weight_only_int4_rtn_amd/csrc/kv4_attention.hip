@@ -199,20 +199,27 @@ __device__ inline float load_queries(const uint16_t* src, float scale, uint4 (&q
     return fmaxf(ldexpf(fabsf(scale) * kLog2e, -e), 1e-37f);
 }
 
-// A row's running softmax over some of its tokens.
+// A row's running softmax over some of its tokens.  Its reference follows the
+// largest logit and value scale only when they have outgrown it by 2^10 and
+// 2^3: weights up to 2^13 are as exact in f16 as those below 1, and the sums so
+// far are multiplied by a power of the reference's change a few times a row
+// instead of at every new maximum (prompt of 4096 tokens: 237 -> 209 us).
 struct Running {
-    float top = -INFINITY;  // largest logit (before the factor)
-    float vlim = 0.0f;      // power of two above the value scales so far
-    float ref = -INFINITY;  // what the probabilities are relative to: top's exponent + log2(vlim)
-    float sum = 0.0f;       // this lane's part of the row's sum
-    // new references for logits up to z and value scales up to v (this row's largest); returns what
+    static constexpr float kSlack = 10.0f, kScaleSlack = 8.0f;
+    float limit = -INFINITY;  // logit (before the factor) that needs a new reference
+    float vlimit = 0.0f;      // value scale that needs one
+    float ref = -INFINITY;    // what the probabilities are relative to: a largest logit's exponent + log2 of a scale's
+    float sum = 0.0f;         // this lane's part of the row's sum
+    // a new reference from logits up to z and value scales up to v (this row's largest); returns what
     // the sums so far are to be multiplied by
     __device__ float raise(float z, float v, float zf) {
-        top = fmaxf(top, z);
-        // never below 2^-60, so that the probabilities' sum stays in range
+        const float top = fmaxf(limit - kSlack / zf, z);
+        // scales count from 2^-60 up, so that the probabilities' sum stays in range
         const int e = max(int(__float_as_uint(v) >> 23) - 126, -60);
-        vlim = fmaxf(vlim, ldexpf(1.0f, e));
-        const float now = top == -INFINITY ? -INFINITY : top * zf + __builtin_amdgcn_logf(vlim);
+        const float scale = fmaxf(vlimit * (1.0f / kScaleSlack), ldexpf(1.0f, e));
+        limit = top + kSlack / zf;
+        vlimit = scale * kScaleSlack;
+        const float now = top == -INFINITY ? -INFINITY : top * zf + __builtin_amdgcn_logf(scale);
         const float f = ref == -INFINITY ? 0.0f : exp2_fast(ref - now);
         ref = now;
         sum *= f;
@@ -344,7 +351,7 @@ __global__ __launch_bounds__(256, D == 256 ? 2 : D == 128 ? 3 : 4) void kv4_atte
 #pragma unroll
                 for (int b = 0; b < NB; ++b) vm = fmaxf(vm, vs[c][b][i]);
             }
-        if (__any(zm > run.top || vm > run.vlim)) {
+        if (__any(zm > run.limit || vm > run.vlimit)) {
             const float f = run.raise(row_max(zm), row_max(vm), zf);
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
@@ -757,7 +764,7 @@ __global__ __launch_bounds__(256, 2) void kv4_rows_kernel(Kv4AttentionArgs a, in
                 for (int c = 0; c < 2; ++c)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) zm = fmaxf(zm, z[g][c][i]);
-                if (__any(zm > run[g].top || vm > run[g].vlim)) {
+                if (__any(zm > run[g].limit || vm > run[g].vlimit)) {
                     const float f = run[g].raise(row_max(zm), row_max(vm), zf[g]);
 #pragma unroll
                     for (int b = 0; b < NB; ++b) {
