@@ -531,12 +531,17 @@ __global__ __launch_bounds__(256, D == 256 ? 2 : D == 128 ? 3 : 4) void kv4_atte
 // ---------------------------------------------------------------------------
 // Many rows of a request (prompts, prompt pieces, action chunks).
 //
-// One workgroup: 64 CG rows of one key head over one split of the tokens; each
-// of the four waves owns 16 CG rows and all waves walk the same tokens, so the
-// codes become f16 once a workgroup: in turn each wave turns a quarter of the
-// next step's codes into matrix operands in LDS (in operand order: reads and
-// writes of 16 bytes a lane, no conflicts) while the step before is computed,
-// one barrier a step.  Raw codes are loaded two steps ahead.
+// One workgroup: 64 rows of one key head over one split of the tokens.  Each of
+// the four waves owns 16 rows and all walk the same tokens, so the codes become
+// f16 once a workgroup: each wave turns a quarter of the next step's codes into
+// matrix operands in LDS (in operand order: reads and writes of 16 bytes a lane,
+// no conflicts) while this step is computed, one barrier a step, raw codes
+// loaded a step before that.  32 rows a wave halve the operand reads but leave
+// registers for two waves a SIMD instead of four, which costs more (16 x 64
+// queries on 1000 tokens, D = 128: 54 us against 44; prompt of 4096: 205 against
+// 193).  What bounds it is the issue of instructions: of 200 us, with 29 % of
+// the cycles in matrix and 57 % in vector instructions, copies that leave
+// out the staging, the exponentials or the products each save what those cost.
 // ---------------------------------------------------------------------------
 template <int D>
 struct Stage {
@@ -620,11 +625,11 @@ struct Quarter {
     }
 };
 
-template <int ACT, int D, int CG>
-__global__ __launch_bounds__(256, 2) void kv4_rows_kernel(Kv4AttentionArgs a, int64_t tiles, int span, int splits, uint32_t magic,
-                                                          unsigned* counters, float* partials) {
+template <int ACT, int D>
+__global__ __launch_bounds__(256, D == 256 ? 2 : 4) void kv4_rows_kernel(Kv4AttentionArgs a, int64_t tiles, int span, int splits,
+                                                                        uint32_t magic, unsigned* counters, float* partials) {
     using S = Stage<D>;
-    constexpr int W = S::W, NB = S::NB, CH = S::CH, SUB = S::SUB, ROWS = 64 * CG, STEP = 32 * SUB;
+    constexpr int W = S::W, NB = S::NB, CH = S::CH, SUB = S::SUB, ROWS = 64, STEP = 32 * SUB;
     extern __shared__ uint4 lds_raw[];
     S* const stage = reinterpret_cast<S*>(lds_raw);
     __shared__ int last_one;
@@ -646,8 +651,8 @@ __global__ __launch_bounds__(256, 2) void kv4_rows_kernel(Kv4AttentionArgs a, in
     const int steps = max(0, (s1 - s0 + STEP - 1) / STEP);
 
     // this wave's rows
-    const int w0 = min(t.r0 + 16 * CG * wave, last), w1 = min(w0 + 16 * CG - 1, last);
-    const bool idle = t.r0 + 16 * CG * wave > last;
+    const int w0 = min(t.r0 + 16 * wave, last), w1 = min(w0 + 15, last);
+    const bool idle = t.r0 + 16 * wave > last;
     const int all_lo = view.lo(t.position(w1 / share)), all_hi = min(view.hi(t.position(w0 / share), t.kv), s1);
     const int any_lo = view.lo(t.position(w0 / share)), any_hi = idle ? 0 : min(view.hi(t.position(w1 / share), t.kv), s1);
 
@@ -669,27 +674,20 @@ __global__ __launch_bounds__(256, 2) void kv4_rows_kernel(Kv4AttentionArgs a, in
     };
     if (steps > 0) there[1] = load();
 
-    uint4 q[CG][NB][W / 32];
-    float offset[CG][NB], zf[CG];
-    int lo[CG], hi[CG];
+    const int r = min(t.r0 + 16 * wave + col, last);
+    const int qi = r / share, hd = kh * share + r % share;
+    const int lo = view.lo(t.position(qi)), hi = min(view.hi(t.position(qi), t.kv), s1);
+    uint4 q[NB][W / 32];
+    float offset[NB];
+    const float zf = load_queries<ACT, D>(a.q + (t.q0 + qi) * a.ldq + int64_t(hd) * D + 8 * kq, a.scale, q, offset);
+    f32x4_t acc[NB][CH], ps[NB];
 #pragma unroll
-    for (int g = 0; g < CG; ++g) {
-        const int r = min(t.r0 + 16 * (CG * wave + g) + col, last);
-        const int qi = r / share, hd = kh * share + r % share;
-        lo[g] = view.lo(t.position(qi));
-        hi[g] = min(view.hi(t.position(qi), t.kv), s1);
-        zf[g] = load_queries<ACT, D>(a.q + (t.q0 + qi) * a.ldq + int64_t(hd) * D + 8 * kq, a.scale, q[g], offset[g]);
+    for (int b = 0; b < NB; ++b) {
+        ps[b] = f32x4_t{0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < CH; ++i) acc[b][i] = f32x4_t{0, 0, 0, 0};
     }
-    f32x4_t acc[CG][NB][CH], ps[CG][NB];
-#pragma unroll
-    for (int g = 0; g < CG; ++g)
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-            ps[g][b] = f32x4_t{0, 0, 0, 0};
-#pragma unroll
-            for (int i = 0; i < CH; ++i) acc[g][b][i] = f32x4_t{0, 0, 0, 0};
-        }
-    Running run[CG];
+    Running run;
 
     if (steps > 0) raw.store(stage[0], wave, lane);
     if (steps > 1) there[2] = load();
@@ -705,30 +703,20 @@ __global__ __launch_bounds__(256, 2) void kv4_rows_kernel(Kv4AttentionArgs a, in
             const int tok = s0 + step * STEP + 32 * sub;
             if (tok + 32 <= any_lo || tok >= any_hi) continue;
             const uint32_t on = there[0] >> (2 * sub) & 3;
-            float z[CG][2][4];
+            float z[2][4];
 #pragma unroll
             for (int c = 0; c < 2; ++c)
 #pragma unroll
                 for (int b = 0; b < NB; ++b) {
-                    f32x4_t s[CG];
+                    f32x4_t s = {offset[b], offset[b], offset[b], offset[b]};
 #pragma unroll
-                    for (int g = 0; g < CG; ++g) s[g] = f32x4_t{offset[g][b], offset[g][b], offset[g][b], offset[g][b]};
-#pragma unroll
-                    for (int ks = 0; ks < W / 32; ++ks) {
-                        const uint4 kf = st.k[sub][(c * NB + b) * (W / 32) + ks][lane];
-#pragma unroll
-                        for (int g = 0; g < CG; ++g) s[g] = mfma(kf, q[g][b][ks], s[g]);
-                    }
+                    for (int ks = 0; ks < W / 32; ++ks) s = mfma(st.k[sub][(c * NB + b) * (W / 32) + ks][lane], q[b][ks], s);
                     const float4 f = *reinterpret_cast<const float4*>(&st.ks[sub][b][16 * c + 4 * kq]);
+                    const float y[4] = {s[0] * f.x, s[1] * f.y, s[2] * f.z, s[3] * f.w};
 #pragma unroll
-                    for (int g = 0; g < CG; ++g) {
-                        const float y[4] = {s[g][0] * f.x, s[g][1] * f.y, s[g][2] * f.z, s[g][3] * f.w};
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) z[g][c][i] = b == 0 ? y[i] : z[g][c][i] + y[i];
-                    }
+                    for (int i = 0; i < 4; ++i) z[c][i] = b == 0 ? y[i] : z[c][i] + y[i];
                 }
             float vs[2][NB][4];
-            float vm = 0.0f;
 #pragma unroll
             for (int c = 0; c < 2; ++c)
 #pragma unroll
@@ -737,64 +725,51 @@ __global__ __launch_bounds__(256, 2) void kv4_rows_kernel(Kv4AttentionArgs a, in
                     vs[c][b][0] = f.x; vs[c][b][1] = f.y; vs[c][b][2] = f.z; vs[c][b][3] = f.w;
                 }
             if (!(tok >= all_lo && tok + 32 <= all_hi && on == 3)) {
-                // value scales of tokens that no row of the split may see are not numbers one can multiply by 0
+                // a value scale that was never written is not a number one can multiply by 0
 #pragma unroll
                 for (int c = 0; c < 2; ++c)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int at = tok + 16 * c + 4 * kq + i;
-                        const bool there_ = (on >> c & 1) && at >= any_lo && at < any_hi;
+                        const bool seen = (on >> c & 1) && at >= lo && at < hi;
+                        z[c][i] = seen ? z[c][i] : -INFINITY;
 #pragma unroll
-                        for (int b = 0; b < NB; ++b) vs[c][b][i] = there_ ? vs[c][b][i] : 0.0f;
-#pragma unroll
-                        for (int g = 0; g < CG; ++g) z[g][c][i] = there_ && at >= lo[g] && at < hi[g] ? z[g][c][i] : -INFINITY;
+                        for (int b = 0; b < NB; ++b) vs[c][b][i] = seen ? vs[c][b][i] : 0.0f;
                     }
             }
+            float zm = z[0][0], vm = 0.0f;
 #pragma unroll
             for (int c = 0; c < 2; ++c)
 #pragma unroll
-                for (int b = 0; b < NB; ++b)
+                for (int i = 0; i < 4; ++i) {
+                    zm = fmaxf(zm, z[c][i]);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) vm = fmaxf(vm, vs[c][b][i]);
-            uint4 pw[CG][NB];
-#pragma unroll
-            for (int g = 0; g < CG; ++g) {
-                float zm = z[g][0][0];
-#pragma unroll
-                for (int c = 0; c < 2; ++c)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) zm = fmaxf(zm, z[g][c][i]);
-                if (__any(zm > run[g].limit || vm > run[g].vlimit)) {
-                    const float f = run[g].raise(row_max(zm), row_max(vm), zf[g]);
-#pragma unroll
-                    for (int b = 0; b < NB; ++b) {
-                        ps[g][b] *= f;
-#pragma unroll
-                        for (int i = 0; i < CH; ++i) acc[g][b][i] *= f;
-                    }
+                    for (int b = 0; b < NB; ++b) vm = fmaxf(vm, vs[c][b][i]);
                 }
-                const float base = run[g].ref == -INFINITY ? 0.0f : run[g].ref;
-                float p[2][4];
+            if (__any(zm > run.limit || vm > run.vlimit)) {
+                const float f = run.raise(row_max(zm), row_max(vm), zf);
 #pragma unroll
-                for (int c = 0; c < 2; ++c)
+                for (int b = 0; b < NB; ++b) {
+                    ps[b] *= f;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        p[c][i] = exp2_fast(fmaf(z[g][c][i], zf[g], -base));
-                        run[g].sum += p[c][i];
-                    }
-#pragma unroll
-                for (int b = 0; b < NB; ++b) pw[g][b] = weights<D>(p, vs, b);
+                    for (int i = 0; i < CH; ++i) acc[b][i] *= f;
+                }
             }
+            const float base = run.ref == -INFINITY ? 0.0f : run.ref;
+            float p[2][4];
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    p[c][i] = exp2_fast(fmaf(z[c][i], zf, -base));
+                    run.sum += p[c][i];
+                }
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
+                const uint4 pw = weights<D>(p, vs, b);
+                ps[b] = mfma(make_uint4(kOnes, kOnes, kOnes, kOnes), pw, ps[b]);
 #pragma unroll
-                for (int g = 0; g < CG; ++g) ps[g][b] = mfma(make_uint4(kOnes, kOnes, kOnes, kOnes), pw[g][b], ps[g][b]);
-#pragma unroll
-                for (int i = 0; i < CH; ++i) {
-                    const uint4 vf = st.v[sub][b * CH + i][lane];
-#pragma unroll
-                    for (int g = 0; g < CG; ++g) acc[g][b][i] = mfma(vf, pw[g][b], acc[g][b][i]);
-                }
+                for (int i = 0; i < CH; ++i) acc[b][i] = mfma(st.v[sub][b * CH + i][lane], pw, acc[b][i]);
             }
         }
     }
@@ -805,28 +780,22 @@ __global__ __launch_bounds__(256, 2) void kv4_rows_kernel(Kv4AttentionArgs a, in
     const __amdgpu_buffer_rsrc_t slots =
         buffer_rsrc(live > 1 ? partials + tile * splits * (kSlot / 4) : partials, live > 1 ? int64_t(splits) * kSlot : 0);
 #pragma unroll
-    for (int g = 0; g < CG; ++g) {
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int i = 0; i < CH; ++i) acc[b][i] -= kKvOffset * ps[b];
+    float sum = row_sum(run.sum);
+    if (live > 1) {
+        // as in the kernel above: the last split to finish joins them all
+        const int mine = int(blockIdx.y) * kSlot + wave * kGroupBytes;
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
-            for (int i = 0; i < CH; ++i) acc[g][b][i] -= kKvOffset * ps[g][b];
-        run[g].sum = row_sum(run[g].sum);
-    }
-    if (live > 1) {
-        // as in the kernel above: the last split to finish joins them all
-#pragma unroll
-        for (int g = 0; g < CG; ++g) {
-            const int at = int(blockIdx.y) * kSlot + (CG * wave + g) * kGroupBytes;
-#pragma unroll
-            for (int b = 0; b < NB; ++b)
-#pragma unroll
-                for (int i = 0; i < CH; ++i)
-                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc[g][b][i]), slots,
-                                                           at + ((b * CH + i) * 64 + lane) * 16, 0, kCoherent);
-            if (kq == 0) {
-                __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(run[g].ref), slots, at + kRefs + col * 4, 0, kCoherent);
-                __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(run[g].sum), slots, at + kRefs + 64 + col * 4, 0, kCoherent);
-            }
+            for (int i = 0; i < CH; ++i)
+                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc[b][i]), slots,
+                                                       mine + ((b * CH + i) * 64 + lane) * 16, 0, kCoherent);
+        if (kq == 0) {
+            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(run.ref), slots, mine + kRefs + col * 4, 0, kCoherent);
+            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(sum), slots, mine + kRefs + 64 + col * 4, 0, kCoherent);
         }
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         __syncthreads();
@@ -837,60 +806,50 @@ __global__ __launch_bounds__(256, 2) void kv4_rows_kernel(Kv4AttentionArgs a, in
         }
         __syncthreads();
         if (!last_one) return;
-#pragma unroll
-        for (int g = 0; g < CG; ++g) {
-            float ref = -INFINITY, sum = 0.0f;
-#pragma unroll
-            for (int b = 0; b < NB; ++b)
-#pragma unroll
-                for (int i = 0; i < CH; ++i) acc[g][b][i] = f32x4_t{0, 0, 0, 0};
-            for (int sp = 0; sp < live; ++sp) {
-                const int at = sp * kSlot + (CG * wave + g) * kGroupBytes;
-                const float other = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(slots, at + kRefs + col * 4, 0, kCoherent));
-                const float more = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(slots, at + kRefs + 64 + col * 4, 0, kCoherent));
-                f32x4_t part[NB][CH];
-#pragma unroll
-                for (int b = 0; b < NB; ++b)
-#pragma unroll
-                    for (int i = 0; i < CH; ++i)
-                        part[b][i] = __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
-                                                                     slots, at + ((b * CH + i) * 64 + lane) * 16, 0, kCoherent));
-                const float now = fmaxf(ref, other);
-                const float f0 = ref == -INFINITY ? 0.0f : exp2_fast(ref - now);
-                const float f1 = other == -INFINITY ? 0.0f : exp2_fast(other - now);
-                ref = now;
-                sum = sum * f0 + more * f1;
-#pragma unroll
-                for (int b = 0; b < NB; ++b)
-#pragma unroll
-                    for (int i = 0; i < CH; ++i) acc[g][b][i] = acc[g][b][i] * f0 + part[b][i] * f1;
-            }
-            run[g].sum = sum;
-        }
-    }
-#pragma unroll
-    for (int g = 0; g < CG; ++g) {
-        const int r = t.r0 + 16 * (CG * wave + g) + col;
-        if (r > last) continue;
-        const float inv = run[g].sum > 0.0f ? 1.0f / run[g].sum : 0.0f;
-        uint16_t* dst = a.out + (t.q0 + r / share) * a.ldo + int64_t(kh * share + r % share) * D;
+        float ref = -INFINITY;
+        sum = 0.0f;
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                uint32_t w[CH / 2];
+            for (int i = 0; i < CH; ++i) acc[b][i] = f32x4_t{0, 0, 0, 0};
+        for (int sp = 0; sp < live; ++sp) {
+            const int at = sp * kSlot + wave * kGroupBytes;
+            const float other = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(slots, at + kRefs + col * 4, 0, kCoherent));
+            const float more = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(slots, at + kRefs + 64 + col * 4, 0, kCoherent));
+            f32x4_t part[NB][CH];
 #pragma unroll
-                for (int i = 0; i < CH / 2; ++i)
-                    w[i] = uint32_t(from_f32<ACT>(acc[g][b][2 * i][j] * inv)) | (uint32_t(from_f32<ACT>(acc[g][b][2 * i + 1][j] * inv)) << 16);
-                uint16_t* to = dst + W * b + CH * (4 * kq + j);
-                if constexpr (CH == 8) *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
-                else *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[1]);
-            }
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int i = 0; i < CH; ++i)
+                    part[b][i] = __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
+                                                                 slots, at + ((b * CH + i) * 64 + lane) * 16, 0, kCoherent));
+            const float now = fmaxf(ref, other);
+            const float f0 = ref == -INFINITY ? 0.0f : exp2_fast(ref - now);
+            const float f1 = other == -INFINITY ? 0.0f : exp2_fast(other - now);
+            ref = now;
+            sum = sum * f0 + more * f1;
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int i = 0; i < CH; ++i) acc[b][i] = acc[b][i] * f0 + part[b][i] * f1;
+        }
     }
+    if (t.r0 + 16 * wave + col > last) return;
+    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+    uint16_t* dst = a.out + (t.q0 + qi) * a.ldo + int64_t(hd) * D;
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            uint32_t w[CH / 2];
+#pragma unroll
+            for (int i = 0; i < CH / 2; ++i)
+                w[i] = uint32_t(from_f32<ACT>(acc[b][2 * i][j] * inv)) | (uint32_t(from_f32<ACT>(acc[b][2 * i + 1][j] * inv)) << 16);
+            uint16_t* to = dst + W * b + CH * (4 * kq + j);
+            if constexpr (CH == 8) *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
+            else *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[1]);
+        }
 }
-
-// 16-row groups of a wave: two share each operand read, as far as the registers of two waves a SIMD go
-constexpr int row_groups(int d) { return d == 256 ? 1 : 2; }
 
 // Dynamic LDS beyond 64 KB has to be allowed for a kernel first.
 hipError_t allow_lds(const void* kernel, size_t bytes) {
@@ -904,12 +863,11 @@ hipError_t run(const Kv4AttentionArgs& a, const Kv4Plan& p, hipStream_t stream) 
     unsigned* counters = static_cast<unsigned*>(a.workspace);
     float* partials = p.splits > 1 ? reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + kSyncBytes) : nullptr;
     if (p.rows > 16) {
-        constexpr int CG = row_groups(D);
         const dim3 grid(unsigned(p.tiles * a.kv_heads), unsigned(p.splits));
         const size_t lds = 2 * sizeof(Stage<D>);
-        const hipError_t e = allow_lds(reinterpret_cast<const void*>(&kv4_rows_kernel<ACT, D, CG>), lds);
+        const hipError_t e = allow_lds(reinterpret_cast<const void*>(&kv4_rows_kernel<ACT, D>), lds);
         if (e != hipSuccess) return e;
-        kv4_rows_kernel<ACT, D, CG><<<grid, dim3(256), lds, stream>>>(a, p.tiles, int(p.span), p.splits, magic, counters, partials);
+        kv4_rows_kernel<ACT, D><<<grid, dim3(256), lds, stream>>>(a, p.tiles, int(p.span), p.splits, magic, counters, partials);
         return hipGetLastError();
     }
     const dim3 grid(unsigned(p.tiles), unsigned(a.kv_heads), unsigned(p.splits));
@@ -933,20 +891,26 @@ Kv4Plan plan_kv4_attention(int64_t tokens, int64_t batch, int heads, int kv_head
     Kv4Plan p{};
     const int64_t share = heads / kv_heads;
     p.rows = 16;
-    if (ragged && tokens * share > 32 * batch) p.rows = 64 * row_groups(dim);
-    p.tiles = ragged ? tokens * share / p.rows + batch : batch * ceil_div(share, p.rows);
     // the tokens a tile can see: its window, the queries of its rows, an aligned begin
-    int64_t most = capacity;
-    if (window > 0) {
-        const int64_t reach = (causal ? window : 2 * window) + (ragged ? p.rows : 1) + 64;
-        most = most < reach ? most : reach;
-    }
+    auto reach = [&](int rows) {
+        const int64_t r = (causal ? window : 2 * window) + (ragged ? rows : 1) + 64;
+        return window > 0 && r < capacity ? r : capacity;
+    };
+    // Tiles of 64 rows share the codes' conversion but have fewer workgroups to
+    // spread over the chip: they lead where a request has 16 rows or more and the
+    // call 4 M pairs of a row and a token (D = 128, one request: 128 queries x 32
+    // heads on 1024 tokens 17 us against 20 on tiles of 16, 50 queries 16 against
+    // 13; D = 64: 512 x 16 on 512 11 against 12, 50 x 16 on 1074 12 against 10; D =
+    // 256: 1024 x 8 on 1024 even, 512 x 8 on 512 20 against 16).
+    if (ragged && tokens * share >= 16 * batch && tokens * heads * reach(64) >= int64_t(1) << 22) p.rows = 64;
+    p.tiles = ragged ? tokens * share / p.rows + batch : batch * ceil_div(share, p.rows);
+    const int64_t most = reach(p.rows);
     // Splits: with few tiles as many as fill the chip once (768 workgroups of D
     // = 128; 4 x 131072 tokens: 111 us, twice as many 119, four times 131), else
     // twice over, as lengths may differ (64 x 0..8192 tokens: 92 us, once 100,
     // four times 94).  A tile's splits share a counter of the workspace's header.
     const int64_t base = p.tiles * kv_heads;
-    const int64_t room = 256 * (p.rows > 16 ? 2 : dim == 256 ? 2 : dim == 128 ? 3 : 4);
+    const int64_t room = 256 * (dim == 256 ? 2 : dim == 128 || p.rows > 16 ? 3 : 4);
     const int64_t want = base >= int64_t(kSyncBytes / 4) ? 1 : 4 * base <= room ? room / (base > 0 ? base : 1) : ceil_div(2 * room, base);
     int64_t span = ceil_div(ceil_div(most, want), 128) * 128;
     if (span < 256) span = 256;
