@@ -480,7 +480,7 @@ size_t kv4_pool_bytes(int64_t pages, int64_t page_size, int64_t kv_heads, int64_
  *              multiple of 8.  heads may be 0 (q_out unused).
  *   rope       device FP32 [rope_len][rot_dim], or NULL for no rotation: row p
  *              holds the cosines, then the sines, of rot_dim / 2 angles at
- *              position p; 4-byte aligned.  rot_dim is a multiple of 16, at
+ *              position p; 16-byte aligned.  rot_dim is a multiple of 16, at
  *              most head_dim; channels from rot_dim on are not rotated.
  *              With interleaved == 0 channel i turns with i + rot_dim / 2,
  *              else 2i with 2i + 1:  (a, b) -> (a c - b s, b c + a s), each

@@ -40,99 +40,143 @@ __device__ inline uint4 narrow8(const float v[8]) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// A thread owns 8 channels of one head of one token (16 bytes in).  The W/8
-// threads of a scale group are adjacent lanes.  Grid: x = token, y = parts of
-// 256 threads of the row.
+// A thread owns 16 channels of one head of one token: two octets a, b that the
+// rotation pairs (half layout: channels 8u.. and 8u + rot/2..; otherwise
+// neighbours), so each is loaded once and one row of angles serves both.
+//
+// A workgroup takes 16 consecutive tokens and `passes` x (256 / D) heads: the
+// tokens of a chunk are usually neighbours, and their words and half-words,
+// which interleave in the same cache lines, then reach memory as whole lines
+// from one L2 (one workgroup a token spread each line over the XCDs' L2s, which
+// wrote it back in parts: 8192 tokens of 48 heads of 128, 99 us).  The angles
+// stay in registers over the heads.
 template <int ACT, int D>
-__global__ __launch_bounds__(256) void kv4_append_kernel(Kv4AppendArgs a) {
-    constexpr int W = kv4_width(D), NB = kv4_blocks(D);
-    const int64_t t = blockIdx.x;
-    const int part = blockIdx.y * 256 + threadIdx.x;
-    const int head = part / (D / 8), d0 = part % (D / 8) * 8;
+__global__ __launch_bounds__(256) void kv4_append_kernel(Kv4AppendArgs a, int passes) {
+    constexpr int W = kv4_width(D), NB = kv4_blocks(D), UNITS = D / 16, HEADS = 256 / (16 * UNITS);
+    const int u = threadIdx.x % UNITS, row = threadIdx.x / UNITS;  // 16 tokens x HEADS heads
+    const int64_t t = int64_t(blockIdx.x) * 16 + row % 16;
+    if (t >= a.tokens) return;  // whole rows: a scale group's lanes leave together
     const int heads = a.heads + 2 * a.kv_heads;
-    if (head >= heads) return;  // whole heads: a scale group's lanes leave together
 
-    const uint16_t* row = a.qkv + t * a.ldqkv + int64_t(head) * D;
-    float v[8];
-    widen8<ACT>(*reinterpret_cast<const uint4*>(row + d0), v);
-
-    const bool is_v = head >= a.heads + a.kv_heads;
+    // octets, and whether they turn
+    const int r8 = a.rot / 16;  // octets of half the rotated channels
+    int oa = 2 * u, ob = 2 * u + 1;
+    if (!a.interleaved) {
+        oa = u < r8 ? u : 2 * u;
+        ob = u < r8 ? u + r8 : 2 * u + 1;
+    }
+    const bool turns = u < r8;
+    float c[8], s[8];
     bool known = true;
     if (a.rope) {
         const int64_t pos = a.positions[t];
         known = pos >= 0 && pos < a.rope_len;
-        if (!is_v && d0 < a.rot) {
-            const float* cs = a.rope + (known ? pos : 0) * a.rot;
-            const int half = a.rot / 2;
+        if (turns) {
+            const float4* cs = reinterpret_cast<const float4*>(a.rope + (known ? pos : 0) * a.rot + 8 * u);
+            const float4* sn = reinterpret_cast<const float4*>(a.rope + (known ? pos : 0) * a.rot + a.rot / 2 + 8 * u);
+            const float4 x[4] = {cs[0], cs[1], sn[0], sn[1]};
+            c[0] = x[0].x; c[1] = x[0].y; c[2] = x[0].z; c[3] = x[0].w;
+            c[4] = x[1].x; c[5] = x[1].y; c[6] = x[1].z; c[7] = x[1].w;
+            s[0] = x[2].x; s[1] = x[2].y; s[2] = x[2].z; s[3] = x[2].w;
+            s[4] = x[3].x; s[5] = x[3].y; s[6] = x[3].z; s[7] = x[3].w;
+        }
+    }
+
+    for (int p = 0; p < passes; ++p) {
+        const int head = (int(blockIdx.y) * passes + p) * HEADS + row / 16;
+        if (head >= heads) return;
+        const uint16_t* src = a.qkv + t * a.ldqkv + int64_t(head) * D;
+        float v[2][8];
+        widen8<ACT>(*reinterpret_cast<const uint4*>(src + 8 * oa), v[0]);
+        widen8<ACT>(*reinterpret_cast<const uint4*>(src + 8 * ob), v[1]);
+        const bool is_v = head >= a.heads + a.kv_heads;
+        if (turns && !is_v) {
             if (a.interleaved) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    rotate(v[2 * i], v[2 * i + 1], cs[d0 / 2 + i], cs[half + d0 / 2 + i], v[2 * i], v[2 * i + 1]);
-            } else {
-                const bool low = d0 < half;
-                float w[8];
-                widen8<ACT>(*reinterpret_cast<const uint4*>(row + (low ? d0 + half : d0 - half)), w);
-                const float* c = cs + (low ? d0 : d0 - half);
+                for (int o = 0; o < 2; ++o)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    float x, y;
-                    if (low) rotate(v[i], w[i], c[i], c[half + i], x, y);
-                    else rotate(w[i], v[i], c[i], c[half + i], x, y);
-                    v[i] = low ? x : y;
+                    for (int i = 0; i < 4; ++i)
+                        rotate(v[o][2 * i], v[o][2 * i + 1], c[4 * o + i], s[4 * o + i], v[o][2 * i], v[o][2 * i + 1]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) rotate(v[0][i], v[1][i], c[i], s[i], v[0][i], v[1][i]);
+            }
+        }
+        if (head < a.heads) {
+            if (!known) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[0][i] = v[1][i] = __uint_as_float(0x7FC00000u);
+            }
+            uint16_t* dst = a.q_out + (t * a.heads + head) * D;
+            *reinterpret_cast<uint4*>(dst + 8 * oa) = narrow8<ACT>(v[0]);
+            *reinterpret_cast<uint4*>(dst + 8 * ob) = narrow8<ACT>(v[1]);
+            continue;
+        }
+        const int64_t slot = a.slots[t];
+
+        // largest magnitude of each block, over the head's lanes
+        const int ba = 8 * oa / W, bb = 8 * ob / W;
+        float amax[NB];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) amax[b] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float x = fabsf(v[0][i]), y = fabsf(v[1][i]);
+            if constexpr (NB == 1) {
+                amax[0] = fmaxf(amax[0], fmaxf(x, y));
+            } else {
+#pragma unroll
+                for (int b = 0; b < NB; ++b) amax[b] = fmaxf(amax[b], fmaxf(ba == b ? x : 0.0f, bb == b ? y : 0.0f));
+            }
+        }
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            amax[b] = fmaxf(amax[b], lane_xor<1>(amax[b]));
+            amax[b] = fmaxf(amax[b], lane_xor<2>(amax[b]));
+            if constexpr (UNITS >= 8) amax[b] = fmaxf(amax[b], lane_xor<4>(amax[b]));
+            if constexpr (UNITS >= 16) amax[b] = fmaxf(amax[b], lane_xor<8>(amax[b]));
+        }
+        if (!(known && slot >= 0 && slot < a.pages * a.page)) continue;
+        float scale[NB];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) scale[b] = amax[b] / 7.0f;
+
+        const int64_t pg = slot / a.page;
+        const int tok = int(slot - pg * a.page);
+        const int kh = head - a.heads - (is_v ? a.kv_heads : 0);
+        uint8_t* region = a.pool + (pg * a.kv_heads + kh) * kv4_region(a.page, D);
+        const int tc = tok % kKvChunkTokens;
+#pragma unroll
+        for (int o = 0; o < 2; ++o) {
+            const int octet = o ? ob : oa, b = o ? bb : ba, e = 8 * octet - W * b;
+            const float f = NB == 1 || b == 0 ? scale[0] : scale[NB - 1];
+            uint32_t x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                float r = f != 0.0f ? rintf(v[o][i] / f) : 0.0f;
+                r = fminf(fmaxf(r, -8.0f), 7.0f);
+                x[i] = uint32_t(int(r) + 8);
+            }
+            uint8_t* chunk = region + (int64_t(tok / kKvChunkTokens) * NB + b) * (8 * W);
+            if (!is_v) {
+                uint32_t word = 0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) word |= (x[2 * i] << (4 * i)) | (x[2 * i + 1] << (16 + 4 * i));
+                *reinterpret_cast<uint32_t*>(chunk + (16 * (e % 32 / 8) + tc) * (W / 8) + 4 * (e / 32)) = word;
+            } else {
+                uint8_t* vr = chunk + int64_t(a.page) * D / 2;
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {  // two groups of 4 channels: groups h of one lane (W = 128) or two lanes
+                    const uint16_t half = uint16_t(x[4 * g] | (x[4 * g + 1] << 4) | (x[4 * g + 2] << 8) | (x[4 * g + 3] << 12));
+                    const int l = (e + 4 * g) / (W / 16), h = (e + 4 * g) % (W / 16) / 4;
+                    *reinterpret_cast<uint16_t*>(vr + (16 * (tc / 4) + l) * (W / 8) + 8 * h + 4 * (tc % 4 / 2) + 2 * (tc % 2)) = half;
                 }
             }
         }
+        if (u < NB)
+            reinterpret_cast<float*>(region + int64_t(a.page) * D)[((is_v ? NB : 0) + u) * int64_t(a.page) + tok] =
+                NB == 1 || u == 0 ? scale[0] : scale[NB - 1];
     }
-    if (head < a.heads) {
-        if (!known) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(0x7FC00000u);
-        }
-        *reinterpret_cast<uint4*>(a.q_out + (t * a.heads + head) * D + d0) = narrow8<ACT>(v);
-        return;
-    }
-    const int64_t slot = a.slots[t];
-    const bool stored = known && slot >= 0 && slot < a.pages * a.page;
-
-    float amax = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[i]));
-    amax = fmaxf(amax, lane_xor<1>(amax));
-    amax = fmaxf(amax, lane_xor<2>(amax));
-    amax = fmaxf(amax, lane_xor<4>(amax));
-    if constexpr (W == 128) amax = fmaxf(amax, lane_xor<8>(amax));
-    if (!stored) return;
-    const float s = amax / 7.0f;
-    uint32_t u[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        float r = s != 0.0f ? rintf(v[i] / s) : 0.0f;
-        r = fminf(fmaxf(r, -8.0f), 7.0f);
-        u[i] = uint32_t(int(r) + 8);
-    }
-
-    const int64_t pg = slot / a.page;
-    const int tok = int(slot - pg * a.page);
-    const int kh = head - a.heads - (is_v ? a.kv_heads : 0);
-    uint8_t* region = a.pool + (pg * a.kv_heads + kh) * kv4_region(a.page, D);
-    const int b = d0 / W, e = d0 % W, tc = tok % kKvChunkTokens;
-    const int64_t chunk = (int64_t(tok / kKvChunkTokens) * NB + b) * (8 * W);
-    if (!is_v) {
-        uint32_t word = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) word |= (u[2 * i] << (4 * i)) | (u[2 * i + 1] << (16 + 4 * i));
-        *reinterpret_cast<uint32_t*>(region + chunk + (16 * (e % 32 / 8) + tc) * (W / 8) + 4 * (e / 32)) = word;
-    } else {
-        uint8_t* vr = region + int64_t(a.page) * D / 2 + chunk;
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {  // two groups of 4 channels: groups h of one lane (W = 128) or two lanes
-            const uint16_t half = uint16_t(u[4 * g] | (u[4 * g + 1] << 4) | (u[4 * g + 2] << 8) | (u[4 * g + 3] << 12));
-            const int l = (e + 4 * g) / (W / 16), h = (e + 4 * g) % (W / 16) / 4;
-            *reinterpret_cast<uint16_t*>(vr + (16 * (tc / 4) + l) * (W / 8) + 8 * h + 4 * (tc % 4 / 2) + 2 * (tc % 2)) = half;
-        }
-    }
-    if (e == 0)
-        reinterpret_cast<float*>(region + int64_t(a.page) * D)[(is_v ? NB + b : b) * int64_t(a.page) + tok] = s;
 }
 
 // A thread reads 8 channels of one head of one token of both sides.
@@ -190,11 +234,15 @@ __global__ __launch_bounds__(256) void kv4_read_kernel(Kv4ReadArgs a) {
 
 template <int ACT>
 hipError_t append_by_dim(const Kv4AppendArgs& a, hipStream_t stream) {
-    const dim3 grid(unsigned(a.tokens), unsigned(ceil_div(int64_t(a.heads + 2 * a.kv_heads) * (a.dim / 8), 256)));
+    // heads of a workgroup's pass, and as many passes (up to 4) as leave two workgroups a CU
+    const int64_t per = 256 / a.dim, blocks = ceil_div(a.tokens, 16), rows = ceil_div(int64_t(a.heads + 2 * a.kv_heads), per);
+    int passes = 4;
+    while (passes > 1 && blocks * ceil_div(rows, passes) < 512) passes /= 2;
+    const dim3 grid(unsigned(blocks), unsigned(ceil_div(rows, passes)));
     switch (a.dim) {
-        case 64: kv4_append_kernel<ACT, 64><<<grid, dim3(256), 0, stream>>>(a); break;
-        case 128: kv4_append_kernel<ACT, 128><<<grid, dim3(256), 0, stream>>>(a); break;
-        default: kv4_append_kernel<ACT, 256><<<grid, dim3(256), 0, stream>>>(a); break;
+        case 64: kv4_append_kernel<ACT, 64><<<grid, dim3(256), 0, stream>>>(a, passes); break;
+        case 128: kv4_append_kernel<ACT, 128><<<grid, dim3(256), 0, stream>>>(a, passes); break;
+        default: kv4_append_kernel<ACT, 256><<<grid, dim3(256), 0, stream>>>(a, passes); break;
     }
     return hipGetLastError();
 }

@@ -62,7 +62,7 @@ w4a16_status_t kv4_append(const void* qkv, w4a16_dtype_t dtype, int64_t tokens, 
     if (tokens < 0 || tokens > kMaxDim || ldqkv < width || ldqkv > kMaxDim || ldqkv % 8 != 0) return W4A16_EINVAL;
     if ((rope == nullptr) != (positions == nullptr)) return W4A16_EINVAL;
     if (rope && (rope_len < 1 || rope_len > kMaxTokens || rot_dim < 16 || rot_dim > head_dim || rot_dim % 16 != 0 ||
-                 !aligned(rope, 4) || !aligned(positions, 4)))
+                 !aligned(rope, 16) || !aligned(positions, 4)))
         return W4A16_EINVAL;
     if (tokens == 0) return W4A16_OK;
     if (!qkv || !slots || !pool || (heads > 0 && !q_out)) return W4A16_EINVAL;
