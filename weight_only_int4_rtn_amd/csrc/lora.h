@@ -24,6 +24,7 @@ struct LoraArgs {
 };
 
 struct LoraPlan {
+    int rows;          // rows of the second launch's tiles (16 or 64)
     int slots;         // workgroups that share a row tile's distinct adapters
     int splits;        // parts of K
     int64_t kspan;     // columns of one part (a multiple of 32 except the last)

@@ -4,11 +4,12 @@
 //                                                  not an adapter
 //
 // Two launches.  The first contracts K: t = x A^T in FP32, per part of K.
-// The second adds the parts, contracts the rank and adds y.  Both take tiles
-// of 16 rows in the order given: a tile's distinct adapters are found from
-// its 16 indices, and each is one product in which the rows of other adapters
-// are computed and dropped (matrix instructions are idle here; the weights'
-// bytes are what counts, and each adapter's are read once a tile).
+// The second adds the parts, contracts the rank and adds y.  Both take tiles of
+// rows in the order given: a tile's distinct adapters are found from its
+// indices, and each is one product in which the rows of other adapters are
+// computed and dropped (matrix instructions are idle here; the weights' bytes
+// are what counts, and each adapter's are read once a tile).  With few rows a
+// tile's adapters go to workgroups of their own (slots).
 #include "common.h"
 #include "kernels.h"
 #include "lora.h"
@@ -25,16 +26,17 @@ __device__ inline f32x4_t mfma16(uint4 a, uint4 b, f32x4_t c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, a), __builtin_bit_cast(f16x8_t, b), c, 0, 0, 0);
 }
 
-// The distinct adapters among a tile's rows, taken one by one; lanes 0..15
-// of `mine` (and their copies) hold the rows' indices.
+// The distinct adapters among a tile's ROWS rows (16 or 64), taken one by one;
+// lane L holds row L % ROWS's index in `mine`.
+template <int ROWS>
 struct Distinct {
     int mine;
     uint64_t left;
     __device__ Distinct(const int32_t* index, int64_t row0, int64_t m, int adapters, int lane) {
-        const int64_t row = row0 + lane % 16;
+        const int64_t row = row0 + lane % ROWS;
         mine = row < m ? index[row] : -1;
         if (mine >= adapters) mine = -1;
-        left = __ballot(mine >= 0) & 0xFFFFull;
+        left = __ballot(mine >= 0) & (ROWS == 64 ? ~0ull : 0xFFFFull);
     }
     __device__ int next() {
         const int l = __builtin_amdgcn_readlane(mine, __ffsll((unsigned long long)left) - 1);
@@ -50,11 +52,12 @@ constexpr int kWaves = 4;
 // turn and add up in LDS.
 template <int ACT, int RT>  // RT: 16-row tiles of the rank
 __global__ __launch_bounds__(256) void lora_shrink_kernel(LoraArgs a, int slots, int kspan, float* t) {
+    constexpr int UN = RT >= 8 ? 2 : 4;
     __shared__ float lds[kWaves][RT * 4][64];
     const int lane = threadIdx.x % 64, wave = uniform(threadIdx.x / 64);
     const int col = lane % 16, kq = lane / 16;
     const int64_t row0 = int64_t(blockIdx.x) * 16;
-    Distinct d(a.index, row0, a.m, a.adapters, lane);
+    Distinct<16> d(a.index, row0, a.m, a.adapters, lane);
     const int64_t k0 = int64_t(blockIdx.z) * kspan, k1 = k0 + kspan < a.k ? k0 + kspan : a.k;
     const int64_t row = row0 + col < a.m ? row0 + col : a.m - 1;
     const uint16_t* xr = a.x + row * a.ldx + 8 * kq;
@@ -70,15 +73,35 @@ __global__ __launch_bounds__(256) void lora_shrink_kernel(LoraArgs a, int slots,
         f32x4_t acc[RT];
 #pragma unroll
         for (int i = 0; i < RT; ++i) acc[i] = f32x4_t{0, 0, 0, 0};
-        for (int64_t k = k0 + 32 * wave; k < k1; k += 32 * kWaves) {
-            // K is a multiple of 8: a lane's 8 columns are inside or outside together
-            const bool in = k + 8 * kq < k1;
-            const uint4 zero = make_uint4(0, 0, 0, 0);
-            const uint4 xv = in ? *reinterpret_cast<const uint4*>(xr + k) : zero;
+        // A wave takes runs of 32 UN columns in turn, all of a run's loads in
+        // flight together; of the last run the columns that exist (K is a
+        // multiple of 8: a lane's 8 columns are inside or outside together).
+        for (int64_t k = k0 + 32 * UN * wave; k < k1; k += 32 * UN * kWaves) {
+            if (k + 32 * UN <= k1) {
+                uint4 xv[UN], av[UN][RT];
 #pragma unroll
-            for (int i = 0; i < RT; ++i) {
-                const uint4 av = in ? *reinterpret_cast<const uint4*>(ar[i] + k) : zero;
-                acc[i] = mfma16<ACT>(av, xv, acc[i]);
+                for (int n = 0; n < UN; ++n) {
+                    xv[n] = *reinterpret_cast<const uint4*>(xr + k + 32 * n);
+#pragma unroll
+                    for (int i = 0; i < RT; ++i) av[n][i] = *reinterpret_cast<const uint4*>(ar[i] + k + 32 * n);
+                }
+#pragma unroll
+                for (int n = 0; n < UN; ++n)
+#pragma unroll
+                    for (int i = 0; i < RT; ++i) acc[i] = mfma16<ACT>(av[n][i], xv[n], acc[i]);
+                continue;
+            }
+            for (int64_t kk = k; kk < k1; kk += 32) {
+                uint4 xv = make_uint4(0, 0, 0, 0), av[RT];
+#pragma unroll
+                for (int i = 0; i < RT; ++i) av[i] = xv;
+                if (kk + 8 * kq < k1) {
+                    xv = *reinterpret_cast<const uint4*>(xr + kk);
+#pragma unroll
+                    for (int i = 0; i < RT; ++i) av[i] = *reinterpret_cast<const uint4*>(ar[i] + kk);
+                }
+#pragma unroll
+                for (int i = 0; i < RT; ++i) acc[i] = mfma16<ACT>(av[i], xv, acc[i]);
             }
         }
 #pragma unroll
@@ -100,20 +123,88 @@ __global__ __launch_bounds__(256) void lora_shrink_kernel(LoraArgs a, int slots,
     }
 }
 
-// out[row] = y[row] + scale t[row] B_l^T.  Grid: x = 256 columns, y = row
-// tile, z = slot.  A wave computes 64 columns as two pairs of MFMA tiles whose
-// output rows interleave, so a lane holds 8 consecutive columns of its row.
-// t enters as a high and a low 16-bit part (16 or more significant bits in
-// all), scaled by a power of two per row so that f16 neither overflows nor
-// loses bits.
+// One row's t (its parts added, times the adapter's scale) as MFMA operands: a
+// high and a low 16-bit part (16 or more significant bits in all), scaled by
+// 2^-e so that f16 neither overflows nor loses bits.  Returns e.
 template <int ACT, int RS>  // RS: 32-wide steps of the rank
+__device__ inline int row_operand(const LoraArgs& a, const float* t, int splits, int64_t row, bool mine, float scale, int kq,
+                                  uint4 (&hi)[RS], uint4 (&lo)[RS]) {
+    float v[RS][8];
+    float big = 0.0f;
+#pragma unroll
+    for (int s = 0; s < RS; ++s) {
+        const int r = 32 * s + 8 * kq;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[s][i] = 0.0f;
+        if (mine && r < a.rank) {
+            for (int p = 0; p < splits; ++p) {
+                const float4* src = reinterpret_cast<const float4*>(t + (int64_t(p) * a.m + row) * a.rank + r);
+                const float4 x = src[0], y = src[1];
+                v[s][0] += x.x; v[s][1] += x.y; v[s][2] += x.z; v[s][3] += x.w;
+                v[s][4] += y.x; v[s][5] += y.y; v[s][6] += y.z; v[s][7] += y.w;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            v[s][i] *= scale;
+            big = fmaxf(big, fabsf(v[s][i]));
+        }
+    }
+    big = max_xor32(fmaxf(big, lane_xor<16>(big)));
+    const int e = big > 0.0f && big < 3e38f ? int(__float_as_uint(big) >> 23) - 127 : 0;
+#pragma unroll
+    for (int s = 0; s < RS; ++s) {
+        uint32_t h[4], w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float p = ldexpf(v[s][2 * i], -e), q = ldexpf(v[s][2 * i + 1], -e);
+            const uint16_t ph = from_f32<ACT>(p), qh = from_f32<ACT>(q);
+            h[i] = uint32_t(ph) | (uint32_t(qh) << 16);
+            w[i] = uint32_t(from_f32<ACT>(p - to_f32<ACT>(ph))) | (uint32_t(from_f32<ACT>(q - to_f32<ACT>(qh))) << 16);
+        }
+        hi[s] = make_uint4(h[0], h[1], h[2], h[3]);
+        lo[s] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    return e;
+}
+
+// MFMA row `col` of half h of a 32-column group: columns interleave so that a
+// lane's two times four results are 8 consecutive columns.
+__device__ inline int column_of(int col, int h) { return 8 * (col / 4) + 4 * h + col % 4; }
+
+// out = y + add on 8 columns from n on, as far as they exist.
+template <int ACT>
+__device__ inline void add_columns(const LoraArgs& a, int64_t row, int64_t n, const float (&add)[8]) {
+    const uint16_t* src = a.y + row * a.ldy + n;
+    uint16_t* dst = a.out + row * a.ldo + n;
+    const bool wide = n + 8 <= a.n && a.ldy % 8 == 0 && a.ldo % 8 == 0 &&
+                      ((reinterpret_cast<uintptr_t>(a.y) | reinterpret_cast<uintptr_t>(a.out)) & 15) == 0;
+    if (wide) {
+        const uint4 raw = *reinterpret_cast<const uint4*>(src);
+        const uint32_t in[4] = {raw.x, raw.y, raw.z, raw.w};
+        uint32_t o[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            o[i] = uint32_t(from_f32<ACT>(to_f32<ACT>(uint16_t(in[i])) + add[2 * i])) |
+                   (uint32_t(from_f32<ACT>(to_f32<ACT>(uint16_t(in[i] >> 16)) + add[2 * i + 1])) << 16);
+        *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (n + i < a.n) dst[i] = from_f32<ACT>(to_f32<ACT>(src[i]) + add[i]);
+    }
+}
+
+// Few rows: out[row] = y[row] + scale t[row] B_l^T.  Grid: x = 256 columns, y =
+// tile of 16 rows, z = slot.  A wave computes 64 columns.
+template <int ACT, int RS>
 __global__ __launch_bounds__(256) void lora_expand_kernel(LoraArgs a, int slots, int splits, const float* t) {
     const int lane = threadIdx.x % 64, wave = uniform(threadIdx.x / 64);
     const int col = lane % 16, kq = lane / 16;
     const int64_t row0 = int64_t(blockIdx.y) * 16;
     const int64_t n0 = int64_t(blockIdx.x) * 256 + 64 * wave;
     if (n0 >= a.n) return;
-    Distinct d(a.index, row0, a.m, a.adapters, lane);
+    Distinct<16> d(a.index, row0, a.m, a.adapters, lane);
     const int64_t row = row0 + col;
     const bool real = row < a.m;
     float add[2][8];
@@ -128,58 +219,31 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(LoraArgs a, int slots,
         if (seen % slots != int(blockIdx.z)) continue;
         const bool mine = real && d.mine == l;
         write |= mine;
-        const float scale = a.scales ? a.scales[l] : 1.0f;
-        float v[RS][8];
-        float big = 0.0f;
+        uint4 bv[2][2][RS];
 #pragma unroll
-        for (int s = 0; s < RS; ++s) {
-            const int r = 32 * s + 8 * kq;
+        for (int g = 0; g < 2; ++g)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[s][i] = 0.0f;
-            if (mine && r < a.rank) {
-                for (int p = 0; p < splits; ++p) {
-                    const float4* src = reinterpret_cast<const float4*>(t + (int64_t(p) * a.m + row) * a.rank + r);
-                    const float4 lo = src[0], hi = src[1];
-                    v[s][0] += lo.x; v[s][1] += lo.y; v[s][2] += lo.z; v[s][3] += lo.w;
-                    v[s][4] += hi.x; v[s][5] += hi.y; v[s][6] += hi.z; v[s][7] += hi.w;
+            for (int h = 0; h < 2; ++h) {
+                const int64_t n = n0 + 32 * g + column_of(col, h);
+                const uint16_t* br = a.b + (int64_t(l) * a.n + (n < a.n ? n : a.n - 1)) * a.rank + 8 * kq;
+#pragma unroll
+                for (int s = 0; s < RS; ++s) {
+                    bv[g][h][s] = make_uint4(0, 0, 0, 0);
+                    if (32 * s + 8 * kq < a.rank) bv[g][h][s] = *reinterpret_cast<const uint4*>(br + 32 * s);
                 }
             }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                v[s][i] *= scale;
-                big = fmaxf(big, fabsf(v[s][i]));
-            }
-        }
-        big = max_xor32(fmaxf(big, lane_xor<16>(big)));
-        const int e = big > 0.0f && big < 3e38f ? int(__float_as_uint(big) >> 23) - 127 : 0;
         uint4 hi[RS], lo[RS];
-#pragma unroll
-        for (int s = 0; s < RS; ++s) {
-            uint32_t h[4], w[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float p = ldexpf(v[s][2 * i], -e), q = ldexpf(v[s][2 * i + 1], -e);
-                const uint16_t ph = from_f32<ACT>(p), qh = from_f32<ACT>(q);
-                h[i] = uint32_t(ph) | (uint32_t(qh) << 16);
-                w[i] = uint32_t(from_f32<ACT>(p - to_f32<ACT>(ph))) | (uint32_t(from_f32<ACT>(q - to_f32<ACT>(qh))) << 16);
-            }
-            hi[s] = make_uint4(h[0], h[1], h[2], h[3]);
-            lo[s] = make_uint4(w[0], w[1], w[2], w[3]);
-        }
+        const int e = row_operand<ACT, RS>(a, t, splits, row, mine, a.scales ? a.scales[l] : 1.0f, kq, hi, lo);
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
             f32x4_t acc[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                // MFMA row `col` of half h is column 8 (col / 4) + 4 h + col % 4
-                const int64_t n = n0 + 32 * g + 8 * (col / 4) + 4 * h + col % 4;
-                const uint16_t* br = a.b + (int64_t(l) * a.n + (n < a.n ? n : a.n - 1)) * a.rank + 8 * kq;
                 acc[h] = f32x4_t{0, 0, 0, 0};
 #pragma unroll
                 for (int s = 0; s < RS; ++s) {
-                    const uint4 bv = 32 * s + 8 * kq < a.rank ? *reinterpret_cast<const uint4*>(br + 32 * s) : make_uint4(0, 0, 0, 0);
-                    acc[h] = mfma16<ACT>(bv, hi[s], acc[h]);
-                    acc[h] = mfma16<ACT>(bv, lo[s], acc[h]);
+                    acc[h] = mfma16<ACT>(bv[g][h][s], hi[s], acc[h]);
+                    acc[h] = mfma16<ACT>(bv[g][h][s], lo[s], acc[h]);
                 }
             }
             if (mine) {
@@ -190,26 +254,79 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(LoraArgs a, int slots,
     }
     if (!write) return;
 #pragma unroll
-    for (int g = 0; g < 2; ++g) {
-        const int64_t n = n0 + 32 * g + 8 * kq;
-        const uint16_t* src = a.y + row * a.ldy + n;
-        uint16_t* dst = a.out + row * a.ldo + n;
-        const bool wide = n + 8 <= a.n && a.ldy % 8 == 0 && a.ldo % 8 == 0 &&
-                          ((reinterpret_cast<uintptr_t>(a.y) | reinterpret_cast<uintptr_t>(a.out)) & 15) == 0;
-        if (wide) {
-            const uint4 raw = *reinterpret_cast<const uint4*>(src);
-            const uint32_t in[4] = {raw.x, raw.y, raw.z, raw.w};
-            uint32_t o[4];
+    for (int g = 0; g < 2; ++g) add_columns<ACT>(a, row, n0 + 32 * g + 8 * kq, add[g]);
+}
+
+// Many rows.  Grid: x = 512 columns, y = tile of 64 rows.  A wave takes 128
+// columns of all 64 rows, so each operand of B serves four products and t is
+// turned into operands once for four groups of columns.  A tile's adapters are
+// taken one after another, each reading and writing the rows that are its own.
+constexpr int kTileCols = 512, kTileGroups = 4;
+
+template <int ACT, int RS>
+__global__ __launch_bounds__(256) void lora_expand_rows_kernel(LoraArgs a, int splits, const float* t) {
+    const int lane = threadIdx.x % 64, wave = uniform(threadIdx.x / 64);
+    const int col = lane % 16, kq = lane / 16;
+    const int64_t row0 = int64_t(blockIdx.y) * 64;
+    const int64_t n0 = int64_t(blockIdx.x) * kTileCols + 32 * kTileGroups * wave;
+    if (n0 >= a.n) return;
+    Distinct<64> d(a.index, row0, a.m, a.adapters, lane);
+    int index[4];  // of this lane's row in each group of 16
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                o[i] = uint32_t(from_f32<ACT>(to_f32<ACT>(uint16_t(in[i])) + add[g][2 * i])) |
-                       (uint32_t(from_f32<ACT>(to_f32<ACT>(uint16_t(in[i] >> 16)) + add[g][2 * i + 1])) << 16);
-            *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
-        } else {
+    for (int g = 0; g < 4; ++g) index[g] = __shfl(d.mine, 16 * g + col);
+    while (d.left) {
+        const int l = d.next();
+        const float scale = a.scales ? a.scales[l] : 1.0f;
+        uint4 hi[4][RS], lo[4][RS];
+        int e[4];
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (n + i < a.n) dst[i] = from_f32<ACT>(to_f32<ACT>(src[i]) + add[g][i]);
+        for (int g = 0; g < 4; ++g)
+            e[g] = row_operand<ACT, RS>(a, t, splits, row0 + 16 * g + col, index[g] == l, scale, kq, hi[g], lo[g]);
+#pragma unroll 1
+        for (int c = 0; c < kTileGroups; ++c) {
+            const int64_t c0 = n0 + 32 * c;
+            if (c0 >= a.n) break;
+            uint4 bv[2][RS];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int64_t n = c0 + column_of(col, h);
+                const uint16_t* br = a.b + (int64_t(l) * a.n + (n < a.n ? n : a.n - 1)) * a.rank + 8 * kq;
+#pragma unroll
+                for (int s = 0; s < RS; ++s) {
+                    bv[h][s] = make_uint4(0, 0, 0, 0);
+                    if (32 * s + 8 * kq < a.rank) bv[h][s] = *reinterpret_cast<const uint4*>(br + 32 * s);
+                }
+            }
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                if (!__any(index[g] == l)) continue;
+                f32x4_t acc[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    acc[h] = f32x4_t{0, 0, 0, 0};
+#pragma unroll
+                    for (int s = 0; s < RS; ++s) {
+                        acc[h] = mfma16<ACT>(bv[h][s], hi[g][s], acc[h]);
+                        acc[h] = mfma16<ACT>(bv[h][s], lo[g][s], acc[h]);
+                    }
+                }
+                if (index[g] == l) {
+                    float add[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) add[i] = ldexpf(acc[i / 4][i % 4], e[g]);
+                    add_columns<ACT>(a, row0 + 16 * g + col, c0 + 8 * kq, add);
+                }
+            }
         }
+    }
+    // rows without an adapter
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+        const int64_t row = row0 + 16 * g + col;
+        if (index[g] >= 0 || row >= a.m || a.out == a.y) continue;
+        const float none[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        for (int c = 0; c < kTileGroups; ++c)
+            if (n0 + 32 * c + 8 * kq < a.n) add_columns<ACT>(a, row, n0 + 32 * c + 8 * kq, none);
     }
 }
 
@@ -220,7 +337,10 @@ hipError_t run(const LoraArgs& a, const LoraPlan& p, hipStream_t stream) {
     lora_shrink_kernel<ACT, RT><<<dim3(tiles, unsigned(p.slots), unsigned(p.splits)), dim3(256), 0, stream>>>(a, p.slots, int(p.kspan), t);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    lora_expand_kernel<ACT, (RT + 1) / 2><<<dim3(unsigned(ceil_div(a.n, 256)), tiles, unsigned(p.slots)), dim3(256), 0, stream>>>(a, p.slots, p.splits, t);
+    if (p.rows == 64)
+        lora_expand_rows_kernel<ACT, (RT + 1) / 2><<<dim3(unsigned(ceil_div(a.n, kTileCols)), unsigned(ceil_div(a.m, 64))), dim3(256), 0, stream>>>(a, p.splits, t);
+    else
+        lora_expand_kernel<ACT, (RT + 1) / 2><<<dim3(unsigned(ceil_div(a.n, 256)), tiles, unsigned(p.slots)), dim3(256), 0, stream>>>(a, p.slots, p.splits, t);
     return hipGetLastError();
 }
 
@@ -240,9 +360,11 @@ constexpr int64_t kMaxRows = int64_t(1) << 19;
 LoraPlan plan_lora(int64_t m, int64_t n, int64_t k, int adapters, int rank) {
     LoraPlan p{};
     if (m > kMaxRows) m = kMaxRows;
+    // rows of the second launch's tiles: 64 once those fill the chip twice over
+    p.rows = ceil_div(m, 64) * ceil_div(n, kTileCols) >= 512 ? 64 : 16;
     const int64_t tiles = ceil_div(m, 16);
     const int64_t most = m < 16 ? m : 16;
-    p.slots = int(tiles >= 64 ? 1 : most < adapters ? most : adapters);
+    p.slots = int(p.rows == 64 || tiles >= 64 ? 1 : most < adapters ? most : adapters);
     if (p.slots < 1) p.slots = 1;
     int64_t splits = ceil_div(512, tiles * p.slots);
     if (splits > ceil_div(k, 512)) splits = ceil_div(k, 512);
