@@ -172,26 +172,38 @@ __device__ inline int row_operand(const LoraArgs& a, const float* t, int splits,
 // lane's two times four results are 8 consecutive columns.
 __device__ inline int column_of(int col, int h) { return 8 * (col / 4) + 4 * h + col % 4; }
 
-// out = y + add on 8 columns from n on, as far as they exist.
-template <int ACT>
-__device__ inline void add_columns(const LoraArgs& a, int64_t row, int64_t n, const float (&add)[8]) {
+// y and out on 8 columns from n on, as far as they exist; 16 bytes at once where
+// all do and both sides are aligned.
+__device__ inline bool whole_columns(const LoraArgs& a, int64_t n) {
+    return n + 8 <= a.n && a.ldy % 8 == 0 && a.ldo % 8 == 0 &&
+           ((reinterpret_cast<uintptr_t>(a.y) | reinterpret_cast<uintptr_t>(a.out)) & 15) == 0;
+}
+
+__device__ inline uint4 load_columns(const LoraArgs& a, int64_t row, int64_t n) {
     const uint16_t* src = a.y + row * a.ldy + n;
-    uint16_t* dst = a.out + row * a.ldo + n;
-    const bool wide = n + 8 <= a.n && a.ldy % 8 == 0 && a.ldo % 8 == 0 &&
-                      ((reinterpret_cast<uintptr_t>(a.y) | reinterpret_cast<uintptr_t>(a.out)) & 15) == 0;
-    if (wide) {
-        const uint4 raw = *reinterpret_cast<const uint4*>(src);
-        const uint32_t in[4] = {raw.x, raw.y, raw.z, raw.w};
-        uint32_t o[4];
+    if (whole_columns(a, n)) return *reinterpret_cast<const uint4*>(src);
+    uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            o[i] = uint32_t(from_f32<ACT>(to_f32<ACT>(uint16_t(in[i])) + add[2 * i])) |
-                   (uint32_t(from_f32<ACT>(to_f32<ACT>(uint16_t(in[i] >> 16)) + add[2 * i + 1])) << 16);
+    for (int i = 0; i < 8; ++i)
+        if (n + i < a.n) w[i / 2] |= uint32_t(src[i]) << (16 * (i % 2));
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <int ACT>
+__device__ inline void store_columns(const LoraArgs& a, int64_t row, int64_t n, uint4 y, const float (&add)[8]) {
+    const uint32_t in[4] = {y.x, y.y, y.z, y.w};
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        o[i] = uint32_t(from_f32<ACT>(to_f32<ACT>(uint16_t(in[i])) + add[2 * i])) |
+               (uint32_t(from_f32<ACT>(to_f32<ACT>(uint16_t(in[i] >> 16)) + add[2 * i + 1])) << 16);
+    uint16_t* dst = a.out + row * a.ldo + n;
+    if (whole_columns(a, n)) {
         *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (n + i < a.n) dst[i] = from_f32<ACT>(to_f32<ACT>(src[i]) + add[i]);
+            if (n + i < a.n) dst[i] = uint16_t(o[i / 2] >> (16 * (i % 2)));
     }
 }
 
@@ -254,7 +266,10 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(LoraArgs a, int slots,
     }
     if (!write) return;
 #pragma unroll
-    for (int g = 0; g < 2; ++g) add_columns<ACT>(a, row, n0 + 32 * g + 8 * kq, add[g]);
+    for (int g = 0; g < 2; ++g) {
+        const int64_t n = n0 + 32 * g + 8 * kq;
+        store_columns<ACT>(a, row, n, load_columns(a, row, n), add[g]);
+    }
 }
 
 // Many rows.  Grid: x = 512 columns, y = tile of 64 rows.  A wave takes 128
@@ -271,6 +286,7 @@ __global__ __launch_bounds__(256) void lora_expand_rows_kernel(LoraArgs a, int s
     const int64_t n0 = int64_t(blockIdx.x) * kTileCols + 32 * kTileGroups * wave;
     if (n0 >= a.n) return;
     Distinct<64> d(a.index, row0, a.m, a.adapters, lane);
+    constexpr int PAIR = RS > 2 ? 1 : 2;
     int index[4];  // of this lane's row in each group of 16
 #pragma unroll
     for (int g = 0; g < 4; ++g) index[g] = __shfl(d.mine, 16 * g + col);
@@ -282,39 +298,48 @@ __global__ __launch_bounds__(256) void lora_expand_rows_kernel(LoraArgs a, int s
 #pragma unroll
         for (int g = 0; g < 4; ++g)
             e[g] = row_operand<ACT, RS>(a, t, splits, row0 + 16 * g + col, index[g] == l, scale, kq, hi[g], lo[g]);
+        // 64 columns at a time: a row's line of 128 bytes is read and written in one go
 #pragma unroll 1
-        for (int c = 0; c < kTileGroups; ++c) {
-            const int64_t c0 = n0 + 32 * c;
-            if (c0 >= a.n) break;
-            uint4 bv[2][RS];
+        for (int c = 0; c < kTileGroups; c += PAIR) {
+            uint4 bv[PAIR][2][RS], yv[PAIR][4];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int64_t n = c0 + column_of(col, h);
-                const uint16_t* br = a.b + (int64_t(l) * a.n + (n < a.n ? n : a.n - 1)) * a.rank + 8 * kq;
+            for (int p = 0; p < PAIR; ++p) {
+                const int64_t c0 = n0 + 32 * (c + p);
 #pragma unroll
-                for (int s = 0; s < RS; ++s) {
-                    bv[h][s] = make_uint4(0, 0, 0, 0);
-                    if (32 * s + 8 * kq < a.rank) bv[h][s] = *reinterpret_cast<const uint4*>(br + 32 * s);
+                for (int h = 0; h < 2; ++h) {
+                    const int64_t n = c0 + column_of(col, h);
+                    const uint16_t* br = a.b + (int64_t(l) * a.n + (n < a.n ? n : a.n - 1)) * a.rank + 8 * kq;
+#pragma unroll
+                    for (int s = 0; s < RS; ++s) {
+                        bv[p][h][s] = make_uint4(0, 0, 0, 0);
+                        if (32 * s + 8 * kq < a.rank) bv[p][h][s] = *reinterpret_cast<const uint4*>(br + 32 * s);
+                    }
                 }
+#pragma unroll
+                for (int g = 0; g < 4; ++g)
+                    if (index[g] == l) yv[p][g] = load_columns(a, row0 + 16 * g + col, c0 + 8 * kq);
             }
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
                 if (!__any(index[g] == l)) continue;
-                f32x4_t acc[2];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    acc[h] = f32x4_t{0, 0, 0, 0};
+                for (int p = 0; p < PAIR; ++p) {
+                    f32x4_t acc[2];
 #pragma unroll
-                    for (int s = 0; s < RS; ++s) {
-                        acc[h] = mfma16<ACT>(bv[h][s], hi[g][s], acc[h]);
-                        acc[h] = mfma16<ACT>(bv[h][s], lo[g][s], acc[h]);
+                    for (int h = 0; h < 2; ++h) {
+                        acc[h] = f32x4_t{0, 0, 0, 0};
+#pragma unroll
+                        for (int s = 0; s < RS; ++s) {
+                            acc[h] = mfma16<ACT>(bv[p][h][s], hi[g][s], acc[h]);
+                            acc[h] = mfma16<ACT>(bv[p][h][s], lo[g][s], acc[h]);
+                        }
                     }
-                }
-                if (index[g] == l) {
-                    float add[8];
+                    if (index[g] == l) {
+                        float add[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) add[i] = ldexpf(acc[i / 4][i % 4], e[g]);
-                    add_columns<ACT>(a, row0 + 16 * g + col, c0 + 8 * kq, add);
+                        for (int i = 0; i < 8; ++i) add[i] = ldexpf(acc[i / 4][i % 4], e[g]);
+                        store_columns<ACT>(a, row0 + 16 * g + col, n0 + 32 * (c + p) + 8 * kq, yv[p][g], add);
+                    }
                 }
             }
         }
@@ -326,7 +351,7 @@ __global__ __launch_bounds__(256) void lora_expand_rows_kernel(LoraArgs a, int s
         if (index[g] >= 0 || row >= a.m || a.out == a.y) continue;
         const float none[8] = {0, 0, 0, 0, 0, 0, 0, 0};
         for (int c = 0; c < kTileGroups; ++c)
-            if (n0 + 32 * c + 8 * kq < a.n) add_columns<ACT>(a, row, n0 + 32 * c + 8 * kq, none);
+            store_columns<ACT>(a, row, n0 + 32 * c + 8 * kq, load_columns(a, row, n0 + 32 * c + 8 * kq), none);
     }
 }
 
