@@ -70,6 +70,20 @@ def test_lora_add(dev, case, scaled):
     assert got is yd and torch.equal(yd, out), "in place"
 
 
+# enough rows and columns for the tiles of 64 rows
+LARGE = [
+    (1100, 16901, 72, 5, 24, 70, "bf16"),
+    (2111, 8200, 264, 7, 128, 300, "f16"),
+    (1024, 16384, 40, 9, 64, 1, "bf16"),
+    (4100, 4097, 8, 3, 8, 1000, "f16"),
+]
+
+
+@pytest.mark.parametrize("case", LARGE, ids=["m%d_n%d_k%d_l%d_r%d_run%d_%s" % c for c in LARGE])
+def test_lora_add_large(dev, case):
+    test_lora_add(dev, case, True)
+
+
 def test_lora_strided_rows(dev):
     say("lora on slices")
     lib = w4()

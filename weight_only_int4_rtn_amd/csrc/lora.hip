@@ -45,15 +45,69 @@ struct Distinct {
     }
 };
 
-constexpr int kWaves = 4;
+// One row's t (this lane's channels of it) as MFMA operands: a high and a low
+// 16-bit part (16 or more significant bits in all), scaled by 2^-e so that f16
+// neither overflows nor loses bits.  Returns e.
+template <int ACT, int RS>  // RS: 32-wide steps of the rank
+__device__ inline int operands_of(const float (&v)[RS][8], uint4 (&hi)[RS], uint4 (&lo)[RS]) {
+    float big = 0.0f;
+#pragma unroll
+    for (int s = 0; s < RS; ++s)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) big = fmaxf(big, fabsf(v[s][i]));
+    big = max_xor32(fmaxf(big, lane_xor<16>(big)));
+    const int e = big > 0.0f && big < 3e38f ? int(__float_as_uint(big) >> 23) - 127 : 0;
+#pragma unroll
+    for (int s = 0; s < RS; ++s) {
+        uint32_t h[4], w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float p = ldexpf(v[s][2 * i], -e), q = ldexpf(v[s][2 * i + 1], -e);
+            const uint16_t ph = from_f32<ACT>(p), qh = from_f32<ACT>(q);
+            h[i] = uint32_t(ph) | (uint32_t(qh) << 16);
+            w[i] = uint32_t(from_f32<ACT>(p - to_f32<ACT>(ph))) | (uint32_t(from_f32<ACT>(q - to_f32<ACT>(qh))) << 16);
+        }
+        hi[s] = make_uint4(h[0], h[1], h[2], h[3]);
+        lo[s] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    return e;
+}
+
+// The same of a row's sums in the workspace (their parts added, times the adapter's scale).
+template <int ACT, int RS>
+__device__ inline int row_operand(const LoraArgs& a, const float* t, int splits, int64_t row, bool mine, float scale, int kq,
+                                  uint4 (&hi)[RS], uint4 (&lo)[RS]) {
+    float v[RS][8];
+#pragma unroll
+    for (int s = 0; s < RS; ++s) {
+        const int r = 32 * s + 8 * kq;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[s][i] = 0.0f;
+        if (mine && r < a.rank) {
+            for (int p = 0; p < splits; ++p) {
+                const float4* src = reinterpret_cast<const float4*>(t + (int64_t(p) * a.m + row) * a.rank + r);
+                const float4 x = src[0], y = src[1];
+                v[s][0] += x.x; v[s][1] += x.y; v[s][2] += x.z; v[s][3] += x.w;
+                v[s][4] += y.x; v[s][5] += y.y; v[s][6] += y.z; v[s][7] += y.w;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[s][i] *= scale;
+    }
+    return operands_of<ACT, RS>(v, hi, lo);
+}
+
 
 // t[split][row][r] = sum over the split's columns of x[row] A_l[r].
 // Grid: x = row tile, y = slot, z = split.  The waves take 32-column steps in
 // turn and add up in LDS.
-template <int ACT, int RT>  // RT: 16-row tiles of the rank
-__global__ __launch_bounds__(256) void lora_shrink_kernel(LoraArgs a, int slots, int kspan, float* t) {
-    constexpr int UN = RT >= 8 ? 2 : 4;
-    __shared__ float lds[kWaves][RT * 4][64];
+//
+// OPERANDS (one split): instead of sums, the rows' operands for the second
+// launch (operands_of): [row tile][32-wide step of the rank][high, low][lane].
+template <int ACT, int RT, bool OPERANDS>  // RT: 16-row tiles of the rank
+__global__ __launch_bounds__(OPERANDS ? 512 : 256) void lora_shrink_kernel(LoraArgs a, int slots, int kspan, float* t, uint4* operands, float* factors) {
+    constexpr int UN = RT >= 8 ? 2 : 4, WAVES = OPERANDS ? 8 : 4;
+    __shared__ float lds[WAVES][RT * 4][64];
     const int lane = threadIdx.x % 64, wave = uniform(threadIdx.x / 64);
     const int col = lane % 16, kq = lane / 16;
     const int64_t row0 = int64_t(blockIdx.x) * 16;
@@ -76,7 +130,7 @@ __global__ __launch_bounds__(256) void lora_shrink_kernel(LoraArgs a, int slots,
         // A wave takes runs of 32 UN columns in turn, all of a run's loads in
         // flight together; of the last run the columns that exist (K is a
         // multiple of 8: a lane's 8 columns are inside or outside together).
-        for (int64_t k = k0 + 32 * UN * wave; k < k1; k += 32 * UN * kWaves) {
+        for (int64_t k = k0 + 32 * UN * wave; k < k1; k += 32 * UN * WAVES) {
             if (k + 32 * UN <= k1) {
                 uint4 xv[UN], av[UN][RT];
 #pragma unroll
@@ -109,102 +163,83 @@ __global__ __launch_bounds__(256) void lora_shrink_kernel(LoraArgs a, int slots,
 #pragma unroll
             for (int j = 0; j < 4; ++j) lds[wave][4 * i + j][lane] = acc[i][j];
         __syncthreads();
-        // wave w adds and stores the rank tiles w, w + 4, ..
-        for (int i = wave; i < RT; i += kWaves) {
-            float s[4];
+        if constexpr (OPERANDS) {
+            if (wave == 0) {
+                constexpr int RS = (RT + 1) / 2;
+                const float scale = a.scales ? a.scales[l] : 1.0f;
+                float v[RS][8];
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                s[j] = lds[0][4 * i + j][lane] + lds[1][4 * i + j][lane] + lds[2][4 * i + j][lane] + lds[3][4 * i + j][lane];
-            const int r = 16 * i + 4 * kq;
-            if (d.mine == l && row0 + col < a.m && r < a.rank)
-                *reinterpret_cast<float4*>(t + (int64_t(blockIdx.z) * a.m + row0 + col) * a.rank + r) = make_float4(s[0], s[1], s[2], s[3]);
+                for (int s = 0; s < RS; ++s)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        // rank index 32 s + 8 kq + i: rank tile 2 s + kq / 2, quarter 2 (kq % 2) + i / 4 of its rows
+                        const int tile = 2 * s + kq / 2, from = (2 * (kq % 2) + i / 4) * 16 + col;
+                        float x = 0.0f;
+                        if (tile < RT && 32 * s + 8 * kq < a.rank) {
+#pragma unroll
+                            for (int w = 0; w < WAVES; ++w) x += lds[w][4 * tile + i % 4][from];
+                        }
+                        v[s][i] = x * scale;
+                    }
+                uint4 hi[RS], lo[RS];
+                const int e = operands_of<ACT, RS>(v, hi, lo);
+                if (d.mine == l && row0 + col < a.m) {
+                    uint4* to = operands + int64_t(blockIdx.x) * RS * 128 + lane;
+#pragma unroll
+                    for (int s = 0; s < RS; ++s) {
+                        to[(2 * s) * 64] = hi[s];
+                        to[(2 * s + 1) * 64] = lo[s];
+                    }
+                    if (kq == 0) factors[row0 + col] = ldexpf(1.0f, e);
+                }
+            }
+        } else {
+            // wave w adds and stores the rank tiles w, w + 4, ..
+            for (int i = wave; i < RT; i += WAVES) {
+                float s[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    s[j] = lds[0][4 * i + j][lane] + lds[1][4 * i + j][lane] + lds[2][4 * i + j][lane] + lds[3][4 * i + j][lane];
+                const int r = 16 * i + 4 * kq;
+                if (d.mine == l && row0 + col < a.m && r < a.rank)
+                    *reinterpret_cast<float4*>(t + (int64_t(blockIdx.z) * a.m + row0 + col) * a.rank + r) = make_float4(s[0], s[1], s[2], s[3]);
+            }
         }
         __syncthreads();
     }
-}
-
-// One row's t (its parts added, times the adapter's scale) as MFMA operands: a
-// high and a low 16-bit part (16 or more significant bits in all), scaled by
-// 2^-e so that f16 neither overflows nor loses bits.  Returns e.
-template <int ACT, int RS>  // RS: 32-wide steps of the rank
-__device__ inline int row_operand(const LoraArgs& a, const float* t, int splits, int64_t row, bool mine, float scale, int kq,
-                                  uint4 (&hi)[RS], uint4 (&lo)[RS]) {
-    float v[RS][8];
-    float big = 0.0f;
-#pragma unroll
-    for (int s = 0; s < RS; ++s) {
-        const int r = 32 * s + 8 * kq;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[s][i] = 0.0f;
-        if (mine && r < a.rank) {
-            for (int p = 0; p < splits; ++p) {
-                const float4* src = reinterpret_cast<const float4*>(t + (int64_t(p) * a.m + row) * a.rank + r);
-                const float4 x = src[0], y = src[1];
-                v[s][0] += x.x; v[s][1] += x.y; v[s][2] += x.z; v[s][3] += x.w;
-                v[s][4] += y.x; v[s][5] += y.y; v[s][6] += y.z; v[s][7] += y.w;
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            v[s][i] *= scale;
-            big = fmaxf(big, fabsf(v[s][i]));
-        }
-    }
-    big = max_xor32(fmaxf(big, lane_xor<16>(big)));
-    const int e = big > 0.0f && big < 3e38f ? int(__float_as_uint(big) >> 23) - 127 : 0;
-#pragma unroll
-    for (int s = 0; s < RS; ++s) {
-        uint32_t h[4], w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float p = ldexpf(v[s][2 * i], -e), q = ldexpf(v[s][2 * i + 1], -e);
-            const uint16_t ph = from_f32<ACT>(p), qh = from_f32<ACT>(q);
-            h[i] = uint32_t(ph) | (uint32_t(qh) << 16);
-            w[i] = uint32_t(from_f32<ACT>(p - to_f32<ACT>(ph))) | (uint32_t(from_f32<ACT>(q - to_f32<ACT>(qh))) << 16);
-        }
-        hi[s] = make_uint4(h[0], h[1], h[2], h[3]);
-        lo[s] = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-    return e;
 }
 
 // MFMA row `col` of half h of a 32-column group: columns interleave so that a
 // lane's two times four results are 8 consecutive columns.
 __device__ inline int column_of(int col, int h) { return 8 * (col / 4) + 4 * h + col % 4; }
 
-// y and out on 8 columns from n on, as far as they exist; 16 bytes at once where
-// all do and both sides are aligned.
-__device__ inline bool whole_columns(const LoraArgs& a, int64_t n) {
-    return n + 8 <= a.n && a.ldy % 8 == 0 && a.ldo % 8 == 0 &&
-           ((reinterpret_cast<uintptr_t>(a.y) | reinterpret_cast<uintptr_t>(a.out)) & 15) == 0;
-}
-
-__device__ inline uint4 load_columns(const LoraArgs& a, int64_t row, int64_t n) {
-    const uint16_t* src = a.y + row * a.ldy + n;
-    if (whole_columns(a, n)) return *reinterpret_cast<const uint4*>(src);
+// 8 columns of a row, of which `left` (any number) exist.
+__device__ inline uint4 load_columns(const uint16_t* src, int64_t left) {
     uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-        if (n + i < a.n) w[i / 2] |= uint32_t(src[i]) << (16 * (i % 2));
+        if (i < left) w[i / 2] |= uint32_t(src[i]) << (16 * (i % 2));
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
+__device__ inline void store_columns(uint16_t* dst, int64_t left, uint4 v) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (i < left) dst[i] = uint16_t(w[i / 2] >> (16 * (i % 2)));
+}
 
+// y + f acc on 8 columns, rounded once
 template <int ACT>
-__device__ inline void store_columns(const LoraArgs& a, int64_t row, int64_t n, uint4 y, const float (&add)[8]) {
+__device__ inline uint4 add_columns(uint4 y, f32x4_t lo, f32x4_t hi, float f) {
     const uint32_t in[4] = {y.x, y.y, y.z, y.w};
     uint32_t o[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        o[i] = uint32_t(from_f32<ACT>(to_f32<ACT>(uint16_t(in[i])) + add[2 * i])) |
-               (uint32_t(from_f32<ACT>(to_f32<ACT>(uint16_t(in[i] >> 16)) + add[2 * i + 1])) << 16);
-    uint16_t* dst = a.out + row * a.ldo + n;
-    if (whole_columns(a, n)) {
-        *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (n + i < a.n) dst[i] = uint16_t(o[i / 2] >> (16 * (i % 2)));
+    for (int i = 0; i < 4; ++i) {
+        const float p = i < 2 ? lo[2 * i] : hi[2 * i - 4], q = i < 2 ? lo[2 * i + 1] : hi[2 * i - 3];
+        o[i] = uint32_t(from_f32<ACT>(fmaf(p, f, to_f32<ACT>(uint16_t(in[i]))))) |
+               (uint32_t(from_f32<ACT>(fmaf(q, f, to_f32<ACT>(uint16_t(in[i] >> 16))))) << 16);
     }
+    return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 // Few rows: out[row] = y[row] + scale t[row] B_l^T.  Grid: x = 256 columns, y =
@@ -219,11 +254,10 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(LoraArgs a, int slots,
     Distinct<16> d(a.index, row0, a.m, a.adapters, lane);
     const int64_t row = row0 + col;
     const bool real = row < a.m;
-    float add[2][8];
+    f32x4_t add[2][2];
+    float f = 0.0f;
 #pragma unroll
-    for (int g = 0; g < 2; ++g)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) add[g][i] = 0.0f;
+    for (int g = 0; g < 2; ++g) add[g][0] = add[g][1] = f32x4_t{0, 0, 0, 0};
     // rows without an adapter are copied by the first slot
     bool write = real && d.mine < 0 && blockIdx.z == 0;
     for (int seen = 0; d.left; ++seen) {
@@ -259,56 +293,82 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(LoraArgs a, int slots,
                 }
             }
             if (mine) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) add[g][i] = ldexpf(acc[i / 4][i % 4], e);
+                add[g][0] = acc[0];
+                add[g][1] = acc[1];
+                f = ldexpf(1.0f, e);
             }
         }
     }
     if (!write) return;
+    const bool aligned = a.ldy % 8 == 0 && a.ldo % 8 == 0 && ((reinterpret_cast<uintptr_t>(a.y) | reinterpret_cast<uintptr_t>(a.out)) & 15) == 0;
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
         const int64_t n = n0 + 32 * g + 8 * kq;
-        store_columns<ACT>(a, row, n, load_columns(a, row, n), add[g]);
+        const uint16_t* src = a.y + row * a.ldy + n;
+        uint16_t* dst = a.out + row * a.ldo + n;
+        if (aligned && n + 8 <= a.n) *reinterpret_cast<uint4*>(dst) = add_columns<ACT>(*reinterpret_cast<const uint4*>(src), add[g][0], add[g][1], f);
+        else store_columns(dst, a.n - n, add_columns<ACT>(load_columns(src, a.n - n), add[g][0], add[g][1], f));
     }
 }
 
-// Many rows.  Grid: x = 512 columns, y = tile of 64 rows.  A wave takes 128
-// columns of all 64 rows, so each operand of B serves four products and t is
-// turned into operands once for four groups of columns.  A tile's adapters are
-// taken one after another, each reading and writing the rows that are its own.
-constexpr int kTileCols = 512, kTileGroups = 4;
+// Many rows.  Grid: x = kTileCols columns, y = tile of 64 rows.  A wave takes a
+// quarter of the columns of all 64 rows, 64 at a time (a row's line of 128
+// bytes is read and written in one go), so each operand of B serves four
+// products; t comes as operands.  A tile's adapters are taken one after another,
+// each reading and writing the rows that are its own.
+constexpr int kTileCols = 512;
 
 template <int ACT, int RS>
-__global__ __launch_bounds__(256) void lora_expand_rows_kernel(LoraArgs a, int splits, const float* t) {
+__global__ __launch_bounds__(256) void lora_expand_rows_kernel(LoraArgs a, const uint4* operands, const float* factors) {
+    constexpr int PAIR = RS > 2 ? 1 : 2;  // groups of 32 columns at a time, as registers go
     const int lane = threadIdx.x % 64, wave = uniform(threadIdx.x / 64);
     const int col = lane % 16, kq = lane / 16;
     const int64_t row0 = int64_t(blockIdx.y) * 64;
-    const int64_t n0 = int64_t(blockIdx.x) * kTileCols + 32 * kTileGroups * wave;
+    const int64_t n0 = int64_t(blockIdx.x) * kTileCols + kTileCols / 4 * wave;
     if (n0 >= a.n) return;
+    const int64_t n1 = n0 + kTileCols / 4 < a.n ? n0 + kTileCols / 4 : a.n;
     Distinct<64> d(a.index, row0, a.m, a.adapters, lane);
-    constexpr int PAIR = RS > 2 ? 1 : 2;
     int index[4];  // of this lane's row in each group of 16
+    const uint16_t* src[4];
+    uint16_t* dst[4];
 #pragma unroll
-    for (int g = 0; g < 4; ++g) index[g] = __shfl(d.mine, 16 * g + col);
+    for (int g = 0; g < 4; ++g) {
+        index[g] = __shfl(d.mine, 16 * g + col);
+        const int64_t row = row0 + 16 * g + col < a.m ? row0 + 16 * g + col : a.m - 1;
+        src[g] = a.y + row * a.ldy + 8 * kq;
+        dst[g] = a.out + row * a.ldo + 8 * kq;
+    }
+    const bool aligned = a.ldy % 8 == 0 && a.ldo % 8 == 0 && ((reinterpret_cast<uintptr_t>(a.y) | reinterpret_cast<uintptr_t>(a.out)) & 15) == 0;
     while (d.left) {
         const int l = d.next();
-        const float scale = a.scales ? a.scales[l] : 1.0f;
         uint4 hi[4][RS], lo[4][RS];
-        int e[4];
+        float f[4];
 #pragma unroll
-        for (int g = 0; g < 4; ++g)
-            e[g] = row_operand<ACT, RS>(a, t, splits, row0 + 16 * g + col, index[g] == l, scale, kq, hi[g], lo[g]);
-        // 64 columns at a time: a row's line of 128 bytes is read and written in one go
+        for (int g = 0; g < 4; ++g) {
+            f[g] = 0.0f;
+#pragma unroll
+            for (int s = 0; s < RS; ++s) hi[g][s] = lo[g][s] = make_uint4(0, 0, 0, 0);
+            if (index[g] == l) {
+                const uint4* from = operands + (int64_t(blockIdx.y) * 4 + g) * RS * 128 + lane;
+                f[g] = factors[row0 + 16 * g + col];
+#pragma unroll
+                for (int s = 0; s < RS; ++s) {
+                    hi[g][s] = from[(2 * s) * 64];
+                    lo[g][s] = from[(2 * s + 1) * 64];
+                }
+            }
+        }
+        const uint16_t* b = a.b + int64_t(l) * a.n * a.rank + 8 * kq;
 #pragma unroll 1
-        for (int c = 0; c < kTileGroups; c += PAIR) {
+        for (int64_t c0 = n0; c0 < n1; c0 += 32 * PAIR) {
+            const bool whole = aligned && c0 + 32 * PAIR <= a.n;
             uint4 bv[PAIR][2][RS], yv[PAIR][4];
 #pragma unroll
             for (int p = 0; p < PAIR; ++p) {
-                const int64_t c0 = n0 + 32 * (c + p);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const int64_t n = c0 + column_of(col, h);
-                    const uint16_t* br = a.b + (int64_t(l) * a.n + (n < a.n ? n : a.n - 1)) * a.rank + 8 * kq;
+                    const int64_t n = c0 + 32 * p + column_of(col, h);
+                    const uint16_t* br = b + (n < a.n ? n : a.n - 1) * a.rank;
 #pragma unroll
                     for (int s = 0; s < RS; ++s) {
                         bv[p][h][s] = make_uint4(0, 0, 0, 0);
@@ -317,7 +377,9 @@ __global__ __launch_bounds__(256) void lora_expand_rows_kernel(LoraArgs a, int s
                 }
 #pragma unroll
                 for (int g = 0; g < 4; ++g)
-                    if (index[g] == l) yv[p][g] = load_columns(a, row0 + 16 * g + col, c0 + 8 * kq);
+                    if (index[g] == l)
+                        yv[p][g] = whole ? *reinterpret_cast<const uint4*>(src[g] + c0 + 32 * p)
+                                         : load_columns(src[g] + c0 + 32 * p, a.n - (c0 + 32 * p + 8 * kq));
             }
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
@@ -335,10 +397,9 @@ __global__ __launch_bounds__(256) void lora_expand_rows_kernel(LoraArgs a, int s
                         }
                     }
                     if (index[g] == l) {
-                        float add[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) add[i] = ldexpf(acc[i / 4][i % 4], e[g]);
-                        store_columns<ACT>(a, row0 + 16 * g + col, n0 + 32 * (c + p) + 8 * kq, yv[p][g], add);
+                        const uint4 o = add_columns<ACT>(yv[p][g], acc[0], acc[1], f[g]);
+                        if (whole) *reinterpret_cast<uint4*>(dst[g] + c0 + 32 * p) = o;
+                        else store_columns(dst[g] + c0 + 32 * p, a.n - (c0 + 32 * p + 8 * kq), o);
                     }
                 }
             }
@@ -347,11 +408,11 @@ __global__ __launch_bounds__(256) void lora_expand_rows_kernel(LoraArgs a, int s
     // rows without an adapter
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
-        const int64_t row = row0 + 16 * g + col;
-        if (index[g] >= 0 || row >= a.m || a.out == a.y) continue;
-        const float none[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        for (int c = 0; c < kTileGroups; ++c)
-            store_columns<ACT>(a, row, n0 + 32 * c + 8 * kq, load_columns(a, row, n0 + 32 * c + 8 * kq), none);
+        if (index[g] >= 0 || row0 + 16 * g + col >= a.m || a.out == a.y) continue;
+        for (int64_t c0 = n0; c0 < n1; c0 += 32) {
+            if (aligned && c0 + 32 <= a.n) *reinterpret_cast<uint4*>(dst[g] + c0) = *reinterpret_cast<const uint4*>(src[g] + c0);
+            else store_columns(dst[g] + c0, a.n - (c0 + 8 * kq), load_columns(src[g] + c0, a.n - (c0 + 8 * kq)));
+        }
     }
 }
 
@@ -359,13 +420,21 @@ template <int ACT, int RT>
 hipError_t run(const LoraArgs& a, const LoraPlan& p, hipStream_t stream) {
     float* t = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + kSyncBytes);
     const unsigned tiles = unsigned(ceil_div(a.m, 16));
-    lora_shrink_kernel<ACT, RT><<<dim3(tiles, unsigned(p.slots), unsigned(p.splits)), dim3(256), 0, stream>>>(a, p.slots, int(p.kspan), t);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    if (p.rows == 64)
-        lora_expand_rows_kernel<ACT, (RT + 1) / 2><<<dim3(unsigned(ceil_div(a.n, kTileCols)), unsigned(ceil_div(a.m, 64))), dim3(256), 0, stream>>>(a, p.splits, t);
-    else
-        lora_expand_kernel<ACT, (RT + 1) / 2><<<dim3(unsigned(ceil_div(a.n, 256)), tiles, unsigned(p.slots)), dim3(256), 0, stream>>>(a, p.slots, p.splits, t);
+    constexpr int RS = (RT + 1) / 2;
+    const dim3 grid(tiles, unsigned(p.slots), unsigned(p.splits));
+    if (p.rows == 64) {
+        uint4* operands = reinterpret_cast<uint4*>(t);
+        float* factors = reinterpret_cast<float*>(operands + int64_t(tiles) * RS * 128);
+        lora_shrink_kernel<ACT, RT, true><<<grid, dim3(512), 0, stream>>>(a, p.slots, int(p.kspan), t, operands, factors);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        lora_expand_rows_kernel<ACT, RS><<<dim3(unsigned(ceil_div(a.n, kTileCols)), unsigned(ceil_div(a.m, 64))), dim3(256), 0, stream>>>(a, operands, factors);
+    } else {
+        lora_shrink_kernel<ACT, RT, false><<<grid, dim3(256), 0, stream>>>(a, p.slots, int(p.kspan), t, nullptr, nullptr);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        lora_expand_kernel<ACT, RS><<<dim3(unsigned(ceil_div(a.n, 256)), tiles, unsigned(p.slots)), dim3(256), 0, stream>>>(a, p.slots, p.splits, t);
+    }
     return hipGetLastError();
 }
 
@@ -391,12 +460,14 @@ LoraPlan plan_lora(int64_t m, int64_t n, int64_t k, int adapters, int rank) {
     const int64_t most = m < 16 ? m : 16;
     p.slots = int(p.rows == 64 || tiles >= 64 ? 1 : most < adapters ? most : adapters);
     if (p.slots < 1) p.slots = 1;
-    int64_t splits = ceil_div(512, tiles * p.slots);
+    int64_t splits = p.rows == 64 ? 1 : ceil_div(512, tiles * p.slots);
     if (splits > ceil_div(k, 512)) splits = ceil_div(k, 512);
     if (splits > 16) splits = 16;
     p.kspan = ceil_div(ceil_div(k, splits), 32) * 32;
     p.splits = int(ceil_div(k, p.kspan));
-    p.workspace = size_t(p.splits) * size_t(m) * size_t(rank) * 4;
+    // sums [split][row][rank], or operands (2 KB a row tile and 32-wide step of the rank) and a factor a row
+    p.workspace = p.rows == 64 ? size_t(tiles) * (size_t(rank <= 32 ? 1 : rank <= 64 ? 2 : 4) * 2048 + 64)
+                               : size_t(p.splits) * size_t(m) * size_t(rank) * 4;
     return p;
 }
 
