@@ -26,7 +26,7 @@ __device__ inline f32x4_t mfma16(uint4 a, uint4 b, f32x4_t c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, a), __builtin_bit_cast(f16x8_t, b), c, 0, 0, 0);
 }
 
-// The distinct adapters among a tile's ROWS rows (16 or 64), taken one by one;
+// The distinct adapters among a tile's ROWS rows (at most 64), taken one by one;
 // lane L holds row L % ROWS's index in `mine`.
 template <int ROWS>
 struct Distinct {
@@ -36,7 +36,7 @@ struct Distinct {
         const int64_t row = row0 + lane % ROWS;
         mine = row < m ? index[row] : -1;
         if (mine >= adapters) mine = -1;
-        left = __ballot(mine >= 0) & (ROWS == 64 ? ~0ull : 0xFFFFull);
+        left = __ballot(mine >= 0) & (~0ull >> (64 - ROWS));
     }
     __device__ int next() {
         const int l = __builtin_amdgcn_readlane(mine, __ffsll((unsigned long long)left) - 1);
@@ -84,6 +84,7 @@ __device__ inline int row_operand(const LoraArgs& a, const float* t, int splits,
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[s][i] = 0.0f;
         if (mine && r < a.rank) {
+#pragma unroll 4
             for (int p = 0; p < splits; ++p) {
                 const float4* src = reinterpret_cast<const float4*>(t + (int64_t(p) * a.m + row) * a.rank + r);
                 const float4 x = src[0], y = src[1];
@@ -311,28 +312,28 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(LoraArgs a, int slots,
     }
 }
 
-// Many rows.  Grid: x = kTileCols columns, y = tile of 64 rows.  A wave takes a
+// Many rows.  Grid: x = kTallCols columns, y = tile of 64 rows.  A wave takes a
 // quarter of the columns of all 64 rows, 64 at a time (a row's line of 128
 // bytes is read and written in one go), so each operand of B serves four
 // products; t comes as operands.  A tile's adapters are taken one after another,
 // each reading and writing the rows that are its own.
-constexpr int kTileCols = 512;
+constexpr int kTallCols = 512, kTallGroups = 4, kTallRows = 16 * kTallGroups;
 
 template <int ACT, int RS>
 __global__ __launch_bounds__(256) void lora_expand_rows_kernel(LoraArgs a, const uint4* operands, const float* factors) {
     constexpr int PAIR = RS > 2 ? 1 : 2;  // groups of 32 columns at a time, as registers go
     const int lane = threadIdx.x % 64, wave = uniform(threadIdx.x / 64);
     const int col = lane % 16, kq = lane / 16;
-    const int64_t row0 = int64_t(blockIdx.y) * 64;
-    const int64_t n0 = int64_t(blockIdx.x) * kTileCols + kTileCols / 4 * wave;
+    const int64_t row0 = int64_t(blockIdx.y) * kTallRows;
+    const int64_t n0 = int64_t(blockIdx.x) * kTallCols + kTallCols / 4 * wave;
     if (n0 >= a.n) return;
-    const int64_t n1 = n0 + kTileCols / 4 < a.n ? n0 + kTileCols / 4 : a.n;
-    Distinct<64> d(a.index, row0, a.m, a.adapters, lane);
-    int index[4];  // of this lane's row in each group of 16
-    const uint16_t* src[4];
-    uint16_t* dst[4];
+    const int64_t n1 = n0 + kTallCols / 4 < a.n ? n0 + kTallCols / 4 : a.n;
+    Distinct<kTallRows> d(a.index, row0, a.m, a.adapters, lane);
+    int index[kTallGroups];  // of this lane's row in each group of 16
+    const uint16_t* src[kTallGroups];
+    uint16_t* dst[kTallGroups];
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
+    for (int g = 0; g < kTallGroups; ++g) {
         index[g] = __shfl(d.mine, 16 * g + col);
         const int64_t row = row0 + 16 * g + col < a.m ? row0 + 16 * g + col : a.m - 1;
         src[g] = a.y + row * a.ldy + 8 * kq;
@@ -341,15 +342,15 @@ __global__ __launch_bounds__(256) void lora_expand_rows_kernel(LoraArgs a, const
     const bool aligned = a.ldy % 8 == 0 && a.ldo % 8 == 0 && ((reinterpret_cast<uintptr_t>(a.y) | reinterpret_cast<uintptr_t>(a.out)) & 15) == 0;
     while (d.left) {
         const int l = d.next();
-        uint4 hi[4][RS], lo[4][RS];
-        float f[4];
+        uint4 hi[kTallGroups][RS], lo[kTallGroups][RS];
+        float f[kTallGroups];
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
+        for (int g = 0; g < kTallGroups; ++g) {
             f[g] = 0.0f;
 #pragma unroll
             for (int s = 0; s < RS; ++s) hi[g][s] = lo[g][s] = make_uint4(0, 0, 0, 0);
             if (index[g] == l) {
-                const uint4* from = operands + (int64_t(blockIdx.y) * 4 + g) * RS * 128 + lane;
+                const uint4* from = operands + (int64_t(blockIdx.y) * kTallGroups + g) * RS * 128 + lane;
                 f[g] = factors[row0 + 16 * g + col];
 #pragma unroll
                 for (int s = 0; s < RS; ++s) {
@@ -362,7 +363,7 @@ __global__ __launch_bounds__(256) void lora_expand_rows_kernel(LoraArgs a, const
 #pragma unroll 1
         for (int64_t c0 = n0; c0 < n1; c0 += 32 * PAIR) {
             const bool whole = aligned && c0 + 32 * PAIR <= a.n;
-            uint4 bv[PAIR][2][RS], yv[PAIR][4];
+            uint4 bv[PAIR][2][RS], yv[PAIR][kTallGroups];
 #pragma unroll
             for (int p = 0; p < PAIR; ++p) {
 #pragma unroll
@@ -376,13 +377,13 @@ __global__ __launch_bounds__(256) void lora_expand_rows_kernel(LoraArgs a, const
                     }
                 }
 #pragma unroll
-                for (int g = 0; g < 4; ++g)
+                for (int g = 0; g < kTallGroups; ++g)
                     if (index[g] == l)
                         yv[p][g] = whole ? *reinterpret_cast<const uint4*>(src[g] + c0 + 32 * p)
                                          : load_columns(src[g] + c0 + 32 * p, a.n - (c0 + 32 * p + 8 * kq));
             }
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
+            for (int g = 0; g < kTallGroups; ++g) {
                 if (!__any(index[g] == l)) continue;
 #pragma unroll
                 for (int p = 0; p < PAIR; ++p) {
@@ -407,7 +408,7 @@ __global__ __launch_bounds__(256) void lora_expand_rows_kernel(LoraArgs a, const
     }
     // rows without an adapter
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
+    for (int g = 0; g < kTallGroups; ++g) {
         if (index[g] >= 0 || row0 + 16 * g + col >= a.m || a.out == a.y) continue;
         for (int64_t c0 = n0; c0 < n1; c0 += 32) {
             if (aligned && c0 + 32 <= a.n) *reinterpret_cast<uint4*>(dst[g] + c0) = *reinterpret_cast<const uint4*>(src[g] + c0);
@@ -422,13 +423,13 @@ hipError_t run(const LoraArgs& a, const LoraPlan& p, hipStream_t stream) {
     const unsigned tiles = unsigned(ceil_div(a.m, 16));
     constexpr int RS = (RT + 1) / 2;
     const dim3 grid(tiles, unsigned(p.slots), unsigned(p.splits));
-    if (p.rows == 64) {
+    if (p.rows > 16) {
         uint4* operands = reinterpret_cast<uint4*>(t);
         float* factors = reinterpret_cast<float*>(operands + int64_t(tiles) * RS * 128);
         lora_shrink_kernel<ACT, RT, true><<<grid, dim3(512), 0, stream>>>(a, p.slots, int(p.kspan), t, operands, factors);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
-        lora_expand_rows_kernel<ACT, RS><<<dim3(unsigned(ceil_div(a.n, kTileCols)), unsigned(ceil_div(a.m, 64))), dim3(256), 0, stream>>>(a, operands, factors);
+        lora_expand_rows_kernel<ACT, RS><<<dim3(unsigned(ceil_div(a.n, kTallCols)), unsigned(ceil_div(a.m, kTallRows))), dim3(256), 0, stream>>>(a, operands, factors);
     } else {
         lora_shrink_kernel<ACT, RT, false><<<grid, dim3(256), 0, stream>>>(a, p.slots, int(p.kspan), t, nullptr, nullptr);
         const hipError_t e = hipGetLastError();
@@ -455,18 +456,20 @@ LoraPlan plan_lora(int64_t m, int64_t n, int64_t k, int adapters, int rank) {
     LoraPlan p{};
     if (m > kMaxRows) m = kMaxRows;
     // rows of the second launch's tiles: 64 once those fill the chip twice over
-    p.rows = ceil_div(m, 64) * ceil_div(n, kTileCols) >= 512 ? 64 : 16;
+    p.rows = ceil_div(m, kTallRows) * ceil_div(n, kTallCols) >= 512 ? kTallRows : 16;
     const int64_t tiles = ceil_div(m, 16);
     const int64_t most = m < 16 ? m : 16;
-    p.slots = int(p.rows == 64 || tiles >= 64 ? 1 : most < adapters ? most : adapters);
+    // many tiles: a tile seldom holds more than the end of one request and the start of the next
+    const int64_t share = p.rows > 16 ? 2 : tiles >= 64 ? 1 : most;
+    p.slots = int(share < adapters ? share : adapters);
     if (p.slots < 1) p.slots = 1;
-    int64_t splits = p.rows == 64 ? 1 : ceil_div(512, tiles * p.slots);
+    int64_t splits = p.rows > 16 ? 1 : ceil_div(512, tiles * p.slots);
     if (splits > ceil_div(k, 512)) splits = ceil_div(k, 512);
     if (splits > 16) splits = 16;
     p.kspan = ceil_div(ceil_div(k, splits), 32) * 32;
     p.splits = int(ceil_div(k, p.kspan));
     // sums [split][row][rank], or operands (2 KB a row tile and 32-wide step of the rank) and a factor a row
-    p.workspace = p.rows == 64 ? size_t(tiles) * (size_t(rank <= 32 ? 1 : rank <= 64 ? 2 : 4) * 2048 + 64)
+    p.workspace = p.rows > 16 ? size_t(tiles) * (size_t(rank <= 32 ? 1 : rank <= 64 ? 2 : 4) * 2048 + 64)
                                : size_t(p.splits) * size_t(m) * size_t(rank) * 4;
     return p;
 }
