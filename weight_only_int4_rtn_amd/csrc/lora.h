@@ -24,7 +24,8 @@ struct LoraArgs {
 };
 
 struct LoraPlan {
-    int rows;          // rows of the second launch's tiles (16 or 64)
+    bool tall;         // many rows: the second launch takes tiles of 64 rows by 512 columns
+    int tile;          // rows of the first launch's tiles (few rows: of both)
     int slots;         // workgroups that share a row tile's distinct adapters
     int splits;        // parts of K
     int64_t kspan;     // columns of one part (a multiple of 32 except the last)

@@ -38,12 +38,29 @@ struct Distinct {
         if (mine >= adapters) mine = -1;
         left = __ballot(mine >= 0) & (~0ull >> (64 - ROWS));
     }
-    __device__ int next() {
+    // the next adapter, and its rows (a bit each)
+    __device__ int next(uint64_t& rows) {
         const int l = __builtin_amdgcn_readlane(mine, __ffsll((unsigned long long)left) - 1);
-        left &= ~__ballot(mine == l);
+        rows = __ballot(mine == l) & left;
+        left &= ~rows;
         return l;
     }
 };
+
+// Position of the n-th set bit (n from 0; any position if there are not so many).
+__device__ inline int nth_bit(uint64_t mask, int n) {
+    int at = 0;
+#pragma unroll
+    for (int w = 32; w > 0; w /= 2) {
+        const uint64_t low = mask & ((uint64_t(1) << w) - 1);
+        const int have = __popcll(low);
+        const bool up = n >= have;
+        at += up ? w : 0;
+        n -= up ? have : 0;
+        mask = up ? mask >> w : low;
+    }
+    return at;
+}
 
 // One row's t (this lane's channels of it) as MFMA operands: a high and a low
 // 16-bit part (16 or more significant bits in all), scaled by 2^-e so that f16
@@ -100,113 +117,122 @@ __device__ inline int row_operand(const LoraArgs& a, const float* t, int splits,
 
 
 // t[split][row][r] = sum over the split's columns of x[row] A_l[r].
-// Grid: x = row tile, y = slot, z = split.  The waves take 32-column steps in
-// turn and add up in LDS.
+// Grid: x = tile of TILE rows, y = slot, z = split.  An adapter's rows are
+// gathered, 16 to a product, so its weights are read once a tile wherever its
+// rows stand.  The waves take runs of columns in turn and add up in LDS.
 //
-// OPERANDS (one split): instead of sums, the rows' operands for the second
-// launch (operands_of): [row tile][32-wide step of the rank][high, low][lane].
-template <int ACT, int RT, bool OPERANDS>  // RT: 16-row tiles of the rank
+// OPERANDS (one split, tiles of 16 rows in place): instead of sums, the rows'
+// operands for the second launch (operands_of): [row tile][32-wide step of the
+// rank][high, low][lane].
+template <int ACT, int RT, int TILE, bool OPERANDS>  // RT: 16-row tiles of the rank
 __global__ __launch_bounds__(OPERANDS ? 512 : 256) void lora_shrink_kernel(LoraArgs a, int slots, int kspan, float* t, uint4* operands, float* factors) {
-    constexpr int UN = RT >= 8 ? 2 : 4, WAVES = OPERANDS ? 8 : 4;
-    __shared__ float lds[WAVES][RT * 4][64];
+    constexpr int UN = RT >= 8 ? 2 : 4, WAVES = OPERANDS ? 8 : 4, THREADS = 64 * WAVES;
+    __shared__ float lds[WAVES][RT * 4 * 64];
     const int lane = threadIdx.x % 64, wave = uniform(threadIdx.x / 64);
     const int col = lane % 16, kq = lane / 16;
-    const int64_t row0 = int64_t(blockIdx.x) * 16;
-    Distinct<16> d(a.index, row0, a.m, a.adapters, lane);
+    const int64_t row0 = int64_t(blockIdx.x) * TILE;
+    Distinct<TILE> d(a.index, row0, a.m, a.adapters, lane);
     const int64_t k0 = int64_t(blockIdx.z) * kspan, k1 = k0 + kspan < a.k ? k0 + kspan : a.k;
-    const int64_t row = row0 + col < a.m ? row0 + col : a.m - 1;
-    const uint16_t* xr = a.x + row * a.ldx + 8 * kq;
     for (int seen = 0; d.left; ++seen) {
-        const int l = d.next();
+        uint64_t rows;
+        const int l = d.next(rows);
         if (seen % slots != int(blockIdx.y)) continue;
+        const float scale = OPERANDS && a.scales ? a.scales[l] : 1.0f;
         const uint16_t* ar[RT];
 #pragma unroll
         for (int i = 0; i < RT; ++i) {
             const int r = min(16 * i + col, a.rank - 1);
             ar[i] = a.a + (int64_t(l) * a.rank + r) * a.k + 8 * kq;
         }
-        f32x4_t acc[RT];
+        const int count = __popcll(rows);
+        for (int first = 0; first < (OPERANDS ? 1 : count); first += 16) {
+            const bool mine = OPERANDS ? (rows >> col & 1) : first + col < count;
+            const int at = OPERANDS ? col : nth_bit(rows, mine ? first + col : first);
+            const int64_t row = row0 + at < a.m ? row0 + at : a.m - 1;
+            const uint16_t* xr = a.x + row * a.ldx + 8 * kq;
+            f32x4_t acc[RT];
 #pragma unroll
-        for (int i = 0; i < RT; ++i) acc[i] = f32x4_t{0, 0, 0, 0};
-        // A wave takes runs of 32 UN columns in turn, all of a run's loads in
-        // flight together; of the last run the columns that exist (K is a
-        // multiple of 8: a lane's 8 columns are inside or outside together).
-        for (int64_t k = k0 + 32 * UN * wave; k < k1; k += 32 * UN * WAVES) {
-            if (k + 32 * UN <= k1) {
-                uint4 xv[UN], av[UN][RT];
+            for (int i = 0; i < RT; ++i) acc[i] = f32x4_t{0, 0, 0, 0};
+            // A wave takes runs of 32 UN columns in turn, all of a run's loads in
+            // flight together; of the last run the columns that exist (K is a
+            // multiple of 8: a lane's 8 columns are inside or outside together).
+            for (int64_t k = k0 + 32 * UN * wave; k < k1; k += 32 * UN * WAVES) {
+                if (k + 32 * UN <= k1) {
+                    uint4 xv[UN], av[UN][RT];
 #pragma unroll
-                for (int n = 0; n < UN; ++n) {
-                    xv[n] = *reinterpret_cast<const uint4*>(xr + k + 32 * n);
+                    for (int n = 0; n < UN; ++n) {
+                        xv[n] = *reinterpret_cast<const uint4*>(xr + k + 32 * n);
 #pragma unroll
-                    for (int i = 0; i < RT; ++i) av[n][i] = *reinterpret_cast<const uint4*>(ar[i] + k + 32 * n);
+                        for (int i = 0; i < RT; ++i) av[n][i] = *reinterpret_cast<const uint4*>(ar[i] + k + 32 * n);
+                    }
+#pragma unroll
+                    for (int n = 0; n < UN; ++n)
+#pragma unroll
+                        for (int i = 0; i < RT; ++i) acc[i] = mfma16<ACT>(av[n][i], xv[n], acc[i]);
+                    continue;
                 }
+                for (int64_t kk = k; kk < k1; kk += 32) {
+                    uint4 xv = make_uint4(0, 0, 0, 0), av[RT];
 #pragma unroll
-                for (int n = 0; n < UN; ++n)
+                    for (int i = 0; i < RT; ++i) av[i] = xv;
+                    if (kk + 8 * kq < k1) {
+                        xv = *reinterpret_cast<const uint4*>(xr + kk);
 #pragma unroll
-                    for (int i = 0; i < RT; ++i) acc[i] = mfma16<ACT>(av[n][i], xv[n], acc[i]);
-                continue;
-            }
-            for (int64_t kk = k; kk < k1; kk += 32) {
-                uint4 xv = make_uint4(0, 0, 0, 0), av[RT];
+                        for (int i = 0; i < RT; ++i) av[i] = *reinterpret_cast<const uint4*>(ar[i] + kk);
+                    }
 #pragma unroll
-                for (int i = 0; i < RT; ++i) av[i] = xv;
-                if (kk + 8 * kq < k1) {
-                    xv = *reinterpret_cast<const uint4*>(xr + kk);
-#pragma unroll
-                    for (int i = 0; i < RT; ++i) av[i] = *reinterpret_cast<const uint4*>(ar[i] + kk);
+                    for (int i = 0; i < RT; ++i) acc[i] = mfma16<ACT>(av[i], xv, acc[i]);
                 }
-#pragma unroll
-                for (int i = 0; i < RT; ++i) acc[i] = mfma16<ACT>(av[i], xv, acc[i]);
             }
-        }
 #pragma unroll
-        for (int i = 0; i < RT; ++i)
+            for (int i = 0; i < RT; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) lds[wave][4 * i + j][lane] = acc[i][j];
-        __syncthreads();
-        if constexpr (OPERANDS) {
-            if (wave == 0) {
-                constexpr int RS = (RT + 1) / 2;
-                const float scale = a.scales ? a.scales[l] : 1.0f;
-                float v[RS][8];
+                for (int j = 0; j < 4; ++j) lds[wave][(4 * i + j) * 64 + lane] = acc[i][j];
+            __syncthreads();
+            // the waves' sums added, one value a thread at a time; place p holds component p / 64 of lane p % 64
+            for (int p = threadIdx.x; p < RT * 4 * 64; p += THREADS) {
+                float x = lds[0][p];
 #pragma unroll
-                for (int s = 0; s < RS; ++s)
+                for (int w = 1; w < WAVES; ++w) x += lds[w][p];
+                lds[0][p] = x;
+            }
+            __syncthreads();
+            if constexpr (OPERANDS) {
+                if (wave == 0) {
+                    constexpr int RS = (RT + 1) / 2;
+                    float v[RS][8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        // rank index 32 s + 8 kq + i: rank tile 2 s + kq / 2, quarter 2 (kq % 2) + i / 4 of its rows
-                        const int tile = 2 * s + kq / 2, from = (2 * (kq % 2) + i / 4) * 16 + col;
-                        float x = 0.0f;
-                        if (tile < RT && 32 * s + 8 * kq < a.rank) {
+                    for (int s = 0; s < RS; ++s)
 #pragma unroll
-                            for (int w = 0; w < WAVES; ++w) x += lds[w][4 * tile + i % 4][from];
+                        for (int i = 0; i < 8; ++i) {
+                            // rank index 32 s + 8 kq + i: rank tile 2 s + kq / 2, quarter 2 (kq % 2) + i / 4 of its rows
+                            const int tile = min(2 * s + kq / 2, RT - 1), from = (2 * (kq % 2) + i / 4) * 16 + col;
+                            const float x = lds[0][(4 * tile + i % 4) * 64 + from] * scale;
+                            v[s][i] = 32 * s + 8 * kq < a.rank ? x : 0.0f;
                         }
-                        v[s][i] = x * scale;
-                    }
-                uint4 hi[RS], lo[RS];
-                const int e = operands_of<ACT, RS>(v, hi, lo);
-                if (d.mine == l && row0 + col < a.m) {
-                    uint4* to = operands + int64_t(blockIdx.x) * RS * 128 + lane;
+                    uint4 hi[RS], lo[RS];
+                    const int e = operands_of<ACT, RS>(v, hi, lo);
+                    if (mine) {
+                        uint4* to = operands + int64_t(blockIdx.x) * RS * 128 + lane;
 #pragma unroll
-                    for (int s = 0; s < RS; ++s) {
-                        to[(2 * s) * 64] = hi[s];
-                        to[(2 * s + 1) * 64] = lo[s];
+                        for (int s = 0; s < RS; ++s) {
+                            to[(2 * s) * 64] = hi[s];
+                            to[(2 * s + 1) * 64] = lo[s];
+                        }
+                        if (kq == 0) factors[row] = ldexpf(1.0f, e);
                     }
-                    if (kq == 0) factors[row0 + col] = ldexpf(1.0f, e);
+                }
+            } else {
+                for (int i = wave; i < RT; i += WAVES) {
+                    const int r = 16 * i + 4 * kq;
+                    if (mine && r < a.rank)
+                        *reinterpret_cast<float4*>(t + (int64_t(blockIdx.z) * a.m + row) * a.rank + r) =
+                            make_float4(lds[0][(4 * i) * 64 + lane], lds[0][(4 * i + 1) * 64 + lane], lds[0][(4 * i + 2) * 64 + lane],
+                                        lds[0][(4 * i + 3) * 64 + lane]);
                 }
             }
-        } else {
-            // wave w adds and stores the rank tiles w, w + 4, ..
-            for (int i = wave; i < RT; i += WAVES) {
-                float s[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    s[j] = lds[0][4 * i + j][lane] + lds[1][4 * i + j][lane] + lds[2][4 * i + j][lane] + lds[3][4 * i + j][lane];
-                const int r = 16 * i + 4 * kq;
-                if (d.mine == l && row0 + col < a.m && r < a.rank)
-                    *reinterpret_cast<float4*>(t + (int64_t(blockIdx.z) * a.m + row0 + col) * a.rank + r) = make_float4(s[0], s[1], s[2], s[3]);
-            }
+            __syncthreads();
         }
-        __syncthreads();
     }
 }
 
@@ -244,28 +270,39 @@ __device__ inline uint4 add_columns(uint4 y, f32x4_t lo, f32x4_t hi, float f) {
 }
 
 // Few rows: out[row] = y[row] + scale t[row] B_l^T.  Grid: x = 256 columns, y =
-// tile of 16 rows, z = slot.  A wave computes 64 columns.
-template <int ACT, int RS>
+// tile of TILE rows, z = slot.  A wave computes 64 columns of an adapter's rows,
+// gathered 16 to a product; the operands of B are read once a tile.
+template <int ACT, int RS, int TILE>
 __global__ __launch_bounds__(256) void lora_expand_kernel(LoraArgs a, int slots, int splits, const float* t) {
     const int lane = threadIdx.x % 64, wave = uniform(threadIdx.x / 64);
     const int col = lane % 16, kq = lane / 16;
-    const int64_t row0 = int64_t(blockIdx.y) * 16;
+    const int64_t row0 = int64_t(blockIdx.y) * TILE;
     const int64_t n0 = int64_t(blockIdx.x) * 256 + 64 * wave;
     if (n0 >= a.n) return;
-    Distinct<16> d(a.index, row0, a.m, a.adapters, lane);
-    const int64_t row = row0 + col;
-    const bool real = row < a.m;
-    f32x4_t add[2][2];
-    float f = 0.0f;
+    Distinct<TILE> d(a.index, row0, a.m, a.adapters, lane);
+    const bool aligned = a.ldy % 8 == 0 && a.ldo % 8 == 0 && ((reinterpret_cast<uintptr_t>(a.y) | reinterpret_cast<uintptr_t>(a.out)) & 15) == 0;
+    auto add = [&](int64_t row, const f32x4_t (&acc)[2][2], float f) {
 #pragma unroll
-    for (int g = 0; g < 2; ++g) add[g][0] = add[g][1] = f32x4_t{0, 0, 0, 0};
-    // rows without an adapter are copied by the first slot
-    bool write = real && d.mine < 0 && blockIdx.z == 0;
+        for (int g = 0; g < 2; ++g) {
+            const int64_t n = n0 + 32 * g + 8 * kq;
+            const uint16_t* src = a.y + row * a.ldy + n;
+            uint16_t* dst = a.out + row * a.ldo + n;
+            if (aligned && n + 8 <= a.n) *reinterpret_cast<uint4*>(dst) = add_columns<ACT>(*reinterpret_cast<const uint4*>(src), acc[g][0], acc[g][1], f);
+            else store_columns(dst, a.n - n, add_columns<ACT>(load_columns(src, a.n - n), acc[g][0], acc[g][1], f));
+        }
+    };
+    if (blockIdx.z == 0 && a.out != a.y) {
+        // rows without an adapter are copied by the first slot
+        const uint64_t none = __ballot(d.mine < 0 && lane < TILE && row0 + lane < a.m);
+        const f32x4_t zero[2][2] = {};
+        for (int first = 0; first < __popcll(none); first += 16)
+            if (first + col < __popcll(none)) add(row0 + nth_bit(none, first + col), zero, 0.0f);
+    }
     for (int seen = 0; d.left; ++seen) {
-        const int l = d.next();
+        uint64_t rows;
+        const int l = d.next(rows);
         if (seen % slots != int(blockIdx.z)) continue;
-        const bool mine = real && d.mine == l;
-        write |= mine;
+        const float scale = a.scales ? a.scales[l] : 1.0f;
         uint4 bv[2][2][RS];
 #pragma unroll
         for (int g = 0; g < 2; ++g)
@@ -279,36 +316,26 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(LoraArgs a, int slots,
                     if (32 * s + 8 * kq < a.rank) bv[g][h][s] = *reinterpret_cast<const uint4*>(br + 32 * s);
                 }
             }
-        uint4 hi[RS], lo[RS];
-        const int e = row_operand<ACT, RS>(a, t, splits, row, mine, a.scales ? a.scales[l] : 1.0f, kq, hi, lo);
+        const int count = __popcll(rows);
+        for (int first = 0; first < count; first += 16) {
+            const bool mine = first + col < count;
+            const int64_t row = row0 + nth_bit(rows, mine ? first + col : first);
+            uint4 hi[RS], lo[RS];
+            const int e = row_operand<ACT, RS>(a, t, splits, row, mine, scale, kq, hi, lo);
+            f32x4_t acc[2][2];
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-            f32x4_t acc[2];
+            for (int g = 0; g < 2; ++g)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                acc[h] = f32x4_t{0, 0, 0, 0};
+                for (int h = 0; h < 2; ++h) {
+                    acc[g][h] = f32x4_t{0, 0, 0, 0};
 #pragma unroll
-                for (int s = 0; s < RS; ++s) {
-                    acc[h] = mfma16<ACT>(bv[g][h][s], hi[s], acc[h]);
-                    acc[h] = mfma16<ACT>(bv[g][h][s], lo[s], acc[h]);
+                    for (int s = 0; s < RS; ++s) {
+                        acc[g][h] = mfma16<ACT>(bv[g][h][s], hi[s], acc[g][h]);
+                        acc[g][h] = mfma16<ACT>(bv[g][h][s], lo[s], acc[g][h]);
+                    }
                 }
-            }
-            if (mine) {
-                add[g][0] = acc[0];
-                add[g][1] = acc[1];
-                f = ldexpf(1.0f, e);
-            }
+            if (mine) add(row, acc, ldexpf(1.0f, e));
         }
-    }
-    if (!write) return;
-    const bool aligned = a.ldy % 8 == 0 && a.ldo % 8 == 0 && ((reinterpret_cast<uintptr_t>(a.y) | reinterpret_cast<uintptr_t>(a.out)) & 15) == 0;
-#pragma unroll
-    for (int g = 0; g < 2; ++g) {
-        const int64_t n = n0 + 32 * g + 8 * kq;
-        const uint16_t* src = a.y + row * a.ldy + n;
-        uint16_t* dst = a.out + row * a.ldo + n;
-        if (aligned && n + 8 <= a.n) *reinterpret_cast<uint4*>(dst) = add_columns<ACT>(*reinterpret_cast<const uint4*>(src), add[g][0], add[g][1], f);
-        else store_columns(dst, a.n - n, add_columns<ACT>(load_columns(src, a.n - n), add[g][0], add[g][1], f));
     }
 }
 
@@ -341,7 +368,8 @@ __global__ __launch_bounds__(256) void lora_expand_rows_kernel(LoraArgs a, const
     }
     const bool aligned = a.ldy % 8 == 0 && a.ldo % 8 == 0 && ((reinterpret_cast<uintptr_t>(a.y) | reinterpret_cast<uintptr_t>(a.out)) & 15) == 0;
     while (d.left) {
-        const int l = d.next();
+        uint64_t rows;
+        const int l = d.next(rows);
         uint4 hi[kTallGroups][RS], lo[kTallGroups][RS];
         float f[kTallGroups];
 #pragma unroll
@@ -420,21 +448,25 @@ __global__ __launch_bounds__(256) void lora_expand_rows_kernel(LoraArgs a, const
 template <int ACT, int RT>
 hipError_t run(const LoraArgs& a, const LoraPlan& p, hipStream_t stream) {
     float* t = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + kSyncBytes);
-    const unsigned tiles = unsigned(ceil_div(a.m, 16));
+    const unsigned tiles = unsigned(ceil_div(a.m, p.tile));
     constexpr int RS = (RT + 1) / 2;
     const dim3 grid(tiles, unsigned(p.slots), unsigned(p.splits));
-    if (p.rows > 16) {
+    if (p.tall) {
         uint4* operands = reinterpret_cast<uint4*>(t);
         float* factors = reinterpret_cast<float*>(operands + int64_t(tiles) * RS * 128);
-        lora_shrink_kernel<ACT, RT, true><<<grid, dim3(512), 0, stream>>>(a, p.slots, int(p.kspan), t, operands, factors);
+        lora_shrink_kernel<ACT, RT, 16, true><<<grid, dim3(512), 0, stream>>>(a, p.slots, int(p.kspan), t, operands, factors);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
         lora_expand_rows_kernel<ACT, RS><<<dim3(unsigned(ceil_div(a.n, kTallCols)), unsigned(ceil_div(a.m, kTallRows))), dim3(256), 0, stream>>>(a, operands, factors);
     } else {
-        lora_shrink_kernel<ACT, RT, false><<<grid, dim3(256), 0, stream>>>(a, p.slots, int(p.kspan), t, nullptr, nullptr);
+        const bool wide = p.tile == 64;
+        if (wide) lora_shrink_kernel<ACT, RT, 64, false><<<grid, dim3(256), 0, stream>>>(a, p.slots, int(p.kspan), t, nullptr, nullptr);
+        else lora_shrink_kernel<ACT, RT, 16, false><<<grid, dim3(256), 0, stream>>>(a, p.slots, int(p.kspan), t, nullptr, nullptr);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
-        lora_expand_kernel<ACT, RS><<<dim3(unsigned(ceil_div(a.n, 256)), tiles, unsigned(p.slots)), dim3(256), 0, stream>>>(a, p.slots, p.splits, t);
+        const dim3 columns(unsigned(ceil_div(a.n, 256)), tiles, unsigned(p.slots));
+        if (wide) lora_expand_kernel<ACT, RS, 64><<<columns, dim3(256), 0, stream>>>(a, p.slots, p.splits, t);
+        else lora_expand_kernel<ACT, RS, 16><<<columns, dim3(256), 0, stream>>>(a, p.slots, p.splits, t);
     }
     return hipGetLastError();
 }
@@ -455,22 +487,29 @@ constexpr int64_t kMaxRows = int64_t(1) << 19;
 LoraPlan plan_lora(int64_t m, int64_t n, int64_t k, int adapters, int rank) {
     LoraPlan p{};
     if (m > kMaxRows) m = kMaxRows;
-    // rows of the second launch's tiles: 64 once those fill the chip twice over
-    p.rows = ceil_div(m, kTallRows) * ceil_div(n, kTallCols) >= 512 ? kTallRows : 16;
-    const int64_t tiles = ceil_div(m, 16);
-    const int64_t most = m < 16 ? m : 16;
-    // many tiles: a tile seldom holds more than the end of one request and the start of the next
-    const int64_t share = p.rows > 16 ? 2 : tiles >= 64 ? 1 : most;
-    p.slots = int(share < adapters ? share : adapters);
-    if (p.slots < 1) p.slots = 1;
-    int64_t splits = p.rows > 16 ? 1 : ceil_div(512, tiles * p.slots);
-    if (splits > ceil_div(k, 512)) splits = ceil_div(k, 512);
+    p.tall = ceil_div(m, kTallRows) * ceil_div(n, kTallCols) >= 512;
+    // Few rows: a tile of 64 reads an adapter's weights once where a tile of 16 reads them up to four times (64 rows, 16
+    // adapters of rank 64, 4096 x 16384: 26 us against 42), but a few adapters make too few workgroups of it (64 rows, 2
+    // adapters, 4096 x 4096: 22 us against 15).
+    p.tile = p.tall || m <= 16 || adapters < 8 ? 16 : 64;
+    const int64_t tiles = ceil_div(m, p.tile);
+    // Slots: one for every adapter while the launches are small; a tall call's tile of 16 seldom holds more than the
+    // end of one request and the start of the next.
+    int64_t slots = p.tall ? 2 : ceil_div(1024, tiles * ceil_div(n, 256));
+    if (slots > p.tile) slots = p.tile;
+    if (slots > adapters) slots = adapters;
+    if (slots > m) slots = m;
+    p.slots = int(slots);
+    // parts of K that make 256 workgroups, in whole turns of their waves (64 rows, 48 adapters of rank 16, 4096 x 4096:
+    // 12.9 us; 512 workgroups 13.7, 128 14.8: each part is another read of the second launch)
+    int64_t splits = p.tall ? 1 : ceil_div(256, tiles * slots);
     if (splits > 16) splits = 16;
-    p.kspan = ceil_div(ceil_div(k, splits), 32) * 32;
+    const int64_t turn = rank > 64 ? 256 : 512;
+    p.kspan = p.tall ? k : ceil_div(ceil_div(k, splits), turn) * turn;
     p.splits = int(ceil_div(k, p.kspan));
     // sums [split][row][rank], or operands (2 KB a row tile and 32-wide step of the rank) and a factor a row
-    p.workspace = p.rows > 16 ? size_t(tiles) * (size_t(rank <= 32 ? 1 : rank <= 64 ? 2 : 4) * 2048 + 64)
-                               : size_t(p.splits) * size_t(m) * size_t(rank) * 4;
+    p.workspace = p.tall ? size_t(tiles) * (size_t(rank <= 32 ? 1 : rank <= 64 ? 2 : 4) * 2048 + 64)
+                         : size_t(p.splits) * size_t(m) * size_t(rank) * 4;
     return p;
 }
 
