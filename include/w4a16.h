@@ -553,7 +553,7 @@ w4a16_status_t kv4_attention(const void* q, w4a16_dtype_t dtype, int64_t tokens,
                              const int32_t* cu_q, int64_t batch, int causal, int64_t window, float scale, void* out,
                              int64_t ldo, void* workspace, size_t workspace_bytes, void* stream);
 
-/* Workspace bytes of lora_add (0 for invalid or empty sizes); header rules as above. */
+/* Workspace bytes of lora_add (0: none needed, or invalid or empty sizes); header rules as above. */
 size_t lora_add_workspace_bytes(int64_t m, int64_t n, int64_t k, int64_t adapters, int64_t rank);
 
 /*

@@ -389,7 +389,7 @@ def lora_add(y: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor,
     device = _device_index(x, y, a, b, index, scales, out, workspace)
     if out is None:
         out = y.new_empty((m, n))
-    if need == 0:
+    if m == 0 or n == 0:
         return out
     stream = _raw_stream(device)
     ws, ws_bytes = _workspace(workspace, need, device, stream)

@@ -24,6 +24,7 @@ struct LoraArgs {
 };
 
 struct LoraPlan {
+    bool one;          // a row or two: one launch, no workspace
     bool tall;         // many rows: the second launch takes tiles of 64 rows by 512 columns
     int tile;          // rows of the first launch's tiles (few rows: of both)
     int slots;         // workgroups that share a row tile's distinct adapters

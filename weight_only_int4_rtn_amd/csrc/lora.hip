@@ -116,17 +116,99 @@ __device__ inline int row_operand(const LoraArgs& a, const float* t, int splits,
 }
 
 
+// x A_l^T of 16 rows (lane L: row at xr, quarter L / 16 of each 32 columns) over
+// columns [k0, k1), by a whole workgroup: the waves take runs of columns in turn
+// and add up in LDS.  Left in sum: place p = component p / 64 of lane p % 64 (rank
+// index 16 (p / 256) + 4 (lane / 16) + p / 64 % 4 of row lane % 16).
+template <int ACT, int RT, int WAVES>  // RT: 16-row tiles of the rank
+__device__ inline void contract(const LoraArgs& a, int l, const uint16_t* xr, int64_t k0, int64_t k1, int wave, int lane,
+                                float (*lds)[RT * 4 * 64]) {
+    constexpr int UN = RT >= 8 ? 2 : 4;
+    const int col = lane % 16, kq = lane / 16;
+    const uint16_t* ar[RT];
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+        const int r = min(16 * i + col, a.rank - 1);
+        ar[i] = a.a + (int64_t(l) * a.rank + r) * a.k + 8 * kq;
+    }
+    f32x4_t acc[RT];
+#pragma unroll
+    for (int i = 0; i < RT; ++i) acc[i] = f32x4_t{0, 0, 0, 0};
+    // A wave takes runs of 32 UN columns in turn, all of a run's loads in flight
+    // together; of the last run the columns that exist (K is a multiple of 8: a
+    // lane's 8 columns are inside or outside together).
+    for (int64_t k = k0 + 32 * UN * wave; k < k1; k += 32 * UN * WAVES) {
+        if (k + 32 * UN <= k1) {
+            uint4 xv[UN], av[UN][RT];
+#pragma unroll
+            for (int n = 0; n < UN; ++n) {
+                xv[n] = *reinterpret_cast<const uint4*>(xr + k + 32 * n);
+#pragma unroll
+                for (int i = 0; i < RT; ++i) av[n][i] = *reinterpret_cast<const uint4*>(ar[i] + k + 32 * n);
+            }
+#pragma unroll
+            for (int n = 0; n < UN; ++n)
+#pragma unroll
+                for (int i = 0; i < RT; ++i) acc[i] = mfma16<ACT>(av[n][i], xv[n], acc[i]);
+            continue;
+        }
+        for (int64_t kk = k; kk < k1; kk += 32) {
+            uint4 xv = make_uint4(0, 0, 0, 0), av[RT];
+#pragma unroll
+            for (int i = 0; i < RT; ++i) av[i] = xv;
+            if (kk + 8 * kq < k1) {
+                xv = *reinterpret_cast<const uint4*>(xr + kk);
+#pragma unroll
+                for (int i = 0; i < RT; ++i) av[i] = *reinterpret_cast<const uint4*>(ar[i] + kk);
+            }
+#pragma unroll
+            for (int i = 0; i < RT; ++i) acc[i] = mfma16<ACT>(av[i], xv, acc[i]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) lds[wave][(4 * i + j) * 64 + lane] = acc[i][j];
+    __syncthreads();
+    for (int p = threadIdx.x; p < RT * 4 * 64; p += 64 * WAVES) {
+        float x = lds[0][p];
+#pragma unroll
+        for (int w = 1; w < WAVES; ++w) x += lds[w][p];
+        lds[0][p] = x;
+    }
+    __syncthreads();
+}
+
+// The operands of the sums that contract() left, times the adapter's scale.  Returns e.
+template <int ACT, int RT>
+__device__ inline int contracted_operand(const LoraArgs& a, const float* sum, float scale, int lane, uint4 (&hi)[(RT + 1) / 2],
+                                         uint4 (&lo)[(RT + 1) / 2]) {
+    constexpr int RS = (RT + 1) / 2;
+    const int col = lane % 16, kq = lane / 16;
+    float v[RS][8];
+#pragma unroll
+    for (int s = 0; s < RS; ++s)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            // rank index 32 s + 8 kq + i: rank tile 2 s + kq / 2, quarter 2 (kq % 2) + i / 4 of its rows
+            const int tile = min(2 * s + kq / 2, RT - 1), from = (2 * (kq % 2) + i / 4) * 16 + col;
+            const float x = sum[(4 * tile + i % 4) * 64 + from] * scale;
+            v[s][i] = 32 * s + 8 * kq < a.rank ? x : 0.0f;
+        }
+    return operands_of<ACT, RS>(v, hi, lo);
+}
+
 // t[split][row][r] = sum over the split's columns of x[row] A_l[r].
 // Grid: x = tile of TILE rows, y = slot, z = split.  An adapter's rows are
 // gathered, 16 to a product, so its weights are read once a tile wherever its
-// rows stand.  The waves take runs of columns in turn and add up in LDS.
+// rows stand.
 //
 // OPERANDS (one split, tiles of 16 rows in place): instead of sums, the rows'
 // operands for the second launch (operands_of): [row tile][32-wide step of the
 // rank][high, low][lane].
 template <int ACT, int RT, int TILE, bool OPERANDS>  // RT: 16-row tiles of the rank
 __global__ __launch_bounds__(OPERANDS ? 512 : 256) void lora_shrink_kernel(LoraArgs a, int slots, int kspan, float* t, uint4* operands, float* factors) {
-    constexpr int UN = RT >= 8 ? 2 : 4, WAVES = OPERANDS ? 8 : 4, THREADS = 64 * WAVES;
+    constexpr int WAVES = OPERANDS ? 8 : 4;
     __shared__ float lds[WAVES][RT * 4 * 64];
     const int lane = threadIdx.x % 64, wave = uniform(threadIdx.x / 64);
     const int col = lane % 16, kq = lane / 16;
@@ -138,80 +220,18 @@ __global__ __launch_bounds__(OPERANDS ? 512 : 256) void lora_shrink_kernel(LoraA
         const int l = d.next(rows);
         if (seen % slots != int(blockIdx.y)) continue;
         const float scale = OPERANDS && a.scales ? a.scales[l] : 1.0f;
-        const uint16_t* ar[RT];
-#pragma unroll
-        for (int i = 0; i < RT; ++i) {
-            const int r = min(16 * i + col, a.rank - 1);
-            ar[i] = a.a + (int64_t(l) * a.rank + r) * a.k + 8 * kq;
-        }
         const int count = __popcll(rows);
         for (int first = 0; first < (OPERANDS ? 1 : count); first += 16) {
             const bool mine = OPERANDS ? (rows >> col & 1) : first + col < count;
             const int at = OPERANDS ? col : nth_bit(rows, mine ? first + col : first);
             const int64_t row = row0 + at < a.m ? row0 + at : a.m - 1;
             const uint16_t* xr = a.x + row * a.ldx + 8 * kq;
-            f32x4_t acc[RT];
-#pragma unroll
-            for (int i = 0; i < RT; ++i) acc[i] = f32x4_t{0, 0, 0, 0};
-            // A wave takes runs of 32 UN columns in turn, all of a run's loads in
-            // flight together; of the last run the columns that exist (K is a
-            // multiple of 8: a lane's 8 columns are inside or outside together).
-            for (int64_t k = k0 + 32 * UN * wave; k < k1; k += 32 * UN * WAVES) {
-                if (k + 32 * UN <= k1) {
-                    uint4 xv[UN], av[UN][RT];
-#pragma unroll
-                    for (int n = 0; n < UN; ++n) {
-                        xv[n] = *reinterpret_cast<const uint4*>(xr + k + 32 * n);
-#pragma unroll
-                        for (int i = 0; i < RT; ++i) av[n][i] = *reinterpret_cast<const uint4*>(ar[i] + k + 32 * n);
-                    }
-#pragma unroll
-                    for (int n = 0; n < UN; ++n)
-#pragma unroll
-                        for (int i = 0; i < RT; ++i) acc[i] = mfma16<ACT>(av[n][i], xv[n], acc[i]);
-                    continue;
-                }
-                for (int64_t kk = k; kk < k1; kk += 32) {
-                    uint4 xv = make_uint4(0, 0, 0, 0), av[RT];
-#pragma unroll
-                    for (int i = 0; i < RT; ++i) av[i] = xv;
-                    if (kk + 8 * kq < k1) {
-                        xv = *reinterpret_cast<const uint4*>(xr + kk);
-#pragma unroll
-                        for (int i = 0; i < RT; ++i) av[i] = *reinterpret_cast<const uint4*>(ar[i] + kk);
-                    }
-#pragma unroll
-                    for (int i = 0; i < RT; ++i) acc[i] = mfma16<ACT>(av[i], xv, acc[i]);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < RT; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) lds[wave][(4 * i + j) * 64 + lane] = acc[i][j];
-            __syncthreads();
-            // the waves' sums added, one value a thread at a time; place p holds component p / 64 of lane p % 64
-            for (int p = threadIdx.x; p < RT * 4 * 64; p += THREADS) {
-                float x = lds[0][p];
-#pragma unroll
-                for (int w = 1; w < WAVES; ++w) x += lds[w][p];
-                lds[0][p] = x;
-            }
-            __syncthreads();
+            contract<ACT, RT, WAVES>(a, l, xr, k0, k1, wave, lane, lds);
             if constexpr (OPERANDS) {
                 if (wave == 0) {
                     constexpr int RS = (RT + 1) / 2;
-                    float v[RS][8];
-#pragma unroll
-                    for (int s = 0; s < RS; ++s)
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            // rank index 32 s + 8 kq + i: rank tile 2 s + kq / 2, quarter 2 (kq % 2) + i / 4 of its rows
-                            const int tile = min(2 * s + kq / 2, RT - 1), from = (2 * (kq % 2) + i / 4) * 16 + col;
-                            const float x = lds[0][(4 * tile + i % 4) * 64 + from] * scale;
-                            v[s][i] = 32 * s + 8 * kq < a.rank ? x : 0.0f;
-                        }
                     uint4 hi[RS], lo[RS];
-                    const int e = operands_of<ACT, RS>(v, hi, lo);
+                    const int e = contracted_operand<ACT, RT>(a, lds[0], scale, lane, hi, lo);
                     if (mine) {
                         uint4* to = operands + int64_t(blockIdx.x) * RS * 128 + lane;
 #pragma unroll
@@ -339,6 +359,69 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(LoraArgs a, int slots,
     }
 }
 
+// A row or two: both steps in one launch.  Grid: x = 256 columns; every
+// workgroup contracts K for itself, which the L2 serves, and saves the second
+// launch and the way through memory between the two.
+template <int ACT, int RT>
+__global__ __launch_bounds__(512) void lora_one_kernel(LoraArgs a) {
+    constexpr int WAVES = 8, RS = (RT + 1) / 2;
+    __shared__ float lds[WAVES][RT * 4 * 64];
+    const int lane = threadIdx.x % 64, wave = uniform(threadIdx.x / 64);
+    const int col = lane % 16, kq = lane / 16;
+    const int64_t n0 = int64_t(blockIdx.x) * 256 + 32 * wave;
+    Distinct<16> d(a.index, 0, a.m, a.adapters, lane);
+    const int64_t row = col < a.m ? col : a.m - 1;
+    const int64_t n = n0 + 8 * kq;
+    const uint16_t* src = a.y + row * a.ldy + n;
+    uint16_t* dst = a.out + row * a.ldo + n;
+    const bool whole = n + 8 <= a.n && a.ldy % 8 == 0 && a.ldo % 8 == 0 &&
+                       ((reinterpret_cast<uintptr_t>(a.y) | reinterpret_cast<uintptr_t>(a.out)) & 15) == 0;
+    uint4 y = make_uint4(0, 0, 0, 0);
+    if (whole) y = *reinterpret_cast<const uint4*>(src);
+    else y = load_columns(src, a.n - n);
+    f32x4_t add[2] = {f32x4_t{0, 0, 0, 0}, f32x4_t{0, 0, 0, 0}};
+    float f = 0.0f;
+    while (d.left) {
+        uint64_t rows;
+        const int l = d.next(rows);
+        const float scale = a.scales ? a.scales[l] : 1.0f;
+        uint4 bv[2][RS];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int64_t c = n0 + column_of(col, h);
+            const uint16_t* br = a.b + (int64_t(l) * a.n + (c < a.n ? c : a.n - 1)) * a.rank + 8 * kq;
+#pragma unroll
+            for (int s = 0; s < RS; ++s) {
+                bv[h][s] = make_uint4(0, 0, 0, 0);
+                if (32 * s + 8 * kq < a.rank) bv[h][s] = *reinterpret_cast<const uint4*>(br + 32 * s);
+            }
+        }
+        contract<ACT, RT, WAVES>(a, l, a.x + row * a.ldx + 8 * kq, 0, a.k, wave, lane, lds);
+        uint4 hi[RS], lo[RS];
+        const int e = contracted_operand<ACT, RT>(a, lds[0], scale, lane, hi, lo);
+        f32x4_t acc[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            acc[h] = f32x4_t{0, 0, 0, 0};
+#pragma unroll
+            for (int s = 0; s < RS; ++s) {
+                acc[h] = mfma16<ACT>(bv[h][s], hi[s], acc[h]);
+                acc[h] = mfma16<ACT>(bv[h][s], lo[s], acc[h]);
+            }
+        }
+        if (rows >> col & 1) {
+            add[0] = acc[0];
+            add[1] = acc[1];
+            f = ldexpf(1.0f, e);
+        }
+        __syncthreads();
+    }
+    if (col >= a.m) return;
+    const uint4 o = add_columns<ACT>(y, add[0], add[1], f);
+    if (whole) *reinterpret_cast<uint4*>(dst) = o;
+    else store_columns(dst, a.n - n, o);
+}
+
 // Many rows.  Grid: x = kTallCols columns, y = tile of 64 rows.  A wave takes a
 // quarter of the columns of all 64 rows, 64 at a time (a row's line of 128
 // bytes is read and written in one go), so each operand of B serves four
@@ -451,7 +534,9 @@ hipError_t run(const LoraArgs& a, const LoraPlan& p, hipStream_t stream) {
     const unsigned tiles = unsigned(ceil_div(a.m, p.tile));
     constexpr int RS = (RT + 1) / 2;
     const dim3 grid(tiles, unsigned(p.slots), unsigned(p.splits));
-    if (p.tall) {
+    if (p.one) {
+        lora_one_kernel<ACT, RT><<<dim3(unsigned(ceil_div(a.n, 256))), dim3(512), 0, stream>>>(a);
+    } else if (p.tall) {
         uint4* operands = reinterpret_cast<uint4*>(t);
         float* factors = reinterpret_cast<float*>(operands + int64_t(tiles) * RS * 128);
         lora_shrink_kernel<ACT, RT, 16, true><<<grid, dim3(512), 0, stream>>>(a, p.slots, int(p.kspan), t, operands, factors);
@@ -487,6 +572,9 @@ constexpr int64_t kMaxRows = int64_t(1) << 19;
 LoraPlan plan_lora(int64_t m, int64_t n, int64_t k, int adapters, int rank) {
     LoraPlan p{};
     if (m > kMaxRows) m = kMaxRows;
+    // One launch for a row or two whose workgroups read no more than 128 KB of A each (2048 x 2560, rank 16: 1 row 5.3 us
+    // against 7.9 in two launches, 2 rows 6.6 against 8.2; rank 64, twice that limit: 11.7 against 10.2).
+    p.one = m <= 2 && m * rank * k <= int64_t(1) << 16;
     p.tall = ceil_div(m, kTallRows) * ceil_div(n, kTallCols) >= 512;
     // Few rows: a tile of 64 reads an adapter's weights once where a tile of 16 reads them up to four times (64 rows, 16
     // adapters of rank 64, 4096 x 16384: 26 us against 42), but a few adapters make too few workgroups of it (64 rows, 2
@@ -508,8 +596,9 @@ LoraPlan plan_lora(int64_t m, int64_t n, int64_t k, int adapters, int rank) {
     p.kspan = p.tall ? k : ceil_div(ceil_div(k, splits), turn) * turn;
     p.splits = int(ceil_div(k, p.kspan));
     // sums [split][row][rank], or operands (2 KB a row tile and 32-wide step of the rank) and a factor a row
-    p.workspace = p.tall ? size_t(tiles) * (size_t(rank <= 32 ? 1 : rank <= 64 ? 2 : 4) * 2048 + 64)
-                         : size_t(p.splits) * size_t(m) * size_t(rank) * 4;
+    p.workspace = p.one    ? 0
+                  : p.tall ? size_t(tiles) * (size_t(rank <= 32 ? 1 : rank <= 64 ? 2 : 4) * 2048 + 64)
+                           : size_t(p.splits) * size_t(m) * size_t(rank) * 4;
     return p;
 }
 

@@ -210,7 +210,8 @@ size_t lora_add_workspace_bytes(int64_t m, int64_t n, int64_t k, int64_t adapter
     if (m <= 0 || m > kMaxDim || n <= 0 || n > kMaxDim || k <= 0 || k > kMaxDim || k % 8 != 0 || adapters <= 0 ||
         adapters > kMaxDim || rank <= 0 || rank > kMaxLoraRank || rank % 8 != 0)
         return 0;
-    return kSyncBytes + plan_lora(m, n, k, int(adapters), int(rank)).workspace;
+    const size_t w = plan_lora(m, n, k, int(adapters), int(rank)).workspace;
+    return w ? kSyncBytes + w : 0;
 }
 
 w4a16_status_t lora_add(const void* x, w4a16_dtype_t dtype, int64_t m, int64_t k, int64_t ldx, const void* a,
@@ -235,8 +236,9 @@ w4a16_status_t lora_add(const void* x, w4a16_dtype_t dtype, int64_t m, int64_t k
         overlap(out, ob, index, ib) || overlap(out, ob, scales, sb))
         return W4A16_EINVAL;
     const size_t need = lora_add_workspace_bytes(m, n, k, adapters, rank);
-    if (!workspace || workspace_bytes < need) return W4A16_EWORKSPACE;
-    if (!aligned(workspace, 16) || overlap(workspace, need, x, xb) || overlap(workspace, need, y, yb) ||
+    if (need > 0 && (!workspace || workspace_bytes < need)) return W4A16_EWORKSPACE;
+    if (need > 0 && !aligned(workspace, 16)) return W4A16_EINVAL;
+    if (overlap(workspace, need, x, xb) || overlap(workspace, need, y, yb) ||
         overlap(workspace, need, out, ob) || overlap(workspace, need, a, ab) || overlap(workspace, need, b, bb) ||
         overlap(workspace, need, index, ib) || overlap(workspace, need, scales, sb))
         return W4A16_EINVAL;
