@@ -463,7 +463,7 @@ const char* w4a16_status_string(w4a16_status_t status);
  * at most 4096) for kv_heads heads of head_dim channels (64, 128 or 256), or
  * 0 for invalid sizes.  Keys and values are kept as the weights are: signed
  * 4-bit codes with one FP32 scale per token, head and group of
- * min(head_dim, 128) channels.  A page of one head is one contiguous region of
+ * min(head_dim, 128) channels.  At most 256 GiB.  A page of one head is one contiguous region of
  *   page_size * head_dim + 8 * page_size * (head_dim / min(head_dim, 128))
  * bytes, [pages][kv_heads][region]; inside it is the library's own execution
  * layout (write it with kv4_append, read it with kv4_read).  The buffer needs

@@ -349,3 +349,44 @@ def test_attention_on_another_stream_and_in_a_graph(dev, qs):
     torch.cuda.synchronize()
     check_attention(cache, q, counts, [1100, 1499], True, 0, out, what="replay with other lengths")
     assert not ws[:min(need, 1 << 20)].any(), "the workspace's header is not zero"
+
+
+def test_attention_of_rows_of_256_channels_in_a_graph(dev):
+    """Row tiles of 256 channels need more than 64 KB of LDS, which is asked for per launch: under capture too."""
+    lib = w4()
+    say("row tiles of 256 channels in a graph")
+    kv, qs = [700, 900], [600, 450]
+    cache = Cache(dev, kv, 1, 256, 16, seed=12)
+    q, counts, want = run_attention(dev, cache, qs, kv, 8, True, 0, torch.bfloat16)
+    check_attention(cache, q, counts, kv, True, 0, want, what="eager")
+    qd, table, lens = q.to(dev), cache.table.to(dev), torch.tensor(kv, dtype=torch.int32, device=dev)
+    cu = torch.tensor([0, qs[0], sum(qs)], dtype=torch.int32, device=dev)
+    need = lib.kv4_attention_workspace_bytes(q.shape[0], 2, 8, 1, 256, table.shape[1], 16, ragged=True)
+    ws = torch.zeros(max(need, 16), dtype=torch.uint8, device=dev)
+    out = torch.empty_like(qd)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        lib.kv4_attention(qd, cache.pool, table, lens, cu_q=cu, out=out, workspace=ws)
+    for rep in range(3):
+        out.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want), f"replay {rep}"
+
+
+@pytest.mark.parametrize("d,hk,share", [(64, 8, 8), (128, 4, 16), (256, 2, 16)], ids=["d64", "d128", "d256"])
+def test_attention_row_tiles(dev, d, hk, share):
+    """Tiles of 64 rows: prompts whole and in pieces, with windows, without a mask, on bad pages, split and unsplit (rows
+    and tokens enough that every call takes them)."""
+    say("row tiles", d, hk, share)
+    for kv, qs, causal, window, page in (([700, 33, 1300], [700, 33, 140], True, 0, 48), ([900, 1000], [333, 500], True, 130, 16),
+                                         ([2500], [190], False, 0, 64), ([1200, 640], [320, 640], False, 77, 32)):
+        cache = Cache(dev, kv, hk, d, page, seed=sum(kv) + d + window)
+        there = [np.ones(cache.table.shape[1], bool) for _ in kv]
+        cache.table[0, 3] = -7
+        there[0][3] = False
+        q, counts, out = run_attention(dev, cache, qs, kv, share * hk, causal, window, torch.bfloat16)
+        check_attention(cache, q, counts, kv, causal, window, out, what=f"{kv} {qs}", pages_there=there)
+        again = run_attention(dev, cache, qs, kv, share * hk, causal, window, torch.bfloat16)[2]
+        assert torch.equal(out.view(torch.int16), again.view(torch.int16)), "two runs differ"

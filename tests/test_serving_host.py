@@ -144,6 +144,19 @@ def test_lora_workspace(lib):
         assert f(*bad) == 0
 
 
+def test_size_limits(lib):
+    """Sizes whose launches or offsets would not fit are refused, the largest that do are not."""
+    assert lib.kv4_pool_bytes(1 << 21, 64, 8, 128) == (1 << 21) * 8 * 64 * 136  # 136 GiB
+    assert lib.kv4_pool_bytes(1 << 22, 64, 8, 128) == 0                         # 272 GiB
+    assert append(lib, tokens=0) == B.OK and append(lib, tokens=(1 << 23) + 1) == B.EINVAL
+    big = dict(table=A + 2 * GB, width=4, ldt=4, cu=A + 6 * GB)
+    assert attend(lib, tokens=1 << 25, heads=4, **big) == B.EINVAL   # 2^27 rows
+    assert attend(lib, tokens=4, batch=(1 << 20) + 1, **big) == B.EINVAL
+    f = w4.kv4_attention_workspace_bytes
+    assert f(1 << 20, 1, 64, 8, 128, 1 << 16, 16, ragged=True) == 0  # fits, in one part
+    assert f((1 << 20) + 1, 1, 64, 8, 128, 1 << 16, 16, ragged=True) == 0
+
+
 # the binding's own checks come before the library and the device: CPU tensors reach them
 
 

@@ -902,7 +902,10 @@ Kv4Plan plan_kv4_attention(int64_t tokens, int64_t batch, int heads, int kv_head
     // heads on 1024 tokens 17 us against 20 on tiles of 16, 50 queries 16 against
     // 13; D = 64: 512 x 16 on 512 11 against 12, 50 x 16 on 1074 12 against 10; D =
     // 256: 1024 x 8 on 1024 even, 512 x 8 on 512 20 against 16).
-    if (ragged && tokens * share >= 16 * batch && tokens * heads * reach(64) >= int64_t(1) << 22) p.rows = 64;
+    // (their grid is one line of tiles and key heads, which has to fit)
+    if (ragged && tokens * share >= 16 * batch && tokens * heads * reach(64) >= int64_t(1) << 22 &&
+        (tokens * share / 64 + batch) * kv_heads < int64_t(1) << 23)
+        p.rows = 64;
     p.tiles = ragged ? tokens * share / p.rows + batch : batch * ceil_div(share, p.rows);
     const int64_t most = reach(p.rows);
     // Splits: with few tiles as many as fill the chip once (768 workgroups of D

@@ -17,7 +17,10 @@ constexpr int64_t kMaxDim = int64_t(1) << 24;
 constexpr int64_t kMaxHeads = 1024;
 constexpr int64_t kMaxPage = 4096;
 constexpr int64_t kMaxTokens = int64_t(1) << 28;  // of one request in the cache
-constexpr int64_t kMaxRows = int64_t(1) << 30;    // query tokens x heads of a call
+constexpr int64_t kMaxRows = int64_t(1) << 26;    // query tokens x heads of a call: a launch's work items fit 32 bits
+constexpr int64_t kMaxBatch = int64_t(1) << 20;
+constexpr int64_t kMaxCacheTokens = int64_t(1) << 23;         // appended or read by a call
+constexpr uint64_t kMaxPoolBytes = uint64_t(1) << 38;         // scales are addressed in units of 64 bytes
 constexpr int64_t kMaxLoraRank = 128;
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -40,7 +43,8 @@ int act_of(w4a16_dtype_t t) { return t == W4A16_BF16 ? kActBf16 : kActF16; }
 
 bool valid_pool(int64_t pages, int64_t page, int64_t kv_heads, int64_t dim) {
     return pages >= 1 && pages <= (int64_t(1) << 31) - 1 && page >= 16 && page <= kMaxPage && page % 16 == 0 &&
-           kv_heads >= 1 && kv_heads <= kMaxHeads && (dim == 64 || dim == 128 || dim == 256);
+           kv_heads >= 1 && kv_heads <= kMaxHeads && (dim == 64 || dim == 128 || dim == 256) &&
+           uint64_t(pages) * uint64_t(kv_heads) * uint64_t(kv4_region(page, int(dim))) <= kMaxPoolBytes;
 }
 
 }  // namespace
@@ -59,7 +63,7 @@ w4a16_status_t kv4_append(const void* qkv, w4a16_dtype_t dtype, int64_t tokens, 
     if (!act_dtype(dtype)) return W4A16_EUNSUPPORTED;
     if (!valid_pool(pages, page_size, kv_heads, head_dim) || heads < 0 || heads > kMaxHeads) return W4A16_EINVAL;
     const int64_t width = (heads + 2 * kv_heads) * head_dim;
-    if (tokens < 0 || tokens > kMaxDim || ldqkv < width || ldqkv > kMaxDim || ldqkv % 8 != 0) return W4A16_EINVAL;
+    if (tokens < 0 || tokens > kMaxCacheTokens || ldqkv < width || ldqkv > kMaxDim || ldqkv % 8 != 0) return W4A16_EINVAL;
     if ((rope == nullptr) != (positions == nullptr)) return W4A16_EINVAL;
     if (rope && (rope_len < 1 || rope_len > kMaxTokens || rot_dim < 16 || rot_dim > head_dim || rot_dim % 16 != 0 ||
                  !aligned(rope, 16) || !aligned(positions, 4)))
@@ -98,7 +102,7 @@ w4a16_status_t kv4_append(const void* qkv, w4a16_dtype_t dtype, int64_t tokens, 
 w4a16_status_t kv4_read(const void* pool, int64_t pages, int64_t page_size, int64_t kv_heads, int64_t head_dim,
                         const int64_t* slots, int64_t tokens, w4a16_dtype_t out_dtype, void* k, void* v, void* stream) {
     if (out_dtype != W4A16_F32 && !act_dtype(out_dtype)) return W4A16_EUNSUPPORTED;
-    if (!valid_pool(pages, page_size, kv_heads, head_dim) || tokens < 0 || tokens > kMaxDim) return W4A16_EINVAL;
+    if (!valid_pool(pages, page_size, kv_heads, head_dim) || tokens < 0 || tokens > kMaxCacheTokens) return W4A16_EINVAL;
     if (tokens == 0) return W4A16_OK;
     if (!pool || !slots || !k || !v || !aligned(pool, 16) || !aligned(slots, 8) || !aligned(k, 16) || !aligned(v, 16))
         return W4A16_EINVAL;
@@ -128,7 +132,7 @@ bool valid_attention(int64_t tokens, int64_t batch, int64_t heads, int64_t kv_he
                      int64_t table_width, int64_t page_size, bool ragged, int64_t window) {
     if (!valid_pool(1, page_size, kv_heads, head_dim)) return false;
     if (heads < 1 || heads > kMaxHeads || heads % kv_heads != 0) return false;
-    if (tokens < 0 || tokens > kMaxDim || batch < 0 || batch > kMaxDim || tokens * heads > kMaxRows) return false;
+    if (tokens < 0 || tokens > kMaxDim || batch < 0 || batch > kMaxBatch || tokens * heads > kMaxRows) return false;
     if (!ragged && tokens != batch) return false;
     if (tokens > 0 && batch == 0) return false;
     if (table_width < 1 || table_width * page_size >= kMaxTokens) return false;
