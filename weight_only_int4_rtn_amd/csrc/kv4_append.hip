@@ -183,12 +183,15 @@ __global__ __launch_bounds__(256) void kv4_append_kernel(Kv4AppendArgs a, int pa
 // A thread reads 8 channels of one head of one token of both sides (8192 tokens
 // of 8 heads of 128: 14 us, its 34 MB of output at 2.4 TB/s).
 template <int DT, int D>  // DT: 0 = f32, 1 = bf16, 2 = f16
-__global__ __launch_bounds__(256) void kv4_read_kernel(Kv4ReadArgs a) {
+__global__ __launch_bounds__(256) void kv4_read_kernel(Kv4ReadArgs a, int tokens) {
     constexpr int W = kv4_width(D), NB = kv4_blocks(D);
-    const int64_t t = blockIdx.x;
-    const int part = blockIdx.y * 256 + threadIdx.x;
+    // a workgroup takes `tokens` whole tokens, or 256 threads of one at a time (y)
+    const int row = a.kv_heads * (D / 8);
+    const int in = tokens > 1 ? int(threadIdx.x) / row : 0;
+    const int64_t t = int64_t(blockIdx.x) * tokens + in;
+    const int part = blockIdx.y * 256 + threadIdx.x - in * row;
     const int head = part / (D / 8), d0 = part % (D / 8) * 8;
-    if (head >= a.kv_heads) return;
+    if (in >= tokens || t >= a.tokens || head >= a.kv_heads) return;
     const int64_t slot = a.slots[t];
     const int64_t to = (t * a.kv_heads + head) * D + d0;
     float k[8], v[8];
@@ -251,11 +254,12 @@ hipError_t append_by_dim(const Kv4AppendArgs& a, hipStream_t stream) {
 
 template <int DT>
 hipError_t read_by_dim(const Kv4ReadArgs& a, hipStream_t stream) {
-    const dim3 grid(unsigned(a.tokens), unsigned(ceil_div(int64_t(a.kv_heads) * (a.dim / 8), 256)));
+    const int row = a.kv_heads * (a.dim / 8), tokens = row < 256 ? 256 / row : 1;
+    const dim3 grid(unsigned(ceil_div(a.tokens, tokens)), unsigned(ceil_div(row, 256)));
     switch (a.dim) {
-        case 64: kv4_read_kernel<DT, 64><<<grid, dim3(256), 0, stream>>>(a); break;
-        case 128: kv4_read_kernel<DT, 128><<<grid, dim3(256), 0, stream>>>(a); break;
-        default: kv4_read_kernel<DT, 256><<<grid, dim3(256), 0, stream>>>(a); break;
+        case 64: kv4_read_kernel<DT, 64><<<grid, dim3(256), 0, stream>>>(a, tokens); break;
+        case 128: kv4_read_kernel<DT, 128><<<grid, dim3(256), 0, stream>>>(a, tokens); break;
+        default: kv4_read_kernel<DT, 256><<<grid, dim3(256), 0, stream>>>(a, tokens); break;
     }
     return hipGetLastError();
 }
