@@ -63,6 +63,28 @@ __device__ inline uint32_t kv4_pair(uint32_t w) {
     return and_or(v, kKvMask, kKvMagic);
 }
 
+// The four f16 pairs 24 + q of each of two words (pair i: nibbles i and i + 4).
+// The words go through 64-bit shifts together: half the shifts, and the bits that
+// one word hands the other fall outside the mask.  The 16-row tiles use it (64
+// ragged sequences 91 -> 85 us, 4 of 131072 tokens 109 -> 104); the 64-row tiles,
+// which convert once for four waves, keep single words (a prompt of 4096 tokens
+// 192 us, 196 with pairs of words).
+template <int N>
+__device__ inline uint64_t shl64(uint64_t v) {
+    uint64_t d;
+    asm("v_lshlrev_b64 %0, %1, %2" : "=v"(d) : "i"(N), "v"(v));
+    return d;
+}
+__device__ inline void kv4_pairs(uint32_t a, uint32_t b, uint32_t (&pa)[4], uint32_t (&pb)[4]) {
+    const uint64_t v = uint64_t(a) | (uint64_t(b) << 32);
+    const uint64_t s[4] = {shl64<6>(v), shl64<2>(v), shr64<2>(v), shr64<6>(v)};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        pa[i] = and_or(uint32_t(s[i]), kKvMask, kKvMagic);
+        pb[i] = and_or(uint32_t(s[i] >> 32), kKvMask, kKvMagic);
+    }
+}
+
 // ---------------------------------------------------------------------------
 // Launch arguments
 // ---------------------------------------------------------------------------

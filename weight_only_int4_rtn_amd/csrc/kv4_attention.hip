@@ -245,11 +245,11 @@ constexpr uint32_t kOnes = 0x3C003C00u;  // two f16 ones
 // last of a tile's workgroups to finish, in split order.
 //
 // HBM bounds long contexts: 4 requests of 131072 tokens, 8 heads of 128, 570 MB,
-// take 103 to 109 us, 5.2 to 5.5 TB/s.  Shorter ones are bounded by the chain of
+// take 98 to 105 us, 5.4 to 5.8 TB/s.  Shorter ones are bounded by the chain of
 // dependent accesses of a part (lengths, pages, codes, join; 5 to 8 us): 64
-// requests of 0 to 8192 tokens 89 us (3.2 TB/s), 1 of 1000 tokens 10.5 us at D =
+// requests of 0 to 8192 tokens 84 us (3.4 TB/s), 1 of 1000 tokens 10.5 us at D =
 // 256.  Equal stretches of all requests' tokens a workgroup, in one round, pay
-// that chain twice and were slower (95 us).
+// that chain twice and were slower (95 us, where these splits took 89).
 template <int ACT, int D>
 __global__ __launch_bounds__(256, D == 256 ? 2 : D == 128 ? 3 : 4) void kv4_attention_kernel(Kv4AttentionArgs a, int span, int splits,
                                                                               uint32_t magic, unsigned* counters,
@@ -313,9 +313,11 @@ __global__ __launch_bounds__(256, D == 256 ? 2 : D == 128 ? 3 : 4) void kv4_atte
             for (int b = 0; b < NB; ++b) {
                 f32x4_t s = {offset[b], offset[b], offset[b], offset[b]};
 #pragma unroll
-                for (int ks = 0; ks < W / 32; ++ks) {
-                    const uint32_t w = k.w[c][b][ks];
-                    s = mfma(make_uint4(kv4_pair<0>(w), kv4_pair<1>(w), kv4_pair<2>(w), kv4_pair<3>(w)), q[b][ks], s);
+                for (int ks = 0; ks < W / 32; ks += 2) {
+                    uint32_t x[4], y[4];
+                    kv4_pairs(k.w[c][b][ks], k.w[c][b][ks + 1], x, y);
+                    s = mfma(make_uint4(x[0], x[1], x[2], x[3]), q[b][ks], s);
+                    s = mfma(make_uint4(y[0], y[1], y[2], y[3]), q[b][ks + 1], s);
                 }
                 const float4 f = k.s[c][b];
                 const float y[4] = {s[0] * f.x, s[1] * f.y, s[2] * f.z, s[3] * f.w};
@@ -380,12 +382,15 @@ __global__ __launch_bounds__(256, D == 256 ? 2 : D == 128 ? 3 : 4) void kv4_atte
         for (int b = 0; b < NB; ++b) {
             const uint4 pw = weights<D>(p, vs, b);
             ps[b] = mfma(make_uint4(kOnes, kOnes, kOnes, kOnes), pw, ps[b]);
-            static_for<0, CH>([&](auto ic) {
-                constexpr int i = ic, h = i / 4, ii = i % 4;
-                acc[b][i] = mfma(make_uint4(kv4_pair<ii>(v.w[0][b][2 * h]), kv4_pair<ii>(v.w[0][b][2 * h + 1]),
-                                            kv4_pair<ii>(v.w[1][b][2 * h]), kv4_pair<ii>(v.w[1][b][2 * h + 1])),
-                                 pw, acc[b][i]);
-            });
+#pragma unroll
+            for (int h = 0; h < CH / 4; ++h) {
+                uint32_t x[2][4], y[2][4];
+#pragma unroll
+                for (int c = 0; c < 2; ++c) kv4_pairs(v.w[c][b][2 * h], v.w[c][b][2 * h + 1], x[c], y[c]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    acc[b][4 * h + i] = mfma(make_uint4(x[0][i], y[0][i], x[1][i], y[1][i]), pw, acc[b][4 * h + i]);
+            }
         }
         if (more) v.load(pool + a.page * (D / 2), pool + NB * a.page * 4, ch, (step + 1) % 32, a.page, lane);
     }
