@@ -181,7 +181,7 @@ __global__ __launch_bounds__(256) void kv4_append_kernel(Kv4AppendArgs a, int pa
 }
 
 // A thread reads 8 channels of one head of one token of both sides (8192 tokens
-// of 8 heads of 128: 12.6 us, its 34 MB of output at 2.7 TB/s; 14 us with one
+// of 8 heads of 128: 13 us, its 34 MB of output at 2.6 TB/s; 14 us with one
 // token a workgroup).
 template <int DT, int D>  // DT: 0 = f32, 1 = bf16, 2 = f16
 __global__ __launch_bounds__(256) void kv4_read_kernel(Kv4ReadArgs a, int tokens) {
