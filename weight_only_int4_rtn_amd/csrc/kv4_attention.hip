@@ -903,6 +903,9 @@ Kv4Plan plan_kv4_attention(int64_t tokens, int64_t batch, int heads, int kv_head
     Kv4Plan p{};
     const int64_t share = heads / kv_heads;
     p.rows = 16;
+    // A window of the whole capacity hides nothing.  Left as given (any int64), it would overflow the sums below, and a
+    // caller's workspace would be checked against another plan than the one launched.
+    if (window >= capacity) window = 0;
     // the tokens a tile can see: its window, the queries of its rows, an aligned begin
     auto reach = [&](int rows) {
         const int64_t r = (causal ? window : 2 * window) + (ragged ? rows : 1) + 64;
