@@ -249,6 +249,13 @@ def kv4_read(pool: torch.Tensor, slots: torch.Tensor, head_dim: int, dtype: torc
     return k, v
 
 
+def _window(window) -> int:
+    """A window that the C ABI's int64 holds: longer ones hide nothing either."""
+    if not isinstance(window, int) or window < 0:
+        raise ValueError("window is 0 (none) or a positive number of tokens")
+    return min(window, (1 << 63) - 1)
+
+
 @_remember
 def _attention_need(*sizes) -> int:
     return int(_lib().kv4_attention_workspace_bytes(*sizes))
@@ -263,7 +270,7 @@ def kv4_attention_workspace_bytes(tokens: int, batch: int, heads: int, kv_heads:
                                   page_size: int, ragged: bool = False, causal: bool = True, window: int = 0) -> int:
     """Workspace kv4_attention needs for these sizes (``ragged``: cu_q is given)."""
     return _attention_need(tokens, batch, heads, kv_heads, head_dim, table_width, page_size, int(bool(ragged)),
-                           int(bool(causal)), window)
+                           int(bool(causal)), _window(window))
 
 
 @_remember
@@ -287,13 +294,12 @@ def _attention_plan(q, pool, table, kv_lens, cu_q, out, causal, window):
         raise ValueError(f"{tokens} query tokens for {batch} requests: pass cu_q")
     if tokens and not batch:
         raise ValueError("query tokens without a request")
-    if not isinstance(window, int) or window < 0:
-        raise ValueError("window is 0 (none) or a positive number of tokens")
+    window = _window(window)
     if out is not None and (out[0] != shape or out[2] != dtype or not _dense(*out[:2])):
         raise ValueError("out must be a contiguous tensor of q's shape and dtype")
     need = _attention_need(tokens, batch, heads, kv_heads, dim, width, page, 0 if cu_q is None else 1, causal, window)
     return (tag, tokens, stride[0] if tokens > 1 else heads * dim, heads, kv_heads, dim, pages, page, width,
-            table[1][0] if batch > 1 else width, batch, need)
+            table[1][0] if batch > 1 else width, batch, window, need)
 
 
 def kv4_attention(q: torch.Tensor, pool: torch.Tensor, block_table: torch.Tensor, kv_lens: torch.Tensor,
@@ -307,7 +313,7 @@ def kv4_attention(q: torch.Tensor, pool: torch.Tensor, block_table: torch.Tensor
     head_dim ** -0.5.  See kv4_attention in include/w4a16.h."""
     causal = 1 if causal else 0
     plan = _attention_plan(_meta(q), _meta(pool), _meta(block_table), _meta(kv_lens), _meta(cu_q), _meta(out), causal, window)
-    tag, tokens, ldq, heads, kv_heads, dim, pages, page, width, ldt, batch, need = plan
+    tag, tokens, ldq, heads, kv_heads, dim, pages, page, width, ldt, batch, window, need = plan
     _no_grad(q)
     index = _device_index(q, pool, block_table, kv_lens, cu_q, out, workspace)
     if out is None:
