@@ -520,6 +520,15 @@ size_t kv4_attention_workspace_bytes(int64_t tokens, int64_t batch, int64_t head
                                      int64_t table_width, int64_t page_size, int ragged, int causal, int64_t window);
 
 /*
+ * Rows (query tokens times the heads that share a key head) of a workgroup's
+ * tile in kv4_attention for these sizes: 16 or 64, each a kernel of its own, or
+ * 0 for invalid sizes or no tokens.  Pure host computation, no launch; one can
+ * tell from it which kernel a call of these sizes takes.
+ */
+int kv4_attention_tile_rows(int64_t tokens, int64_t batch, int64_t heads, int64_t kv_heads, int64_t head_dim,
+                            int64_t table_width, int64_t page_size, int ragged, int causal, int64_t window);
+
+/*
  * out = softmax(scale q k^T) v over the cache, for `batch` requests.
  *   q          device, [tokens][ldq] of dtype (BF16 or F16), rows of heads *
  *              head_dim; heads is a multiple of kv_heads, query head h reads

@@ -52,6 +52,7 @@ from ._binding import (  # noqa: F401
 from ._serving import (  # noqa: F401
     kv4_append,
     kv4_attention,
+    kv4_attention_tile_rows,
     kv4_attention_workspace_bytes,
     kv4_page_size,
     kv4_pool,

@@ -29,6 +29,8 @@ def _lib():
         L.kv4_read.restype = i32
         L.kv4_attention_workspace_bytes.argtypes = [i64] * 7 + [i32, i32, i64]
         L.kv4_attention_workspace_bytes.restype = sz
+        L.kv4_attention_tile_rows.argtypes = [i64] * 7 + [i32, i32, i64]
+        L.kv4_attention_tile_rows.restype = i32
         L.kv4_attention.argtypes = [vp, i32, i64, i64, i64, i64, i64, vp, i64, i64, vp, i64, i64, vp, vp, i64, i32, i64,
                                     ctypes.c_float, vp, i64, vp, sz, vp]
         L.kv4_attention.restype = i32
@@ -271,6 +273,13 @@ def kv4_attention_workspace_bytes(tokens: int, batch: int, heads: int, kv_heads:
     """Workspace kv4_attention needs for these sizes (``ragged``: cu_q is given)."""
     return _attention_need(tokens, batch, heads, kv_heads, head_dim, table_width, page_size, int(bool(ragged)),
                            int(bool(causal)), _window(window))
+
+
+def kv4_attention_tile_rows(tokens: int, batch: int, heads: int, kv_heads: int, head_dim: int, table_width: int, page_size: int,
+                            ragged: bool = False, causal: bool = True, window: int = 0) -> int:
+    """Rows of a workgroup's tile in kv4_attention for these sizes: 16 or 64, each a kernel of its own (0: invalid sizes)."""
+    return _lib().kv4_attention_tile_rows(tokens, batch, heads, kv_heads, head_dim, table_width, page_size, int(bool(ragged)),
+                                          int(bool(causal)), _window(window))
 
 
 @_remember

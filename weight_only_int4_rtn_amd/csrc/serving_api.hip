@@ -152,6 +152,14 @@ size_t kv4_attention_workspace_bytes(int64_t tokens, int64_t batch, int64_t head
     return w ? kSyncBytes + w : 0;
 }
 
+int kv4_attention_tile_rows(int64_t tokens, int64_t batch, int64_t heads, int64_t kv_heads, int64_t head_dim,
+                            int64_t table_width, int64_t page_size, int ragged, int causal, int64_t window) {
+    if (!valid_attention(tokens, batch, heads, kv_heads, head_dim, table_width, page_size, ragged != 0, window) || tokens == 0)
+        return 0;
+    return plan_kv4_attention(tokens, batch, int(heads), int(kv_heads), int(head_dim), table_width * page_size, ragged != 0,
+                              causal != 0, window).rows;
+}
+
 w4a16_status_t kv4_attention(const void* q, w4a16_dtype_t dtype, int64_t tokens, int64_t ldq, int64_t heads,
                              int64_t kv_heads, int64_t head_dim, const void* pool, int64_t pages, int64_t page_size,
                              const int32_t* table, int64_t table_width, int64_t ldt, const int32_t* kv_lens,
