@@ -551,8 +551,9 @@ int kv4_attention_tile_rows(int64_t tokens, int64_t batch, int64_t heads, int64_
  *   out        device, [tokens][ldo] of dtype, 16-byte aligned, ldo a
  *              multiple of 8.  A query that sees nothing gives zeros.
  *   workspace  as w4a16_linear's.
- * Logits, softmax and sums are FP32; the probabilities enter the second
- * product as f16.
+ * Logits, softmax and sums are FP32.  Each probability times its value's scale
+ * enters the second product as f16: 11 bits of those down to 2^-19 of the row's
+ * largest such weight, an absolute error of 2^-30 of the largest below.
  * Returns W4A16_OK (also for tokens == 0), W4A16_EINVAL, W4A16_EUNSUPPORTED,
  * W4A16_EWORKSPACE or W4A16_EHIP.
  */

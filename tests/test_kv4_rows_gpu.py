@@ -82,11 +82,12 @@ def test_row_tiles(dev, case, dts):
 @pytest.mark.parametrize("spread,vsize,voutlier,qsize,scale", [
     (1.0, 1e-3, 0.0, 1.5, None),
     (1.0, 3e4, 0.0, 1.5, None),
+    (1.0, 1.0, 3000.0, 1.5, None),
     (40.0, 1.0, 0.0, 30.0, None),
     (1.0, 1.0, 0.0, 1.5, -0.3),
     (1e-4, 1.0, 0.0, 1e-4, 1.0),
     (1.0, 1.0, 0.0, 1e4, 1e-4),
-], ids=["small_v", "large_v", "one_hot", "negative_scale", "flat", "large_q"])
+], ids=["small_v", "large_v", "outlier_v", "one_hot", "negative_scale", "flat", "large_q"])
 def test_row_tiles_ranges(dev, spread, vsize, voutlier, qsize, scale, d, dts):
     say("row tiles, ranges", spread, vsize, voutlier, qsize, scale, d, dts)
     kv, qs = [333, 1200], [70, 300]

@@ -11,11 +11,10 @@
 // applied in FP32 outside: the key's to the product, the value's to the
 // probability before its rounding to f16.  Queries enter as f16 scaled by a
 // power of two per row (exact for bf16 and f16 inputs up to f16's subnormals
-// 34 binades below the row's largest).  Probabilities are p 2^-E vs with E
-// the exponent of the largest value scale so far, folded into the running
-// maximum, so they use f16's range whatever the values' size; their rounding
-// (2^-11 of each) is an eighth of the bf16 output's.  The running maximum,
-// the sum and the output accumulate in FP32.
+// 34 binades below the row's largest).  The weights p vs are rounded to f16
+// relative to the row's largest of them (Running), so they use f16's range
+// whatever the values' size; their rounding (2^-11 of each) is an eighth of the
+// bf16 output's own.  The sum and the output accumulate in FP32.
 #include "kernels.h"
 #include "kv4.h"
 
@@ -199,27 +198,25 @@ __device__ inline float load_queries(const uint16_t* src, float scale, uint4 (&q
     return fmaxf(ldexpf(fabsf(scale) * kLog2e, -e), 1e-37f);
 }
 
-// A row's running softmax over some of its tokens.  Its reference follows the
-// largest logit and value scale only when they have outgrown it by 2^10 and
-// 2^3: weights up to 2^13 are as exact in f16 as those below 1, and the sums so
-// far are multiplied by a power of the reference's change a few times a row
-// instead of at every new maximum (prompt of 4096 tokens: 237 -> 209 us).
+// A row's running softmax over some of its tokens: probabilities p = 2^(z - ref)
+// in FP32 and weights p vs, which are rounded to f16.  The reference follows the
+// largest weight, not the largest logit and value scale apart: a token with large
+// values that the softmax leaves out must not push the others' weights below f16's
+// normal numbers.  A new reference puts the largest weight seen at 2^5, and the
+// next comes when one exceeds 2^15, so the sums so far are rescaled a few times a
+// row instead of at every new maximum (prompt of 4096 tokens: 237 -> 209 us).
+// Weights then have all of f16's 11 bits down to 2^-19 of the row's largest or
+// lower, and an absolute error of 2^-30 of it below.  Scales count from 2^-80 up:
+// tokens without values have p of at most 2^85, whose sum FP32 holds.
 struct Running {
-    static constexpr float kSlack = 10.0f, kScaleSlack = 8.0f;
-    float limit = -INFINITY;  // logit (before the factor) that needs a new reference
-    float vlimit = 0.0f;      // value scale that needs one
-    float ref = -INFINITY;    // what the probabilities are relative to: a largest logit's exponent + log2 of a scale's
-    float sum = 0.0f;         // this lane's part of the row's sum
-    // a new reference from logits up to z and value scales up to v (this row's largest); returns what
-    // the sums so far are to be multiplied by
-    __device__ float raise(float z, float v, float zf) {
-        const float top = fmaxf(limit - kSlack / zf, z);
-        // scales count from 2^-60 up, so that the probabilities' sum stays in range
-        const int e = max(int(__float_as_uint(v) >> 23) - 126, -60);
-        const float scale = fmaxf(vlimit * (1.0f / kScaleSlack), ldexpf(1.0f, e));
-        limit = top + kSlack / zf;
-        vlimit = scale * kScaleSlack;
-        const float now = top == -INFINITY ? -INFINITY : top * zf + __builtin_amdgcn_logf(scale);
+    static constexpr float kTop = 5.0f, kMaxWeight = 32768.0f, kMaxP = 0x1p+90f, kMinScale = 0x1p-80f;
+    float ref = -INFINITY;
+    float sum = 0.0f;  // this lane's part of the row's sum
+    // what logits (base 2) are relative to; before the first reference so low that any logit calls for one
+    __device__ float base() const { return fmaxf(ref, -3e38f); }
+    // a new reference from the row's largest log2 of a weight; returns what the sums so far are to be multiplied by
+    __device__ float raise(float top) {
+        const float now = fmaxf(ref, top - kTop);
         const float f = ref == -INFINITY ? 0.0f : exp2_fast(ref - now);
         ref = now;
         sum *= f;
@@ -227,11 +224,57 @@ struct Running {
     }
 };
 
-// The probability operands of one step: weights p vs as f16.
-template <int D>
-__device__ inline uint4 weights(const float (&p)[2][4], const float (&vs)[2][kv4_blocks(D)][4], int b) {
-    return make_uint4(pack_f16(p[0][0] * vs[0][b][0], p[0][1] * vs[0][b][1]), pack_f16(p[0][2] * vs[0][b][2], p[0][3] * vs[0][b][3]),
-                      pack_f16(p[1][0] * vs[1][b][0], p[1][1] * vs[1][b][1]), pack_f16(p[1][2] * vs[1][b][2], p[1][3] * vs[1][b][3]));
+// One step's probabilities and weights of a row: z (logits before the factor zf,
+// -inf where masked), vs (0 where masked).  scale(f) multiplies the output sums so far.
+template <int NB, typename F>
+__device__ inline void weigh(Running& run, const float (&z)[2][4], float zf, const float (&vs)[2][NB][4], float (&p)[2][4],
+                             float (&w)[2][NB][4], F&& scale) {
+    auto compute = [&]() {
+        const float base = run.base();
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                p[c][i] = exp2_fast(fmaf(z[c][i], zf, -base));
+#pragma unroll
+                for (int b = 0; b < NB; ++b) w[c][b][i] = p[c][i] * vs[c][b][i];
+            }
+    };
+    compute();
+    float pm = 0.0f, wm = 0.0f;
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            pm = fmaxf(pm, p[c][i]);
+#pragma unroll
+            for (int b = 0; b < NB; ++b) wm = fmaxf(wm, w[c][b][i]);
+        }
+    if (__any(pm > Running::kMaxP || wm > Running::kMaxWeight)) {
+        float top = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float v = Running::kMinScale;
+#pragma unroll
+                for (int b = 0; b < NB; ++b) v = fmaxf(v, vs[c][b][i]);
+                top = fmaxf(top, fmaf(z[c][i], zf, __builtin_amdgcn_logf(v)));
+            }
+        scale(run.raise(row_max(top)));
+        compute();
+    }
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) run.sum += p[c][i];
+}
+
+// The weights of a block as an operand of the second product.
+template <int NB>
+__device__ inline uint4 weights(const float (&w)[2][NB][4], int b) {
+    return make_uint4(pack_f16(w[0][b][0], w[0][b][1]), pack_f16(w[0][b][2], w[0][b][3]),
+                      pack_f16(w[1][b][0], w[1][b][1]), pack_f16(w[1][b][2], w[1][b][3]));
 }
 
 constexpr uint32_t kOnes = 0x3C003C00u;  // two f16 ones
@@ -350,37 +393,18 @@ __global__ __launch_bounds__(256, D == 256 ? 2 : D == 128 ? 3 : 4) void kv4_atte
                     for (int b = 0; b < NB; ++b) vs[c][b][i] = seen ? vs[c][b][i] : 0.0f;
                 }
         }
-        // new references where a logit or a value scale exceeds the old ones
-        float zm = z[0][0], vm = vs[0][0][0];
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                zm = fmaxf(zm, z[c][i]);
-#pragma unroll
-                for (int b = 0; b < NB; ++b) vm = fmaxf(vm, vs[c][b][i]);
-            }
-        if (__any(zm > run.limit || vm > run.vlimit)) {
-            const float f = run.raise(row_max(zm), row_max(vm), zf);
+        float p[2][4], w[2][NB][4];
+        weigh<NB>(run, z, zf, vs, p, w, [&](float f) {
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
                 ps[b] *= f;
 #pragma unroll
                 for (int i = 0; i < CH; ++i) acc[b][i] *= f;
             }
-        }
-        const float base = run.ref == -INFINITY ? 0.0f : run.ref;
-        float p[2][4];
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                p[c][i] = exp2_fast(fmaf(z[c][i], zf, -base));
-                run.sum += p[c][i];
-            }
+        });
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-            const uint4 pw = weights<D>(p, vs, b);
+            const uint4 pw = weights<NB>(w, b);
             ps[b] = mfma(make_uint4(kOnes, kOnes, kOnes, kOnes), pw, ps[b]);
 #pragma unroll
             for (int h = 0; h < CH / 4; ++h) {
@@ -749,36 +773,18 @@ __global__ __launch_bounds__(256, D == 256 ? 2 : 4) void kv4_rows_kernel(Kv4Atte
                         for (int b = 0; b < NB; ++b) vs[c][b][i] = seen ? vs[c][b][i] : 0.0f;
                     }
             }
-            float zm = z[0][0], vm = 0.0f;
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    zm = fmaxf(zm, z[c][i]);
-#pragma unroll
-                    for (int b = 0; b < NB; ++b) vm = fmaxf(vm, vs[c][b][i]);
-                }
-            if (__any(zm > run.limit || vm > run.vlimit)) {
-                const float f = run.raise(row_max(zm), row_max(vm), zf);
+            float p[2][4], w[2][NB][4];
+            weigh<NB>(run, z, zf, vs, p, w, [&](float f) {
 #pragma unroll
                 for (int b = 0; b < NB; ++b) {
                     ps[b] *= f;
 #pragma unroll
                     for (int i = 0; i < CH; ++i) acc[b][i] *= f;
                 }
-            }
-            const float base = run.ref == -INFINITY ? 0.0f : run.ref;
-            float p[2][4];
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    p[c][i] = exp2_fast(fmaf(z[c][i], zf, -base));
-                    run.sum += p[c][i];
-                }
+            });
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
-                const uint4 pw = weights<D>(p, vs, b);
+                const uint4 pw = weights<NB>(w, b);
                 ps[b] = mfma(make_uint4(kOnes, kOnes, kOnes, kOnes), pw, ps[b]);
 #pragma unroll
                 for (int i = 0; i < CH; ++i) acc[b][i] = mfma(st.v[sub][b * CH + i][lane], pw, acc[b][i]);
