@@ -495,6 +495,8 @@ size_t kv4_pool_bytes(int64_t pages, int64_t page_size, int64_t kv_heads, int64_
  *   q_out      device, [tokens][heads * head_dim] of dtype, 16-byte aligned.
  * Keys (after the rotation, in FP32) and values are quantized round-to-nearest:
  *   s = fl32(max|x| / 7), q = clamp(round_half_even(fl32(x / s)), -8, 7), 0 if s == 0.
+ * A group that holds a NaN or an infinity is stored as NaN, all its channels
+ * (and no others).
  * Returns W4A16_OK (also for tokens == 0), W4A16_EINVAL, W4A16_EUNSUPPORTED or W4A16_EHIP.
  */
 w4a16_status_t kv4_append(const void* qkv, w4a16_dtype_t dtype, int64_t tokens, int64_t ldqkv, int64_t heads,

@@ -206,7 +206,8 @@ def kv4_append(qkv: torch.Tensor, pool: torch.Tensor, slots: torch.Tensor, head_
     int64 (page * page_size + token; outside the pool, -1 say: not stored),
     rotated by ``rope`` (rope_table) at ``positions`` [tokens] int32 and
     quantized to 4 bits; returns the rotated queries [tokens, heads, head_dim].
-    Without ``rope`` nothing is rotated and positions are not read.
+    Without ``rope`` nothing is rotated and positions are not read.  A group
+    of channels with a NaN or an infinity reads back as NaN.
     See kv4_append in include/w4a16.h."""
     plan = _append_plan(_meta(qkv), _meta(pool), _meta(slots), head_dim, _meta(rope),
                         None if rope is None else _meta(positions), _meta(q_out))

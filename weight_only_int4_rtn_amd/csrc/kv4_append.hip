@@ -115,14 +115,17 @@ __global__ __launch_bounds__(256) void kv4_append_kernel(Kv4AppendArgs a, int pa
         }
         const int64_t slot = a.slots[t];
 
-        // largest magnitude of each block, over the head's lanes
+        // largest magnitude of each block, over the head's lanes; one that is not finite leaves +inf (the
+        // maximum of floats drops NaN, and its code would read back as an ordinary number)
         const int ba = 8 * oa / W, bb = 8 * ob / W;
         float amax[NB];
 #pragma unroll
         for (int b = 0; b < NB; ++b) amax[b] = 0.0f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float x = fabsf(v[0][i]), y = fabsf(v[1][i]);
+            float x = fabsf(v[0][i]), y = fabsf(v[1][i]);
+            x = x < INFINITY ? x : INFINITY;
+            y = y < INFINITY ? y : INFINITY;
             if constexpr (NB == 1) {
                 amax[0] = fmaxf(amax[0], fmaxf(x, y));
             } else {
@@ -140,7 +143,7 @@ __global__ __launch_bounds__(256) void kv4_append_kernel(Kv4AppendArgs a, int pa
         if (!(known && slot >= 0 && slot < a.pages * a.page)) continue;
         float scale[NB];
 #pragma unroll
-        for (int b = 0; b < NB; ++b) scale[b] = amax[b] / 7.0f;
+        for (int b = 0; b < NB; ++b) scale[b] = amax[b] < INFINITY ? amax[b] / 7.0f : __uint_as_float(0x7FC00000u);
 
         const int64_t pg = slot / a.page;
         const int tok = int(slot - pg * a.page);
