@@ -583,7 +583,8 @@ size_t lora_add_workspace_bytes(int64_t m, int64_t n, int64_t k, int64_t adapter
  *            itself (same ld), else they must not overlap.
  *   workspace  as w4a16_linear's.
  * Sums are FP32; the product with A enters the second one with at least 16
- * significant bits; one rounding, of out.
+ * significant bits (for F16 of components down to 2^-22 of the row's largest,
+ * an absolute error of 2^-39 of the largest below); one rounding, of out.
  * Returns W4A16_OK (also for m == 0 or n == 0), W4A16_EINVAL,
  * W4A16_EUNSUPPORTED, W4A16_EWORKSPACE or W4A16_EHIP.
  */

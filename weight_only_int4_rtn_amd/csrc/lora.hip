@@ -63,8 +63,11 @@ __device__ inline int nth_bit(uint64_t mask, int n) {
 }
 
 // One row's t (this lane's channels of it) as MFMA operands: a high and a low
-// 16-bit part (16 or more significant bits in all), scaled by 2^-e so that f16
-// neither overflows nor loses bits.  Returns e.
+// 16-bit part, scaled by 2^-e so that the row's largest lies in [1, 2) for bf16
+// and in [2^14, 2^15) for f16, near the top of its range: the low parts of small
+// channels then keep 16 or more significant bits together with the high ones, in
+// bf16 at any size, in f16 down to 2^-22 of the row's largest, whose 2^-38 is
+// f16's smallest step (with the largest at 1, 12.6 bits at 2^-14).  Returns e.
 template <int ACT, int RS>  // RS: 32-wide steps of the rank
 __device__ inline int operands_of(const float (&v)[RS][8], uint4 (&hi)[RS], uint4 (&lo)[RS]) {
     float big = 0.0f;
@@ -73,7 +76,7 @@ __device__ inline int operands_of(const float (&v)[RS][8], uint4 (&hi)[RS], uint
 #pragma unroll
         for (int i = 0; i < 8; ++i) big = fmaxf(big, fabsf(v[s][i]));
     big = max_xor32(fmaxf(big, lane_xor<16>(big)));
-    const int e = big > 0.0f && big < 3e38f ? int(__float_as_uint(big) >> 23) - 127 : 0;
+    const int e = big > 0.0f && big < INFINITY ? int(__float_as_uint(big) >> 23) - 127 - (ACT == kActF16 ? 14 : 0) : 0;
 #pragma unroll
     for (int s = 0; s < RS; ++s) {
         uint32_t h[4], w[4];
