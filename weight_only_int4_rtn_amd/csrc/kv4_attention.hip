@@ -177,7 +177,7 @@ __device__ inline float load_queries(const uint16_t* src, float scale, uint4 (&q
                 big = fmaxf(big, fmaxf(fabsf(to_f32<ACT>(uint16_t(w[i]))), fabsf(to_f32<ACT>(uint16_t(w[i] >> 16)))));
         }
     big = row_max(big);
-    const int e = big > 0.0f && big < 3e38f ? 10 - (int(__float_as_uint(big) >> 23) - 127) : 0;
+    const int e = big > 0.0f && big < INFINITY ? 10 - (int(__float_as_uint(big) >> 23) - 127) : 0;
     const float sign = scale < 0.0f ? -1.0f : 1.0f;  // the logits' factor is positive
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
