@@ -102,9 +102,10 @@ def _device_index(first, *others) -> int:
 
 
 def _no_grad(*ts):
+    """Refuses inputs and outputs of a graph that autograd would record; parameters are taken under no_grad."""
     for t in ts:
-        if t is not None and t.requires_grad:
-            raise ValueError("inference only: autograd inputs are not supported")
+        if t is not None and t.requires_grad and torch.is_grad_enabled():
+            raise ValueError("inference only: autograd inputs are not supported (call it under torch.no_grad())")
 
 
 # ---------------------------------------------------------------------------
@@ -212,7 +213,7 @@ def kv4_append(qkv: torch.Tensor, pool: torch.Tensor, slots: torch.Tensor, head_
     plan = _append_plan(_meta(qkv), _meta(pool), _meta(slots), head_dim, _meta(rope),
                         None if rope is None else _meta(positions), _meta(q_out))
     tag, tokens, ld, heads, kv_heads, rope_len, rot, pages, page = plan
-    _no_grad(qkv)
+    _no_grad(qkv, rope, q_out)
     index = _device_index(qkv, pool, slots, positions if rope is not None else None, rope, q_out)
     if q_out is None:
         q_out = qkv.new_empty((tokens, heads, head_dim))
@@ -324,7 +325,7 @@ def kv4_attention(q: torch.Tensor, pool: torch.Tensor, block_table: torch.Tensor
     causal = 1 if causal else 0
     plan = _attention_plan(_meta(q), _meta(pool), _meta(block_table), _meta(kv_lens), _meta(cu_q), _meta(out), causal, window)
     tag, tokens, ldq, heads, kv_heads, dim, pages, page, width, ldt, batch, window, need = plan
-    _no_grad(q)
+    _no_grad(q, out)
     index = _device_index(q, pool, block_table, kv_lens, cu_q, out, workspace)
     if out is None:
         out = q.new_empty((tokens, heads, dim))
@@ -401,7 +402,7 @@ def lora_add(y: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor,
         got = lora_add(y2, x, a, b, index, scales=scales, out=out2, workspace=workspace)
         return out if out is not None else got.view(y.shape)
     tag, m, k, ldx, adapters, rank, n, ldy, ldo, need = plan
-    _no_grad(x, y, a, b, scales)
+    _no_grad(x, y, a, b, scales, out)
     device = _device_index(x, y, a, b, index, scales, out, workspace)
     if out is None:
         out = y.new_empty((m, n))
