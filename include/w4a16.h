@@ -493,6 +493,7 @@ size_t kv4_pool_bytes(int64_t pages, int64_t page_size, int64_t kv_heads, int64_
  *              Two tokens of a call must not share a slot.
  *   pool       device, kv4_pool_bytes(...) bytes, 16-byte aligned.
  *   q_out      device, [tokens][heads * head_dim] of dtype, 16-byte aligned.
+ * At most 2^23 tokens a call, here and in kv4_read.
  * Keys (after the rotation, in FP32) and values are quantized round-to-nearest:
  *   s = fl32(max|x| / 7), q = clamp(round_half_even(fl32(x / s)), -8, 7), 0 if s == 0.
  * A group that holds a NaN or an infinity is stored as NaN, all its channels
@@ -553,6 +554,8 @@ int kv4_attention_tile_rows(int64_t tokens, int64_t batch, int64_t heads, int64_
  *   out        device, [tokens][ldo] of dtype, 16-byte aligned, ldo a
  *              multiple of 8.  A query that sees nothing gives zeros.
  *   workspace  as w4a16_linear's.
+ * At most 2^26 query tokens times heads, 2^20 requests and fewer than 2^28
+ * tokens of a request (table_width * page_size).
  * Logits, softmax and sums are FP32.  Each probability times its value's scale
  * enters the second product as f16: 11 bits of those down to 2^-19 of the row's
  * largest such weight, an absolute error of 2^-30 of the largest below.  For an

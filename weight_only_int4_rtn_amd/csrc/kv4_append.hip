@@ -48,7 +48,7 @@ __device__ inline uint4 narrow8(const float v[8]) {
 // tokens of a chunk are usually neighbours, and their words and half-words,
 // which interleave in the same cache lines, then reach memory as whole lines
 // from one L2.  The angles stay in registers over the heads.  HBM bounds it: 8192
-// tokens of 48 heads of 128 channels, 186 MB, take 42 us, 4.4 TB/s, where a large
+// tokens of 48 heads of 128 channels, 181 MB, take 43 us, 4.2 TB/s, where a large
 // copy reaches 4.8 (one workgroup a token, each thread one octet: 99 us, its
 // lines written back in parts by several XCDs' L2s).
 template <int ACT, int D>
@@ -184,8 +184,9 @@ __global__ __launch_bounds__(256) void kv4_append_kernel(Kv4AppendArgs a, int pa
 }
 
 // A thread reads 8 channels of one head of one token of both sides (8192 tokens
-// of 8 heads of 128: 13 us, its 34 MB of output at 2.6 TB/s; 14 us with one
-// token a workgroup).
+// of 8 heads of 128: 12 us for 43 MB, 3.5 TB/s; 14 us with one token a
+// workgroup).  Its loads of 4 and 2 bytes, gathered from the chunks, hold it below
+// a copy's rate.
 template <int DT, int D>  // DT: 0 = f32, 1 = bf16, 2 = f16
 __global__ __launch_bounds__(256) void kv4_read_kernel(Kv4ReadArgs a, int tokens) {
     constexpr int W = kv4_width(D), NB = kv4_blocks(D);

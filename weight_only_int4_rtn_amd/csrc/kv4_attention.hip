@@ -581,8 +581,10 @@ __global__ __launch_bounds__(256, D == 256 ? 2 : D == 128 ? 3 : 4) void kv4_atte
 // loaded a step before that.  32 rows a wave halve the operand reads but leave
 // registers for two waves a SIMD instead of four, which costs more (16 x 64
 // queries on 1000 tokens, D = 128: 54 us against 44; prompt of 4096: 205 against
-// 193).  What bounds it is the issue of instructions: of 200 us, with 29 % of
-// the cycles in matrix and 57 % in vector instructions, copies that leave
+// 193).  What bounds it is the issue of instructions: over a prompt of 4096 (186
+// to 212 us) matrix units are busy 30 % of the cycles and vector units 65 %, and
+// beside 70.7 M vector (9.0 M of them matrix) and 13.1 M LDS instructions stand
+// 34.1 M scalar ones, mostly chunk addresses and mask bounds; copies that leave
 // out the staging, the exponentials or the products each save what those cost.
 // ---------------------------------------------------------------------------
 template <int D>
@@ -925,11 +927,18 @@ Kv4Plan plan_kv4_attention(int64_t tokens, int64_t batch, int heads, int kv_head
     };
     // Tiles of 64 rows share the codes' conversion but have fewer workgroups to
     // spread over the chip: they lead where a request has 16 rows or more and the
-    // call 4 M pairs of a row and a token (D = 128, one request: 128 queries x 32
-    // heads on 1024 tokens 17 us against 20 on tiles of 16, 50 queries 16 against
-    // 13; D = 64: 512 x 16 on 512 11 against 12, 50 x 16 on 1074 12 against 10; D =
-    // 256: 1024 x 8 on 1024 even, 512 x 8 on 512 20 against 16).
-    // (their grid is one line of tiles and key heads, which has to fit)
+    // call 4 M pairs of a row and a token.  us on tiles of 64 against 16, queries x
+    // heads / key heads on tokens, with the pairs in M:
+    //   D = 128  128 x 32/8 on 1024 (4.2) 17 against 20, 200 x 32/8 on 700 (4.5) 16
+    //            against 21, 512 x 8/8 on 1024 (4.2) 16 against 20, 50 x 32/8 on 1024
+    //            (1.6) 16 against 13; but 64 x 32/8 on 2048 (4.2) 21 against 19
+    //   D = 64   256 x 16/16 on 1024 (4.2) 12.5 against 14.2, 50 x 16/16 on 1074 (0.9)
+    //            12 against 10
+    //   D = 256  512 x 8/1 on 1024 (4.2) 25 against 29, 768 x 8/1 on 1024 (6.3) 29
+    //            against 34, 1024 x 8/1 on 1024 (8.4) 29 against 28, 512 x 8/1 on 512
+    //            (2.1) 20 against 17; but 128 x 8/1 on 4096 (4.2) 42 against 25: few
+    //            rows on long requests are better off on tiles of 16
+    // (the grid of tiles of 64 is one line of tiles and key heads, which has to fit)
     if (ragged && tokens * share >= 16 * batch && tokens * heads * reach(64) >= int64_t(1) << 22 &&
         (tokens * share / 64 + batch) * kv_heads < int64_t(1) << 23)
         p.rows = 64;
@@ -938,13 +947,17 @@ Kv4Plan plan_kv4_attention(int64_t tokens, int64_t batch, int heads, int kv_head
     // Splits: with few tiles as many as fill the chip once (768 workgroups of D
     // = 128; 4 x 131072 tokens: 111 us, twice as many 119, four times 131), else
     // twice over, as lengths may differ (64 x 0..8192 tokens: 92 us, once 100,
-    // four times 94).  A tile's splits share a counter of the workspace's header.
+    // four times 94).  Tiles of 64 rows count as three a CU though four of D = 64 and
+    // 128 fit: four measured no better (200 queries x 32/8 heads of 128 on 30000
+    // tokens 173 us, three 175; 4 x 128 on 4096 69 and 69; D = 64: 300 x 8/1 on
+    // 30000 60 and 57).  A tile's splits share a counter of the workspace's header.
     const int64_t base = p.tiles * kv_heads;
     const int64_t room = 256 * (dim == 256 ? 2 : dim == 128 || p.rows > 16 ? 3 : 4);
     const int64_t want = base >= int64_t(kSyncBytes / 4) ? 1 : 4 * base <= room ? room / (base > 0 ? base : 1) : ceil_div(2 * room, base);
     int64_t span = ceil_div(ceil_div(most, want), 128) * 128;
-    // Each part costs the join a read, each step of 128 tokens the walk a turn: at least sqrt(12 tokens) (one request of
-    // 30000 tokens, D = 128: 22 us in parts of 640, 29 in parts of 256), and 128, or 256 for tiles of many queries.
+    // Each part costs the join a read, each step of 128 tokens the walk a turn: at least sqrt(12 tokens), and 128, or 256
+    // for tiles of many queries.  us with sqrt of 3, 12 and 48 tokens: D = 128, 32/8 heads, one request of 2000 9.6, 8.7,
+    // 9.2, of 30000 26, 22, 22; D = 256, 8/1, of 4000 15, 13, 14, of 131072 54, 42, 48; D = 64, 16/16, of 30000 27, 24, 21.
     int64_t least = ragged ? 256 : 128;
     while (least * least < 12 * most) least += 128;
     if (span < least) span = least;

@@ -296,7 +296,8 @@ __device__ inline uint4 add_columns(uint4 y, f32x4_t lo, f32x4_t hi, float f) {
 // tile of TILE rows, z = slot.  A wave computes 64 columns of an adapter's rows,
 // gathered 16 to a product; the operands of B are read once a tile.  Latency
 // bounds the pair of launches: 64 rows, 48 adapters of rank 16, 4096 x 4096: 7 and
-// 8 us for 14 MB.
+// 8 us for 14 MB.  Part of it is each slot's way to its adapter, a ballot and a
+// lane read for every adapter of the tile before it, before its first load.
 template <int ACT, int RS, int TILE>
 __global__ __launch_bounds__(256) void lora_expand_kernel(LoraArgs a, int slots, int splits, const float* t) {
     const int lane = threadIdx.x % 64, wave = uniform(threadIdx.x / 64);
@@ -434,7 +435,9 @@ __global__ __launch_bounds__(512) void lora_one_kernel(LoraArgs a) {
 // each reading and writing the rows that are its own.  4099 rows by 32768
 // columns at rank 64, 537 MB of y and out, take 147 us, 3.7 TB/s, and the first
 // launch 23 (t turned into operands by every workgroup here: 200 and 19; 32 or 16
-// rows a wave 160 and 210, as B comes from the L2 once for each).
+// rows a wave 160 and 210, as B comes from the L2 once for each).  A wave
+// loads y and B of the next columns only after these are stored: nothing is in
+// flight meanwhile.
 constexpr int kTallCols = 512, kTallGroups = 4, kTallRows = 16 * kTallGroups;
 
 template <int ACT, int RS>
