@@ -55,7 +55,8 @@ typedef enum {
 typedef enum {
     W4A16_F32 = 0,
     W4A16_BF16 = 1,
-    W4A16_F16 = 2
+    W4A16_F16 = 2,
+    W4A16_E4M3 = 3           /* 8-bit floats (OCP e4m3, largest value 448): the input of fp8_linear only */
 } w4a16_dtype_t;
 
 /* Kernel families w4a16_linear chooses between (by M, N, K). */
@@ -597,6 +598,68 @@ w4a16_status_t lora_add(const void* x, w4a16_dtype_t dtype, int64_t m, int64_t k
                         const void* b, int64_t adapters, int64_t rank, int64_t n, const int32_t* index,
                         const float* scales, const void* y, int64_t ldy, void* out, int64_t ldo, void* workspace,
                         size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * The layer on 8-bit floats, for batches whose products are bound by
+ * arithmetic rather than by the weights' bytes (prompts, large decoding
+ * batches): weights and activations in e4m3, one FP32 scale per block of
+ * 128 x 128 weights and per row and 128 columns of the input.  Conventions as
+ * at the top of this file.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * codes[i][j] = e4m3(fl32(x[i][j] / s)), nearest, ties to even, with
+ * s = scales[i][j / 128] = fl32(max|x| / 448) over the row's 128 columns.
+ *   x       device, [m][ldx] of dtype (BF16 or F16), k columns (2k for SwiGLU);
+ *           16-byte aligned, ldx a multiple of 8.
+ *   act     activation applied to x first, rounded to dtype (w4a16_act_t).
+ *   k       a multiple of 128, at most 2^22; at most 2^30 groups in all.
+ *   codes   device, [m][k] bytes, 16-byte aligned.
+ *   scales  device, [m][k / 128] FP32.
+ * A group of zeros has scale 0 and codes 0; a group with a NaN or an infinity
+ * has a NaN scale and NaN codes.  Returns W4A16_OK (also for m == 0),
+ * W4A16_EINVAL, W4A16_EUNSUPPORTED or W4A16_EHIP.
+ */
+w4a16_status_t quantize_fp8_rows(const void* x, w4a16_dtype_t dtype, w4a16_act_t act, int64_t m, int64_t k, int64_t ldx,
+                                 void* codes, float* scales, void* stream);
+
+/*
+ * The same with one scale per block of 128 rows and 128 columns (the last rows'
+ * block may be smaller), for weights: w [n][ldw] of dtype F32, BF16 or F16,
+ * rows 16-byte aligned; codes [n][k], scales [ceil(n / 128)][k / 128].
+ */
+w4a16_status_t quantize_fp8_blocks(const void* w, w4a16_dtype_t dtype, int64_t n, int64_t k, int64_t ldw, void* codes,
+                                   float* scales, void* stream);
+
+/*
+ * Workspace bytes of fp8_linear (0: none needed, or invalid or empty sizes);
+ * header rules as w4a16_linear's.  x_dtype BF16 or F16: room for the quantized
+ * input is included.
+ */
+size_t fp8_linear_workspace_bytes(w4a16_dtype_t x_dtype, int64_t m, int64_t n, int64_t k);
+
+/*
+ * y = x W^T (+ bias) with W = codes w times their block's scale.
+ *   x         device, [m][ldx], k columns; 16-byte aligned rows.  Of BF16 or F16:
+ *             act is applied (SwiGLU rows hold [up | gate], 2k columns) and the
+ *             result quantized as by quantize_fp8_rows; x_scales is NULL.  Of
+ *             E4M3: codes already, with x_scales [m][k / 128] FP32, and no act.
+ *   w         device, [n][k] e4m3 codes, 16-byte aligned.
+ *   w_scales  device, [ceil(n / 128)][k / 128] FP32.
+ *   bias      device, [n] of y_dtype, or NULL.
+ *   y         device, [m][ldy] of y_dtype (BF16 or F16; x's for 16-bit x).
+ * k is a multiple of 128, at most 2^22.  Sums over the groups of 128 columns are
+ * FP32, scaled by both scales (their product, which has to lie in FP32's normal
+ * range to keep its precision); within a group the matrix instruction adds eight
+ * neighbouring products at a time, each cut 2^-13 below the largest's exponent,
+ * in all 1e-5 to 7e-5 of the result.  The bias is added in FP32, before the one
+ * rounding.  A NaN scale or code makes the outputs it enters NaN.
+ * Returns W4A16_OK (also for m == 0 or n == 0), W4A16_EINVAL,
+ * W4A16_EUNSUPPORTED, W4A16_EWORKSPACE or W4A16_EHIP.
+ */
+w4a16_status_t fp8_linear(const void* x, w4a16_dtype_t x_dtype, const float* x_scales, w4a16_act_t act, int64_t m, int64_t k,
+                          int64_t ldx, const void* w, const float* w_scales, int64_t n, const void* bias, void* y,
+                          w4a16_dtype_t y_dtype, int64_t ldy, void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

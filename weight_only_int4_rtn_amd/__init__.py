@@ -16,6 +16,11 @@ INT8 weights (W8A16) take the same calls with the 8-bit quantizer:
     packed8 = pack_int8(codes8, scales8)
     y = linear(x, packed8, n, bias, bits=8)
 
+For many rows (prompts, large decoding batches) the layer on 8-bit floats:
+
+    codes, scales = quantize_fp8_weight(w)                     # load time; one scale per 128 x 128 weights
+    y = linear_fp8(x, codes, scales, bias)                     # x quantized per row and 128 columns
+
 Around the projections of a decoder layer, in serving:
 
     pool = kv4_pool(pages, page_size, kv_heads, head_dim)      # keys and values in 4 bits
@@ -48,6 +53,12 @@ from ._binding import (  # noqa: F401
     unpack_int8,
     update_,
     workspace_bytes,
+)
+from ._fp8 import (  # noqa: F401
+    linear_fp8,
+    linear_fp8_workspace_bytes,
+    quantize_fp8,
+    quantize_fp8_weight,
 )
 from ._serving import (  # noqa: F401
     kv4_append,

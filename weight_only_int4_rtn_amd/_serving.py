@@ -101,6 +101,23 @@ def _device_index(first, *others) -> int:
     return index
 
 
+class _on_device:
+    """The current device while a call launches on tensors of another one."""
+    __slots__ = ("index", "before")
+
+    def __init__(self, index):
+        self.index = index
+
+    def __enter__(self):
+        self.before = torch._C._cuda_getDevice()
+        if self.before != self.index:
+            torch.cuda.set_device(self.index)
+
+    def __exit__(self, *_):
+        if self.before != self.index:
+            torch.cuda.set_device(self.before)
+
+
 def _no_grad(*ts):
     """Refuses inputs and outputs of a graph that autograd would record; parameters are taken under no_grad."""
     for t in ts:
