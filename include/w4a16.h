@@ -571,6 +571,37 @@ w4a16_status_t kv4_attention(const void* q, w4a16_dtype_t dtype, int64_t tokens,
                              const int32_t* cu_q, int64_t batch, int causal, int64_t window, float scale, void* out,
                              int64_t ldo, void* workspace, size_t workspace_bytes, void* stream);
 
+/* Workspace bytes of kv4_prefix_attention (0: invalid or empty sizes); header rules as above. */
+size_t kv4_prefix_attention_workspace_bytes(int64_t tokens, int64_t batch, int64_t groups, int64_t heads, int64_t kv_heads,
+                                            int64_t head_dim, int64_t prefix_width, int64_t table_width, int64_t page_size,
+                                            int ragged, int causal);
+
+/*
+ * kv4_attention for requests that begin with the same tokens: group j's
+ * requests share the prefix_lens[j] tokens on the pages prefix_table[j], which
+ * are met once for all of the group's queries; table and kv_lens hold what each
+ * request has beyond them.  Every query sees its group's whole prefix, and of
+ * its request's own tokens what kv4_attention shows it (no window).
+ *   prefix_table  device, [groups][ldp] int32, ldp >= prefix_width, as table.
+ *   prefix_lens   device, [groups] int32; taken as at least 0 and at most
+ *                 prefix_width * page_size.
+ *   cu_groups     device, [groups + 1] int32: group j's requests are
+ *                 cu_groups[j] .. cu_groups[j + 1] - 1, not decreasing; a
+ *                 request before the first or behind the last has no prefix.
+ *                 NULL: one group of all requests (groups == 1).
+ *   kv_lens       tokens of the request beyond the prefix, its query tokens
+ *                 among them; may be 0 for a query token that is in the cache
+ *                 nowhere.  table_width is at least 1 also then.
+ * The other arguments, limits and roundings are kv4_attention's.  Two launches:
+ * the prefixes' sums pass through the workspace in FP32.
+ */
+w4a16_status_t kv4_prefix_attention(const void* q, w4a16_dtype_t dtype, int64_t tokens, int64_t ldq, int64_t heads,
+                                    int64_t kv_heads, int64_t head_dim, const void* pool, int64_t pages, int64_t page_size,
+                                    const int32_t* prefix_table, int64_t prefix_width, int64_t ldp, const int32_t* prefix_lens,
+                                    const int32_t* cu_groups, int64_t groups, const int32_t* table, int64_t table_width,
+                                    int64_t ldt, const int32_t* kv_lens, const int32_t* cu_q, int64_t batch, int causal,
+                                    float scale, void* out, int64_t ldo, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Workspace bytes of lora_add (0: none needed, or invalid or empty sizes); header rules as above. */
 size_t lora_add_workspace_bytes(int64_t m, int64_t n, int64_t k, int64_t adapters, int64_t rank);
 

@@ -27,6 +27,7 @@ Around the projections of a decoder layer, in serving:
     qkv = lora_add(linear(x, packed, n), x, a, b, index)       # adapters of many requests
     q = kv4_append(qkv, pool, slots, head_dim, positions, rope_table(length, rot_dim))
     o = kv4_attention(q, pool, block_table, kv_lens)           # decode, prompts with cu_q=
+    o = kv4_prefix_attention(q, pool, prefix_table, prefix_lens, block_table, kv_lens)   # requests on one prefix
 """
 import torch  # noqa: F401  (load torch's HIP runtime before the library)
 
@@ -67,6 +68,8 @@ from ._serving import (  # noqa: F401
     kv4_attention_workspace_bytes,
     kv4_page_size,
     kv4_pool,
+    kv4_prefix_attention,
+    kv4_prefix_attention_workspace_bytes,
     kv4_read,
     lora_add,
     lora_add_workspace_bytes,

@@ -34,6 +34,11 @@ def _lib():
         L.kv4_attention.argtypes = [vp, i32, i64, i64, i64, i64, i64, vp, i64, i64, vp, i64, i64, vp, vp, i64, i32, i64,
                                     ctypes.c_float, vp, i64, vp, sz, vp]
         L.kv4_attention.restype = i32
+        L.kv4_prefix_attention_workspace_bytes.argtypes = [i64] * 9 + [i32, i32]
+        L.kv4_prefix_attention_workspace_bytes.restype = sz
+        L.kv4_prefix_attention.argtypes = [vp, i32, i64, i64, i64, i64, i64, vp, i64, i64, vp, i64, i64, vp, vp, i64, vp, i64, i64,
+                                           vp, vp, i64, i32, ctypes.c_float, vp, i64, vp, sz, vp]
+        L.kv4_prefix_attention.restype = i32
         L.lora_add_workspace_bytes.argtypes = [i64] * 5
         L.lora_add_workspace_bytes.restype = sz
         L.lora_add.argtypes = [vp, i32, i64, i64, i64, vp, vp, i64, i64, i64, vp, vp, vp, i64, vp, i64, vp, sz, vp]
@@ -354,6 +359,71 @@ def kv4_attention(q: torch.Tensor, pool: torch.Tensor, block_table: torch.Tensor
                               ws_bytes, stream)
     if st:
         _check(st, "kv4_attention")
+    return out
+
+
+@_remember
+def _prefix_need(*sizes) -> int:
+    return int(_lib().kv4_prefix_attention_workspace_bytes(*sizes))
+
+
+def kv4_prefix_attention_workspace_bytes(tokens: int, batch: int, groups: int, heads: int, kv_heads: int, head_dim: int,
+                                         prefix_width: int, table_width: int, page_size: int, ragged: bool = False,
+                                         causal: bool = True) -> int:
+    """Workspace kv4_prefix_attention needs for these sizes (``ragged``: cu_q is given)."""
+    return _prefix_need(tokens, batch, groups, heads, kv_heads, head_dim, prefix_width, table_width, page_size, int(bool(ragged)),
+                        int(bool(causal)))
+
+
+@_remember
+def _prefix_plan(q, pool, prefix_table, prefix_lens, table, kv_lens, cu_q, cu_groups, out, causal):
+    """kv4_attention's plan of the own part (its need aside), and the prefixes' sizes."""
+    own = _attention_plan(q, pool, table, kv_lens, cu_q, out, causal, 0)
+    if prefix_table[2] != torch.int32 or len(prefix_table[0]) != 2 or prefix_table[0][1] < 1 or prefix_table[1][1] != 1:
+        raise ValueError("prefix_table must be an int32 [groups, width] tensor with contiguous rows")
+    groups, width = prefix_table[0]
+    _vector(prefix_lens, torch.int32, groups, "prefix_lens")
+    if cu_groups is not None:
+        _vector(cu_groups, torch.int32, groups + 1, "cu_groups")
+    elif groups != 1:
+        raise ValueError(f"{groups} prefixes: pass cu_groups")
+    tokens, heads, dim = q[0]
+    kv_heads, batch, page = pool[0][1], table[0][0], own[7]
+    need = _prefix_need(tokens, batch, groups, heads, kv_heads, dim, width, table[0][1], page, 0 if cu_q is None else 1, causal)
+    return own[:-2], groups, width, prefix_table[1][0] if groups > 1 else width, need
+
+
+def kv4_prefix_attention(q: torch.Tensor, pool: torch.Tensor, prefix_table: torch.Tensor, prefix_lens: torch.Tensor,
+                         block_table: torch.Tensor, kv_lens: torch.Tensor, cu_q: torch.Tensor | None = None,
+                         cu_groups: torch.Tensor | None = None, causal: bool = True, scale: float | None = None,
+                         out: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """``kv4_attention`` for requests that share a prefix, which is read once for
+    all of them.  ``prefix_table`` [groups, width] int32 and ``prefix_lens``
+    [groups] int32 hold each group's pages and tokens, ``cu_groups`` [groups + 1]
+    int32 where its requests begin (None: one group of all requests);
+    ``block_table`` and ``kv_lens`` hold each request's tokens beyond the prefix.
+    Every query sees the whole prefix.  See kv4_prefix_attention in
+    include/w4a16.h."""
+    causal = 1 if causal else 0
+    plan = _prefix_plan(_meta(q), _meta(pool), _meta(prefix_table), _meta(prefix_lens), _meta(block_table), _meta(kv_lens), _meta(cu_q),
+                        _meta(cu_groups), _meta(out), causal)
+    (tag, tokens, ldq, heads, kv_heads, dim, pages, page, width, ldt, batch), groups, prefix_width, ldp, need = plan
+    _no_grad(q, out)
+    index = _device_index(q, pool, prefix_table, prefix_lens, block_table, kv_lens, cu_q, cu_groups, out, workspace)
+    if out is None:
+        out = q.new_empty((tokens, heads, dim))
+    if tokens == 0:
+        return out
+    stream = _raw_stream(index)
+    ws, ws_bytes = _workspace(workspace, need, index, stream)
+    with _on_device(index):
+        st = _lib().kv4_prefix_attention(q.data_ptr(), tag, tokens, ldq, heads, kv_heads, dim, pool.data_ptr(), pages, page,
+                                         prefix_table.data_ptr(), prefix_width, ldp, prefix_lens.data_ptr(),
+                                         None if cu_groups is None else cu_groups.data_ptr(), groups, block_table.data_ptr(), width, ldt,
+                                         kv_lens.data_ptr(), None if cu_q is None else cu_q.data_ptr(), batch, causal,
+                                         dim ** -0.5 if scale is None else scale, out.data_ptr(), heads * dim, ws, ws_bytes, stream)
+    if st:
+        _check(st, "kv4_prefix_attention")
     return out
 
 

@@ -135,6 +135,10 @@ struct Kv4AttentionArgs {
     uint16_t* out;
     int64_t ldo;
     void* workspace;
+    // of a shared prefix (below) only
+    const int32_t* cu_groups;  // null: one group of all requests
+    int64_t groups;
+    float* parts;  // [tokens][heads] rows: sums of dim channels, then [tokens][heads][2] references and sums of probabilities
 };
 
 struct Kv4Plan {
@@ -147,5 +151,22 @@ struct Kv4Plan {
 Kv4Plan plan_kv4_attention(int64_t tokens, int64_t batch, int heads, int kv_heads, int dim, int64_t capacity,
                            bool ragged, bool causal, int64_t window);
 hipError_t launch_kv4_attention(const Kv4AttentionArgs& a, int act, hipStream_t stream);
+
+// A shared prefix: one launch over the prefixes, whose "requests" are groups of
+// requests (table, table_width, ldt, kv_lens of the prefixes), then one over the
+// requests' own tokens, which joins both.
+struct Kv4PrefixArgs {
+    Kv4AttentionArgs own;
+    const int32_t* table;
+    int64_t table_width, ldt;
+    const int32_t* lens;
+};
+struct Kv4PrefixPlan {
+    Kv4Plan prefix, own;
+    size_t parts, workspace;  // after the header: the prefixes' rows, then the larger plan's
+};
+Kv4PrefixPlan plan_kv4_prefix(int64_t tokens, int64_t batch, int64_t groups, int heads, int kv_heads, int dim,
+                              int64_t prefix_capacity, int64_t capacity, bool ragged, bool causal);
+hipError_t launch_kv4_prefix(const Kv4PrefixArgs& a, int act, hipStream_t stream);
 
 }  // namespace w4a16

@@ -61,28 +61,45 @@ struct View {
     }
 };
 
+// What a launch computes: a whole attention, the part of it over the groups'
+// shared prefixes, or the part over the requests' own tokens, which takes the
+// other part in.
+enum Part { kWhole = 0, kPrefix = 1, kOwn = 2 };
+
+// First query token of group j (a request outside the batch is its end).
+__device__ inline int64_t group_start(const Kv4AttentionArgs& a, int64_t j) {
+    int64_t b = a.cu_groups ? a.cu_groups[j] : j ? a.batch : 0;
+    b = b < 0 ? 0 : b > a.batch ? a.batch : b;
+    return a.cu_q ? a.cu_q[b] : b;
+}
+
 // Tiles are numbered without a table: request b's start at
 // floor(cu_q[b] share / ROWS) + b, which leaves room for the ragged last tile
-// of every request (a few tiles stay empty).
-template <int ROWS>
+// of every request (a few tiles stay empty).  Over the prefixes a group takes a
+// request's place, with the queries of all its requests.
+template <int ROWS, int PART>
 __device__ inline bool find_tile(const Kv4AttentionArgs& a, int64_t x, Tile& t) {
     const int share = a.heads / a.kv_heads;
-    if (!a.cu_q) {
+    if (PART != kPrefix && !a.cu_q) {
         const int per = (share + ROWS - 1) / ROWS;
         t.b = int(x / per);
         t.q0 = t.b;
         t.qn = 1;
         t.r0 = int(x % per) * ROWS;
     } else {
-        int lo = 0, hi = int(a.batch) - 1;
+        auto first = [&](int64_t b) -> int64_t {
+            if constexpr (PART == kPrefix) return group_start(a, b);
+            else return a.cu_q[b];
+        };
+        int lo = 0, hi = int(PART == kPrefix ? a.groups : a.batch) - 1;
         while (lo < hi) {
             const int mid = (lo + hi + 1) / 2;
-            const int64_t start = int64_t(a.cu_q[mid]) * share / ROWS + mid;
+            const int64_t start = first(mid) * share / ROWS + mid;
             if (start <= x) lo = mid;
             else hi = mid - 1;
         }
         t.b = lo;
-        const int64_t c0 = a.cu_q[lo], c1 = a.cu_q[lo + 1];
+        const int64_t c0 = first(lo), c1 = first(lo + 1);
         t.q0 = c0 < 0 ? 0 : c0 > a.tokens ? a.tokens : c0;
         const int64_t q1 = c1 < t.q0 ? t.q0 : c1 > a.tokens ? a.tokens : c1;
         t.qn = int(q1 - t.q0);
@@ -155,6 +172,77 @@ struct Side {
         }
     }
 };
+
+// Where the parts of a row meet (kPrefix, kOwn): its sums over the prefix, one
+// channel a lane and register as the kernels hold them, and {reference, sum of
+// probabilities}.
+struct Meeting {
+    float *sums, *stats;
+    __device__ Meeting(const Kv4AttentionArgs& a, int64_t token, int head) {
+        const int64_t row = token * a.heads + head;
+        sums = a.parts + row * a.dim;
+        stats = a.parts + a.tokens * a.heads * a.dim + row * 2;
+    }
+};
+
+// Whether request b has a prefix's part to take in.
+__device__ inline bool in_group(const Kv4AttentionArgs& a, int b) {
+    return !a.cu_groups || (b >= a.cu_groups[0] && b < a.cu_groups[a.groups]);
+}
+
+// Takes the prefix's part into a row's sums of N consecutive channels at a time:
+// the factors of both parts.
+struct Taken {
+    float mine = 1.0f, other = 0.0f;
+    // ref, sum: of the own tokens; sum becomes that of both
+    __device__ void stats(const Meeting& m, float ref, float& sum) {
+        const float r = m.stats[0], s = m.stats[1];
+        const float top = fmaxf(ref, r);
+        mine = ref == -INFINITY ? 0.0f : exp2_fast(ref - top);
+        other = r == -INFINITY ? 0.0f : exp2_fast(r - top);
+        sum = sum * mine + s * other;
+    }
+    __device__ float operator()(float v, float prefix) const { return v * mine + prefix * other; }
+};
+
+// A row's sums over the prefix left for the own part: this lane's channels, CH
+// consecutive ones for each block and register.
+template <int D>
+__device__ inline void leave(const Meeting& m, const f32x4_t (&acc)[kv4_blocks(D)][kv4_width(D) / 16], float ref, float sum, int kq) {
+    constexpr int W = kv4_width(D), NB = kv4_blocks(D), CH = W / 16;
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int i = 0; i < CH; i += 4)
+                *reinterpret_cast<float4*>(m.sums + W * b + CH * (4 * kq + j) + i) =
+                    make_float4(acc[b][i][j], acc[b][i + 1][j], acc[b][i + 2][j], acc[b][i + 3][j]);
+    if (kq == 0) *reinterpret_cast<float2*>(m.stats) = make_float2(ref, sum);
+}
+
+// The prefix's part of a row joined to the own part's.
+template <int D>
+__device__ inline void take(const Kv4AttentionArgs& a, const Tile& t, int64_t token, int head,
+                            f32x4_t (&acc)[kv4_blocks(D)][kv4_width(D) / 16], float ref, float& sum, int kq) {
+    constexpr int W = kv4_width(D), NB = kv4_blocks(D), CH = W / 16;
+    if (!in_group(a, t.b)) return;
+    const Meeting m(a, token, head);
+    Taken f;
+    f.stats(m, ref, sum);
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int i = 0; i < CH; i += 4) {
+                const float4 v = *reinterpret_cast<const float4*>(m.sums + W * b + CH * (4 * kq + j) + i);
+                acc[b][i][j] = f(acc[b][i][j], v.x);
+                acc[b][i + 1][j] = f(acc[b][i + 1][j], v.y);
+                acc[b][i + 2][j] = f(acc[b][i + 2][j], v.z);
+                acc[b][i + 3][j] = f(acc[b][i + 3][j], v.w);
+            }
+}
 
 // Workspace of a split: per (tile, key head, split) the accumulators in lane
 // order, then the 16 rows' references and sums.
@@ -299,7 +387,7 @@ constexpr uint32_t kOnes = 0x3C003C00u;  // two f16 ones
 // requests of 0 to 8192 tokens 84 us (3.4 TB/s), 1 of 1000 tokens 10.5 us at D =
 // 256.  Equal stretches of all requests' tokens a workgroup, in one round, pay
 // that chain twice and were slower (95 us, where these splits took 89).
-template <int ACT, int D>
+template <int ACT, int D, int PART>
 __global__ __launch_bounds__(256, D == 256 ? 2 : D == 128 ? 3 : 4) void kv4_attention_kernel(Kv4AttentionArgs a, int span, int splits,
                                                                               uint32_t magic, unsigned* counters,
                                                                               float* partials) {
@@ -311,7 +399,7 @@ __global__ __launch_bounds__(256, D == 256 ? 2 : D == 128 ? 3 : 4) void kv4_atte
     const int kh = blockIdx.y, share = a.heads / a.kv_heads;
 
     Tile t;
-    if (!find_tile<16>(a, blockIdx.x, t)) return;
+    if (!find_tile<16, PART>(a, blockIdx.x, t)) return;
     const View view{a.causal, int(a.window)};
     const int last = min(t.r0 + 15, t.rows - 1);
     const int p_first = t.position(t.r0 / share), p_last = t.position(last / share);
@@ -466,6 +554,11 @@ __global__ __launch_bounds__(256, D == 256 ? 2 : D == 128 ? 3 : 4) void kv4_atte
     if (live == 1) {
         if (wave != 0 || t.r0 + col > last) return;
         sum = row_sum(sum);
+        if constexpr (PART == kPrefix) {
+            leave<D>(Meeting(a, t.q0 + qi, hd), acc, ref, sum, kq);
+            return;
+        }
+        if constexpr (PART == kOwn) take<D>(a, t, t.q0 + qi, hd, acc, ref, sum, kq);
         const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
 #pragma unroll
         for (int b = 0; b < NB; ++b)
@@ -557,6 +650,30 @@ __global__ __launch_bounds__(256, D == 256 ? 2 : D == 128 ? 3 : 4) void kv4_atte
         }
     }
     if (t.r0 + col > last) return;
+    if constexpr (PART == kPrefix) {
+        const Meeting m(a, t.q0 + qi, hd);
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int i = 0; i < PER; ++i) m.sums[W * b + CH * (4 * kq + j) + PER * wave + i] = out[b][i][j];
+        if (wave == 0 && kq == 0) *reinterpret_cast<float2*>(m.stats) = make_float2(ref, total);
+        return;
+    }
+    if constexpr (PART == kOwn) {
+        if (in_group(a, t.b)) {
+            const Meeting m(a, t.q0 + qi, hd);
+            Taken f;
+            f.stats(m, ref, total);
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int i = 0; i < PER; ++i) out[b][i][j] = f(out[b][i][j], m.sums[W * b + CH * (4 * kq + j) + PER * wave + i]);
+        }
+    }
     const float inv = total > 0.0f ? 1.0f / total : 0.0f;
 #pragma unroll
     for (int b = 0; b < NB; ++b)
@@ -669,7 +786,7 @@ struct Quarter {
     }
 };
 
-template <int ACT, int D>
+template <int ACT, int D, int PART>
 __global__ __launch_bounds__(256, D == 256 ? 2 : 4) void kv4_rows_kernel(Kv4AttentionArgs a, int64_t tiles, int span, int splits,
                                                                         uint32_t magic, unsigned* counters, float* partials) {
     using S = Stage<D>;
@@ -685,7 +802,7 @@ __global__ __launch_bounds__(256, D == 256 ? 2 : 4) void kv4_rows_kernel(Kv4Atte
     const int64_t x = tiles - 1 - int64_t(blockIdx.x / unsigned(a.kv_heads));
 
     Tile t;
-    if (!find_tile<ROWS>(a, x, t)) return;
+    if (!find_tile<ROWS, PART>(a, x, t)) return;
     const View view{a.causal, int(a.window)};
     const int last = min(t.r0 + ROWS - 1, t.rows - 1);
     const int begin = view.lo(t.position(t.r0 / share)) / STEP * STEP, end = view.hi(t.position(last / share), t.kv);
@@ -809,7 +926,7 @@ __global__ __launch_bounds__(256, D == 256 ? 2 : 4) void kv4_rows_kernel(Kv4Atte
     for (int b = 0; b < NB; ++b)
 #pragma unroll
         for (int i = 0; i < CH; ++i) acc[b][i] -= kKvOffset * ps[b];
-    float sum = row_sum(run.sum);
+    float sum = row_sum(run.sum), ref = run.ref;
     if (live > 1) {
         // as in the kernel above: the last split to finish joins them all
         const int mine = int(blockIdx.y) * kSlot + wave * kGroupBytes;
@@ -832,7 +949,7 @@ __global__ __launch_bounds__(256, D == 256 ? 2 : 4) void kv4_rows_kernel(Kv4Atte
         }
         __syncthreads();
         if (!last_one) return;
-        float ref = -INFINITY;
+        ref = -INFINITY;
         sum = 0.0f;
 #pragma unroll
         for (int b = 0; b < NB; ++b)
@@ -861,6 +978,11 @@ __global__ __launch_bounds__(256, D == 256 ? 2 : 4) void kv4_rows_kernel(Kv4Atte
         }
     }
     if (t.r0 + 16 * wave + col > last) return;
+    if constexpr (PART == kPrefix) {
+        leave<D>(Meeting(a, t.q0 + qi, hd), acc, ref, sum, kq);
+        return;
+    }
+    if constexpr (PART == kOwn) take<D>(a, t, t.q0 + qi, hd, acc, ref, sum, kq);
     const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
     uint16_t* dst = a.out + (t.q0 + qi) * a.ldo + int64_t(hd) * D;
 #pragma unroll
@@ -882,33 +1004,40 @@ hipError_t allow_lds(const void* kernel, size_t bytes) {
     return bytes <= 65536 ? hipSuccess : hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
 }
 
-template <int ACT, int D>
-hipError_t run(const Kv4AttentionArgs& a, const Kv4Plan& p, hipStream_t stream) {
+template <int ACT, int D, int PART>
+hipError_t run(const Kv4AttentionArgs& a, const Kv4Plan& p, float* partials, hipStream_t stream) {
     const int per = a.page / 16;
     const uint32_t magic = per == 1 ? 0 : uint32_t(((uint64_t(1) << 32) + per - 1) / per);
     unsigned* counters = static_cast<unsigned*>(a.workspace);
-    float* partials = p.splits > 1 ? reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + kSyncBytes) : nullptr;
+    if (p.splits < 2) partials = nullptr;
     if (p.rows > 16) {
         const dim3 grid(unsigned(p.tiles * a.kv_heads), unsigned(p.splits));
         const size_t lds = 2 * sizeof(Stage<D>);
-        const hipError_t e = allow_lds(reinterpret_cast<const void*>(&kv4_rows_kernel<ACT, D>), lds);
+        const hipError_t e = allow_lds(reinterpret_cast<const void*>(&kv4_rows_kernel<ACT, D, PART>), lds);
         if (e != hipSuccess) return e;
-        kv4_rows_kernel<ACT, D><<<grid, dim3(256), lds, stream>>>(a, p.tiles, int(p.span), p.splits, magic, counters, partials);
+        kv4_rows_kernel<ACT, D, PART><<<grid, dim3(256), lds, stream>>>(a, p.tiles, int(p.span), p.splits, magic, counters, partials);
         return hipGetLastError();
     }
     const dim3 grid(unsigned(p.tiles), unsigned(a.kv_heads), unsigned(p.splits));
-    kv4_attention_kernel<ACT, D><<<grid, dim3(256), 0, stream>>>(a, int(p.span), p.splits, magic, counters, partials);
+    kv4_attention_kernel<ACT, D, PART><<<grid, dim3(256), 0, stream>>>(a, int(p.span), p.splits, magic, counters, partials);
     return hipGetLastError();
 }
 
-template <int ACT>
-hipError_t run_by_dim(const Kv4AttentionArgs& a, const Kv4Plan& p, hipStream_t stream) {
+template <int ACT, int PART>
+hipError_t run_by_dim(const Kv4AttentionArgs& a, const Kv4Plan& p, float* partials, hipStream_t stream) {
     switch (a.dim) {
-        case 64: return run<ACT, 64>(a, p, stream);
-        case 128: return run<ACT, 128>(a, p, stream);
-        default: return run<ACT, 256>(a, p, stream);
+        case 64: return run<ACT, 64, PART>(a, p, partials, stream);
+        case 128: return run<ACT, 128, PART>(a, p, partials, stream);
+        default: return run<ACT, 256, PART>(a, p, partials, stream);
     }
 }
+
+template <int PART>
+hipError_t run_by_type(const Kv4AttentionArgs& a, const Kv4Plan& p, float* partials, int act, hipStream_t stream) {
+    return act == kActBf16 ? run_by_dim<kActBf16, PART>(a, p, partials, stream) : run_by_dim<kActF16, PART>(a, p, partials, stream);
+}
+
+float* after_header(void* workspace, size_t bytes) { return reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kSyncBytes + bytes); }
 
 }  // namespace
 
@@ -971,7 +1100,33 @@ Kv4Plan plan_kv4_attention(int64_t tokens, int64_t batch, int heads, int kv_head
 hipError_t launch_kv4_attention(const Kv4AttentionArgs& a, int act, hipStream_t stream) {
     const Kv4Plan p = plan_kv4_attention(a.tokens, a.batch, a.heads, a.kv_heads, a.dim, a.table_width * a.page,
                                          a.cu_q != nullptr, a.causal != 0, a.window);
-    return act == kActBf16 ? run_by_dim<kActBf16>(a, p, stream) : run_by_dim<kActF16>(a, p, stream);
+    return run_by_type<kWhole>(a, p, after_header(a.workspace, 0), act, stream);
+}
+
+Kv4PrefixPlan plan_kv4_prefix(int64_t tokens, int64_t batch, int64_t groups, int heads, int kv_heads, int dim,
+                              int64_t prefix_capacity, int64_t capacity, bool ragged, bool causal) {
+    Kv4PrefixPlan p{};
+    p.prefix = plan_kv4_attention(tokens, groups, heads, kv_heads, dim, prefix_capacity, true, false, 0);
+    p.own = plan_kv4_attention(tokens, batch, heads, kv_heads, dim, capacity, ragged, causal, 0);
+    p.parts = size_t(tokens) * size_t(heads) * size_t(dim + 2) * 4;
+    p.parts = (p.parts + 15) / 16 * 16;
+    p.workspace = p.parts + (p.prefix.workspace > p.own.workspace ? p.prefix.workspace : p.own.workspace);
+    return p;
+}
+
+hipError_t launch_kv4_prefix(const Kv4PrefixArgs& a, int act, hipStream_t stream) {
+    const Kv4AttentionArgs& o = a.own;
+    const Kv4PrefixPlan p = plan_kv4_prefix(o.tokens, o.batch, o.groups, o.heads, o.kv_heads, o.dim, a.table_width * o.page,
+                                            o.table_width * o.page, o.cu_q != nullptr, o.causal != 0);
+    float* const partials = after_header(o.workspace, p.parts);
+    Kv4AttentionArgs f = o;
+    f.table = a.table;
+    f.table_width = a.table_width;
+    f.ldt = a.ldt;
+    f.kv_lens = a.lens;
+    f.causal = 0;
+    const hipError_t e = run_by_type<kPrefix>(f, p.prefix, partials, act, stream);
+    return e == hipSuccess ? run_by_type<kOwn>(o, p.own, partials, act, stream) : e;
 }
 
 }  // namespace w4a16

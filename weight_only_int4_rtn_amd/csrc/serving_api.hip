@@ -139,6 +139,10 @@ bool valid_attention(int64_t tokens, int64_t batch, int64_t heads, int64_t kv_he
     return window >= 0;
 }
 
+bool valid_prefix(int64_t groups, int64_t prefix_width, int64_t page_size) {
+    return groups >= 1 && groups <= kMaxBatch && prefix_width >= 1 && prefix_width < kMaxTokens && prefix_width * page_size < kMaxTokens;
+}
+
 }  // namespace
 
 extern "C" {
@@ -216,6 +220,80 @@ w4a16_status_t kv4_attention(const void* q, w4a16_dtype_t dtype, int64_t tokens,
     a.ldo = ldo;
     a.workspace = workspace;
     return from_hip(launch_kv4_attention(a, act_of(dtype), static_cast<hipStream_t>(stream)));
+}
+
+size_t kv4_prefix_attention_workspace_bytes(int64_t tokens, int64_t batch, int64_t groups, int64_t heads, int64_t kv_heads,
+                                            int64_t head_dim, int64_t prefix_width, int64_t table_width, int64_t page_size,
+                                            int ragged, int causal) {
+    if (!valid_attention(tokens, batch, heads, kv_heads, head_dim, table_width, page_size, ragged != 0, 0) ||
+        !valid_prefix(groups, prefix_width, page_size) || tokens == 0)
+        return 0;
+    return kSyncBytes + plan_kv4_prefix(tokens, batch, groups, int(heads), int(kv_heads), int(head_dim), prefix_width * page_size,
+                                        table_width * page_size, ragged != 0, causal != 0).workspace;
+}
+
+w4a16_status_t kv4_prefix_attention(const void* q, w4a16_dtype_t dtype, int64_t tokens, int64_t ldq, int64_t heads, int64_t kv_heads,
+                                    int64_t head_dim, const void* pool, int64_t pages, int64_t page_size, const int32_t* prefix_table,
+                                    int64_t prefix_width, int64_t ldp, const int32_t* prefix_lens, const int32_t* cu_groups,
+                                    int64_t groups, const int32_t* table, int64_t table_width, int64_t ldt, const int32_t* kv_lens,
+                                    const int32_t* cu_q, int64_t batch, int causal, float scale, void* out, int64_t ldo,
+                                    void* workspace, size_t workspace_bytes, void* stream) {
+    if (!act_dtype(dtype)) return W4A16_EUNSUPPORTED;
+    if (!valid_attention(tokens, batch, heads, kv_heads, head_dim, table_width, page_size, cu_q != nullptr, 0) ||
+        !valid_prefix(groups, prefix_width, page_size) || !valid_pool(pages, page_size, kv_heads, head_dim) || (!cu_groups && groups != 1))
+        return W4A16_EINVAL;
+    const int64_t width = heads * head_dim;
+    if (ldq < width || ldq > kMaxDim || ldq % 8 != 0 || ldo < width || ldo > kMaxDim || ldo % 8 != 0 || ldt < table_width ||
+        ldt > kMaxTokens || ldp < prefix_width || ldp > kMaxTokens || !std::isfinite(scale))
+        return W4A16_EINVAL;
+    if (tokens == 0) return W4A16_OK;
+    if (!q || !pool || !prefix_table || !prefix_lens || !table || !kv_lens || !out) return W4A16_EINVAL;
+    if (!aligned(q, 16) || !aligned(pool, 16) || !aligned(out, 16) || !aligned(prefix_table, 4) || !aligned(prefix_lens, 4) ||
+        !aligned(cu_groups, 4) || !aligned(table, 4) || !aligned(kv_lens, 4) || !aligned(cu_q, 4))
+        return W4A16_EINVAL;
+    const size_t ob = span_bytes(tokens, width, ldo, 2);
+    const size_t need = kv4_prefix_attention_workspace_bytes(tokens, batch, groups, heads, kv_heads, head_dim, prefix_width, table_width,
+                                                             page_size, cu_q != nullptr, causal);
+    if (!workspace || workspace_bytes < need) return W4A16_EWORKSPACE;
+    if (!aligned(workspace, 16)) return W4A16_EINVAL;
+    const struct { const void* p; size_t n; } in[] = {
+        {q, span_bytes(tokens, width, ldq, 2)}, {pool, kv4_pool_bytes(pages, page_size, kv_heads, head_dim)},
+        {prefix_table, span_bytes(groups, prefix_width, ldp, 4)}, {prefix_lens, size_t(groups) * 4},
+        {cu_groups, cu_groups ? size_t(groups + 1) * 4 : 0}, {table, span_bytes(batch, table_width, ldt, 4)},
+        {kv_lens, size_t(batch) * 4}, {cu_q, cu_q ? size_t(batch + 1) * 4 : 0}};
+    for (const auto& i : in)
+        if (overlap(out, ob, i.p, i.n) || overlap(workspace, need, i.p, i.n)) return W4A16_EINVAL;
+    if (overlap(workspace, need, out, ob)) return W4A16_EINVAL;
+    Kv4PrefixArgs p{};
+    Kv4AttentionArgs& a = p.own;
+    a.q = static_cast<const uint16_t*>(q);
+    a.ldq = ldq;
+    a.tokens = tokens;
+    a.heads = int(heads);
+    a.kv_heads = int(kv_heads);
+    a.dim = int(head_dim);
+    a.pool = static_cast<const uint8_t*>(pool);
+    a.pages = pages;
+    a.page = int(page_size);
+    a.table = table;
+    a.table_width = table_width;
+    a.ldt = ldt;
+    a.kv_lens = kv_lens;
+    a.cu_q = cu_q;
+    a.batch = batch;
+    a.causal = causal != 0;
+    a.scale = scale;
+    a.out = static_cast<uint16_t*>(out);
+    a.ldo = ldo;
+    a.workspace = workspace;
+    a.cu_groups = cu_groups;
+    a.groups = groups;
+    a.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kSyncBytes);
+    p.table = prefix_table;
+    p.table_width = prefix_width;
+    p.ldt = ldp;
+    p.lens = prefix_lens;
+    return from_hip(launch_kv4_prefix(p, act_of(dtype), static_cast<hipStream_t>(stream)));
 }
 
 size_t lora_add_workspace_bytes(int64_t m, int64_t n, int64_t k, int64_t adapters, int64_t rank) {
