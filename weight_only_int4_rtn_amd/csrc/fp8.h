@@ -19,6 +19,64 @@ namespace w4a16 {
 constexpr float kFp8Max = 448.0f;
 constexpr uint32_t kFp8Nan = 0x7F;
 
+// ---------------------------------------------------------------------------
+// Quantization of a group (device): 16 lanes hold it, eight values each.
+// ---------------------------------------------------------------------------
+// A magnitude's bits order numbers, infinities and NaNs as integers do; from kFp8Inf on it is not a number.
+constexpr uint32_t kFp8Inf = 0x7F800000u;
+
+__device__ inline float fp8_scale(uint32_t top) { return top >= kFp8Inf ? __uint_as_float(0x7FC00000u) : __uint_as_float(top) / kFp8Max; }
+
+// four values of a group with the largest magnitude `top` and scale s as codes
+__device__ inline uint32_t fp8_codes(float a, float b, float c, float d, float s, uint32_t top) {
+    if (top >= kFp8Inf) return kFp8Nan * 0x01010101u;
+    if (s == 0.0f) return 0;
+    auto q = [&](float v) { return fminf(fmaxf(v / s, -kFp8Max), kFp8Max); };
+    const int w = __builtin_amdgcn_cvt_pk_fp8_f32(q(a), q(b), 0, false);
+    return uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(q(c), q(d), w, true));
+}
+__device__ inline uint2 fp8_codes8(const float (&v)[8], float s, uint32_t top) {
+    return make_uint2(fp8_codes(v[0], v[1], v[2], v[3], s, top), fp8_codes(v[4], v[5], v[6], v[7], s, top));
+}
+
+// Eight consecutive values from element `at` on as FP32, of dtype DT (0: FP32), activated; SwiGLU's gates lie k further.
+template <int DT, int AF>
+__device__ inline void fp8_load8(const void* p, int64_t at, int64_t k, float (&v)[8]) {
+    if constexpr (DT == 0) {
+        const float4 a = reinterpret_cast<const float4*>(static_cast<const float*>(p) + at)[0];
+        const float4 b = reinterpret_cast<const float4*>(static_cast<const float*>(p) + at)[1];
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    } else {
+        const uint16_t* x = static_cast<const uint16_t*>(p) + at;
+        uint4 r = *reinterpret_cast<const uint4*>(x);
+        if constexpr (AF == kActFnSwiglu) r = activate8<DT, AF>(r, *reinterpret_cast<const uint4*>(x + k));
+        if constexpr (AF == kActFnGeluTanh) r = activate8<DT, AF>(r, uint4{});
+        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = to_f32<DT>(uint16_t(w[i]));
+            v[2 * i + 1] = to_f32<DT>(uint16_t(w[i] >> 16));
+        }
+    }
+}
+
+__device__ inline uint32_t fp8_top8(const float (&v)[8]) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+    return top;
+}
+
+template <int M>
+__device__ inline uint32_t fp8_max_xor(uint32_t v) {
+    return max(v, uint32_t(__builtin_amdgcn_ds_swizzle(int(v), 0x1F | (M << 10))));
+}
+// the largest magnitude of the group
+__device__ inline uint32_t fp8_group_top(const float (&v)[8]) {
+    return fp8_max_xor<8>(fp8_max_xor<4>(fp8_max_xor<2>(fp8_max_xor<1>(fp8_top8(v)))));
+}
+
 struct Fp8QuantizeArgs {
     const void* x;
     int64_t m, k, ldx;  // ldx: elements between rows
@@ -32,9 +90,9 @@ hipError_t launch_fp8_quantize(const Fp8QuantizeArgs& a, int dtype, int act_fn, 
 hipError_t launch_fp8_quantize_blocks(const Fp8QuantizeArgs& a, int dtype, hipStream_t stream);
 
 struct Fp8LinearArgs {
-    const uint8_t* x;
+    const uint8_t* x;   // codes, or (few rows) 16-bit values that the kernel quantizes itself
     const float* xs;
-    int64_t m, k, ldx;
+    int64_t m, k, ldx;  // ldx: elements
     const uint8_t* w;
     const float* ws;
     int64_t n;
@@ -53,6 +111,8 @@ struct Fp8Plan {
     size_t workspace;   // FP32 tiles of a K split
 };
 Fp8Plan plan_fp8_linear(int64_t m, int64_t n, int64_t k);
-hipError_t launch_fp8_linear(const Fp8LinearArgs& a, const Fp8Plan& p, int act, hipStream_t stream);
+// Whether the kernel quantizes 16-bit x itself: act_fn is then the activation, else it is not looked at and x holds codes.
+bool fp8_linear_quantizes(int64_t m, const Fp8Plan& p);
+hipError_t launch_fp8_linear(const Fp8LinearArgs& a, const Fp8Plan& p, int act, bool quantize, int act_fn, hipStream_t stream);
 
 }  // namespace w4a16

@@ -88,8 +88,9 @@ w4a16_status_t quantize_fp8_blocks(const void* w, w4a16_dtype_t dtype, int64_t n
 
 size_t fp8_linear_workspace_bytes(w4a16_dtype_t x_dtype, int64_t m, int64_t n, int64_t k) {
     if ((!act_dtype(x_dtype) && x_dtype != W4A16_E4M3) || !valid_linear(m, n, k) || m == 0 || n == 0) return 0;
-    const size_t rows = x_dtype == W4A16_E4M3 ? 0 : codes_bytes(m, k) + scales_bytes(m, k), tiles = plan_fp8_linear(m, n, k).workspace;
-    return rows + tiles ? kSyncBytes + rows + tiles : 0;
+    const Fp8Plan p = plan_fp8_linear(m, n, k);
+    const size_t rows = x_dtype == W4A16_E4M3 || fp8_linear_quantizes(m, p) ? 0 : codes_bytes(m, k) + scales_bytes(m, k);
+    return rows + p.workspace ? kSyncBytes + rows + p.workspace : 0;
 }
 
 w4a16_status_t fp8_linear(const void* x, w4a16_dtype_t x_dtype, const float* x_scales, w4a16_act_t act, int64_t m, int64_t k, int64_t ldx,
@@ -121,11 +122,13 @@ w4a16_status_t fp8_linear(const void* x, w4a16_dtype_t x_dtype, const float* x_s
 
     hipStream_t s = static_cast<hipStream_t>(stream);
     uint8_t* at = static_cast<uint8_t*>(workspace) + (need ? kSyncBytes : 0);
+    const Fp8Plan p = plan_fp8_linear(m, n, k);
+    const bool inside = !codes && fp8_linear_quantizes(m, p);
     Fp8LinearArgs a{};
-    if (codes) {
+    if (codes || inside) {
         a.x = static_cast<const uint8_t*>(x);
         a.xs = x_scales;
-        a.ldx = m > 1 ? ldx : k;
+        a.ldx = ldx;
     } else {
         const Fp8QuantizeArgs q{x, m, k, ldx, at, reinterpret_cast<float*>(at + codes_bytes(m, k))};
         const hipError_t e = launch_fp8_quantize(q, kernel_dtype(x_dtype), int(act), s);
@@ -145,7 +148,7 @@ w4a16_status_t fp8_linear(const void* x, w4a16_dtype_t x_dtype, const float* x_s
     a.ldy = ldy;
     a.counters = static_cast<unsigned*>(workspace);
     a.slots = reinterpret_cast<float*>(at);
-    return from_hip(launch_fp8_linear(a, plan_fp8_linear(m, n, k), kernel_dtype(y_dtype), s));
+    return from_hip(launch_fp8_linear(a, p, kernel_dtype(y_dtype), inside, int(act), s));
 }
 
 }  // extern "C"

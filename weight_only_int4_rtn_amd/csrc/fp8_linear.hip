@@ -17,6 +17,9 @@
 #include "fp8.h"
 #include "kernels.h"
 
+#ifndef FUSE
+#define FUSE 4
+#endif
 namespace w4a16 {
 
 namespace {
@@ -50,7 +53,7 @@ __device__ inline void store_row(const Fp8LinearArgs& a, int64_t row, int64_t n,
         if constexpr (N % 8 == 0) {
 #pragma unroll
             for (int i = 0; i < N / 8; ++i)
-                *reinterpret_cast<u32x4*>(to + 8 * i) = u32x4{w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]};
+                __builtin_nontemporal_store(u32x4{w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]}, reinterpret_cast<u32x4*>(to + 8 * i));
         } else {
             *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[1]);
         }
@@ -59,6 +62,14 @@ __device__ inline void store_row(const Fp8LinearArgs& a, int64_t row, int64_t n,
         for (int i = 0; i < N; ++i)
             if (n + i < a.n) to[i] = from_f32<ACT>(v[i] + b[i]);
     }
+}
+
+// The same as FP32 sums of one part of K, for the split-K reduce kernel (reduce.hip): [splits][m][npad].
+template <int N>
+__device__ inline void store_part(const Fp8LinearArgs& a, int split, int64_t npad, int64_t row, int64_t n, const float (&v)[N]) {
+    float* to = a.slots + (int64_t(split) * a.m + row) * npad + n;
+#pragma unroll
+    for (int i = 0; i < N; i += 4) *reinterpret_cast<float4*>(to + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
 }
 
 // A K split's end: every split stores its FP32 sums past the L2 (SC1: the XCDs'
@@ -88,18 +99,23 @@ __device__ inline bool join_splits(float (&acc)[T][4], float* slot, unsigned* co
     for (int t = 0; t < T; ++t)
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[t][e] = 0.0f;
-    constexpr int B = T < 8 ? T : 8;  // vectors in flight
-    for (int s = 0; s < splits; ++s) {
+    // eight vectors a lane in flight: of one split, or of several at a time where a split has fewer
+    constexpr int V = T < 8 ? T : 8, N = 8 / V;
+    for (int s = 0; s < splits; s += N) {
 #pragma unroll
-        for (int t0 = 0; t0 < T; t0 += B) {
-            u32x4 part[B];
+        for (int t0 = 0; t0 < T; t0 += V) {
+            u32x4 part[N][V];
 #pragma unroll
-            for (int t = 0; t < B; ++t)
-                part[t] = __builtin_amdgcn_raw_buffer_load_b128(sl, s * bytes + (t0 + t) * threads * 16 + at, 0, kCoherent);
+            for (int i = 0; i < N; ++i)
 #pragma unroll
-            for (int t = 0; t < B; ++t)
+                for (int t = 0; t < V; ++t)
+                    part[i][t] = __builtin_amdgcn_raw_buffer_load_b128(sl, min(s + i, splits - 1) * bytes + (t0 + t) * threads * 16 + at, 0, kCoherent);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) acc[t0 + t][e] += __uint_as_float(part[t][e]);
+            for (int i = 0; i < N; ++i)
+#pragma unroll
+                for (int t = 0; t < V; ++t)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[t0 + t][e] += s + i < splits ? __uint_as_float(part[i][t][e]) : 0.0f;
         }
     }
     return true;
@@ -112,9 +128,13 @@ __device__ inline bool join_splits(float (&acc)[T][4], float* slot, unsigned* co
 // ---------------------------------------------------------------------------
 constexpr int kFewWaves = 4, kFewAhead = 4;
 
-template <int ACT>
+// QUANTIZE: x holds 16-bit values (of the output's type), which every workgroup quantizes for itself, activated by AF, while
+// its first rows of W are on their way.
+template <int ACT, bool QUANTIZE, int AF>
 __global__ __launch_bounds__(64 * kFewWaves) void fp8_few_kernel(Fp8LinearArgs a, int splits, int gps) {
     __shared__ f32x4_t sums[kFewWaves][64];
+    __shared__ int flag;
+    extern __shared__ __align__(16) uint8_t few[];  // QUANTIZE: codes [m][ng][128], scales [m][ng]
     const int lane = threadIdx.x % 64, wave = uniform(threadIdx.x / 64);
     const int r = lane % 16, kq = lane / 16;
     const int64_t groups = a.k / kGroup;
@@ -123,9 +143,10 @@ __global__ __launch_bounds__(64 * kFewWaves) void fp8_few_kernel(Fp8LinearArgs a
     const int g0 = split * gps, ng = int(min<int64_t>(gps, groups - g0));
     const int mine = ng > wave ? (ng - wave + kFewWaves - 1) / kFewWaves : 0;
 
+    const int row = min<int>(r, int(a.m) - 1);
     const uint8_t* wp = a.w + min(n0 + r, a.n - 1) * a.k + int64_t(g0 + wave) * kGroup + 16 * kq;
-    const uint8_t* xp = a.x + min<int64_t>(r, a.m - 1) * a.ldx + int64_t(g0 + wave) * kGroup + 16 * kq;
-    const float* xsp = a.xs + min<int64_t>(r, a.m - 1) * groups + g0 + wave;
+    const uint8_t* xp = a.x + row * a.ldx + int64_t(g0 + wave) * kGroup + 16 * kq;
+    const float* xsp = a.xs + row * groups + g0 + wave;
     const float* wsp = a.ws + n0 / 128 * groups + g0 + wave;
 
     struct Chunk {
@@ -136,10 +157,10 @@ __global__ __launch_bounds__(64 * kFewWaves) void fp8_few_kernel(Fp8LinearArgs a
         const int64_t at = int64_t(i) * (kFewWaves * kGroup);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            c.w[h] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(wp + at + 64 * h));
-            c.x[h] = *reinterpret_cast<const u32x4*>(xp + at + 64 * h);
+            c.w[h] = *reinterpret_cast<const u32x4*>(wp + at + 64 * h);
+            if constexpr (!QUANTIZE) c.x[h] = *reinterpret_cast<const u32x4*>(xp + at + 64 * h);
         }
-        c.xs = xsp[i * kFewWaves];
+        if constexpr (!QUANTIZE) c.xs = xsp[i * kFewWaves];
         c.ws = wsp[i * kFewWaves];
     };
     f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
@@ -147,10 +168,30 @@ __global__ __launch_bounds__(64 * kFewWaves) void fp8_few_kernel(Fp8LinearArgs a
 #pragma unroll
     for (int i = 0; i < kFewAhead; ++i)
         if (i < mine) load(ring[i], i);
+    if constexpr (QUANTIZE) {
+        float* const scales = reinterpret_cast<float*>(few + a.m * ng * kGroup);
+        const int sub = threadIdx.x % 16;
+        for (int e = threadIdx.x / 16; e < int(a.m) * ng; e += 4 * kFewWaves) {
+            const int at = e / ng, g = e % ng;
+            float v[8];
+            fp8_load8<ACT, AF>(a.x, at * a.ldx + int64_t(g0 + g) * kGroup + sub * 8, a.k, v);
+            const uint32_t top = fp8_group_top(v);
+            const float s = fp8_scale(top);
+            *reinterpret_cast<uint2*>(few + e * kGroup + sub * 8) = fp8_codes8(v, s, top);
+            if (sub == 0) scales[e] = s;
+        }
+        lds_barrier();
+    }
     for (int c = 0; c < mine; c += kFewAhead) {
 #pragma unroll
         for (int i = 0; i < kFewAhead; ++i) {
             if (c + i >= mine) break;
+            if constexpr (QUANTIZE) {
+                const int e = row * ng + wave + (c + i) * kFewWaves;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) ring[i].x[h] = *reinterpret_cast<const u32x4*>(few + e * kGroup + 64 * h + 16 * kq);
+                ring[i].xs = reinterpret_cast<const float*>(few + a.m * ng * kGroup)[e];
+            }
             const f32x4_t p = fp8_mfma(ring[i].w, ring[i].x);
             const float f = ring[i].xs * ring[i].ws;
 #pragma unroll
@@ -166,125 +207,143 @@ __global__ __launch_bounds__(64 * kFewWaves) void fp8_few_kernel(Fp8LinearArgs a
     for (int w = 0; w < kFewWaves; ++w)
 #pragma unroll
         for (int e = 0; e < 4; ++e) tot[0][e] += sums[w][lane][e];
-    if (splits > 1) {
-        __shared__ int flag;
-        if (!join_splits<1>(tot, a.slots + tile * splits * (kFewWaves * 64 * 4), a.counters + tile, split, splits, &flag)) return;
-    }
+    if (splits > 1 && !join_splits<1>(tot, a.slots + tile * splits * (kFewWaves * 64 * 4), a.counters + tile, split, splits, &flag)) return;
     if (wave != 0 || r >= a.m) return;
     store_row<ACT, 4>(a, r, n0 + 4 * kq, tot[0], ((reinterpret_cast<uintptr_t>(a.y) | uintptr_t(a.ldy * 2)) & 7) == 0);
 }
 
+// Row r of 128 bytes holds them as 8 pieces of 16, piece c at c ^ (r / 2 % 8): the 16 rows that an operand's read touches
+// then cover all 64 banks once.
+__device__ inline int fp8_swizzle(int row, int piece) { return row * 128 + ((piece ^ ((row >> 1) & 7)) << 4); }
+
 // ---------------------------------------------------------------------------
 // Tiles.  A workgroup of WM x WN waves takes BM rows of x and BN columns of y
-// and a part of K in steps of one group.  x goes through LDS (direct loads into
-// a ring of three buffers, two steps ahead, shared by the waves of a row);
-// W goes from memory straight to each wave's registers, a step ahead: a wave's
-// 16 CB rows of W serve its 16 RB rows of x, and taking W through LDS too would
-// have its reads fill LDS's 128 bytes a clock.
+// and a part of K in steps of one group.  Both operands go through LDS by direct
+// loads into a ring of R buffers, issued one at a time between the matrix
+// instructions of the step R - 1 before theirs.
 //
 // A wave's CB tiles of W interleave their rows: tile j's row 4 a + i is
 // column 4 CB a + 4 j + i of the wave's block, so a lane's results of all tiles
 // are 4 CB consecutive columns of one row and leave in 16-byte stores.
 // ---------------------------------------------------------------------------
-template <int RB_, int CB_, int WM_, int WN_>
+template <int RB_, int CB_, int WM_, int WN_, int R_>
 struct Fp8Shape {
-    static constexpr int RB = RB_, CB = CB_, WM = WM_, WN = WN_, WAVES = WM * WN;
+    static constexpr int RB = RB_, CB = CB_, WM = WM_, WN = WN_, R = R_, WAVES = WM * WN;
     static constexpr int BM = 16 * RB * WM, BN = 16 * CB * WN;
-    static constexpr int XP = BM / 8 / WAVES;  // 1 KB pieces of x a wave loads a step
-    static_assert(XP >= 1 && XP * WAVES * 8 == BM && BM <= 64 * WAVES, "every wave loads pieces and scales");
+    static constexpr int XP = BM / 8 / WAVES, WP = BN / 8 / WAVES;  // 1 KB pieces of x and W a wave loads a step
+    static constexpr int LOADS = XP + WP + 1;                       // and one of scales
+    static constexpr int PER = (LOADS + RB * CB - 1) / (RB * CB);   // loads beside a matrix instruction
+    static_assert(XP * WAVES * 8 == BM && WP * WAVES * 8 == BN && BM <= 64 * WAVES, "every wave loads its share");
+    static_assert(CB == 2 || CB == 4, "rows of W in LDS");
 };
 
-// Row r of an x buffer holds its 128 bytes as 8 pieces of 16, piece c at c ^ (r / 2 % 8): the 16 rows that an
-// operand's read touches then cover all 64 banks once.
-__device__ inline int fp8_swizzle(int row, int piece) { return row * 128 + ((piece ^ ((row >> 1) & 7)) << 4); }
+// Rows of W: the 16 that an operand's read touches are 4 CB a + 4 j + i (a, i < 4), so pieces turn with bits 1 and those of a.
+template <int CB>
+__device__ inline int fp8_w_turn(int row) { return ((row >> 1) & 1) | ((row / (4 * CB) & 3) << 1); }
+
+// Tile of a workgroup: an XCD (workgroups go to the 8 of them in turn) takes a run of tiles, the run goes through bands of
+// four rows of tiles, so the tiles that an XCD computes at a time share rows of x and of W in its L2.
+__device__ inline void fp8_tile_of(int64_t id, int64_t mtiles, int64_t ntiles, int64_t& mt, int64_t& nt) {
+    const int64_t total = mtiles * ntiles, xcd = id % 8, at = xcd * (total / 8) + min(xcd, total % 8) + id / 8;
+    const int64_t band = at / (4 * ntiles), in = at % (4 * ntiles), high = min<int64_t>(4, mtiles - 4 * band);
+    mt = 4 * band + in % high;
+    nt = in / high;
+}
 
 template <int ACT, typename S>
 __global__ __launch_bounds__(64 * S::WAVES, S::WAVES / 4) void fp8_tile_kernel(Fp8LinearArgs a, int64_t mtiles, int64_t ntiles, int splits, int gps) {
-    constexpr int RB = S::RB, CB = S::CB, XP = S::XP;
-    constexpr int kMaxXP = 4, kMaxRB = 8, kMaxCB = 4;
-    static_assert(XP <= kMaxXP && RB <= kMaxRB && CB <= kMaxCB, "array maxima");
-    __shared__ __align__(16) uint8_t X0[S::BM * 128], X1[S::BM * 128], X2[S::BM * 128];
-    __shared__ float S0[S::WAVES * 64], S1[S::WAVES * 64], S2[S::WAVES * 64];
-    __shared__ int flag;
+    constexpr int RB = S::RB, CB = S::CB, XP = S::XP, WP = S::WP, R = S::R;
+    constexpr int kMaxPieces = 4, kMaxCB = 4;  // (a captured array whose bound depends on the template would drop the launch stub)
+    static_assert(XP <= kMaxPieces && WP <= kMaxPieces && CB <= kMaxCB && R >= 2 && R <= 6, "array maxima");
+    // buffers with names of their own: the compiler then tells direct loads into one from reads of another
+    __shared__ __align__(16) uint8_t X0[S::BM * 128], X1[S::BM * 128], X2[R > 2 ? S::BM * 128 : 16], X3[R > 3 ? S::BM * 128 : 16],
+        X4[R > 4 ? S::BM * 128 : 16], X5[R > 5 ? S::BM * 128 : 16];
+    __shared__ __align__(16) uint8_t W0[S::BN * 128], W1[S::BN * 128], W2[R > 2 ? S::BN * 128 : 16], W3[R > 3 ? S::BN * 128 : 16],
+        W4[R > 4 ? S::BN * 128 : 16], W5[R > 5 ? S::BN * 128 : 16];
+    __shared__ float S0[S::WAVES * 64], S1[S::WAVES * 64], S2[R > 2 ? S::WAVES * 64 : 16], S3[R > 3 ? S::WAVES * 64 : 16], S4[R > 4 ? S::WAVES * 64 : 16],
+        S5[R > 5 ? S::WAVES * 64 : 16];
     const int lane = threadIdx.x % 64, wave = uniform(threadIdx.x / 64);
     const int r = lane % 16, kq = lane / 16;
     const int wm = wave / S::WN, wn = wave % S::WN;
     const int split = int(blockIdx.x % unsigned(splits));
     const int64_t tile = blockIdx.x / unsigned(splits);
-    const int64_t mt = tile % mtiles, nt = tile / mtiles;
-    const int64_t m0 = mt * S::BM, n0 = nt * S::BN + wn * (16 * CB);
+    int64_t mt, nt;
+    fp8_tile_of(tile, mtiles, ntiles, mt, nt);
+    const int64_t m0 = mt * S::BM, nb = nt * S::BN, n0 = nb + wn * (16 * CB);
     const int64_t groups = a.k / kGroup;
     const int g0 = split * gps, ng = int(min<int64_t>(gps, groups - g0));
 
     // rows of x past M and of W past N read as zeros (the offset that is checked is the lane's, its row's start included)
-    const int64_t rows = min<int64_t>(S::BM, a.m - m0), cols = max<int64_t>(0, min<int64_t>(16 * CB, a.n - n0));
+    const int64_t rows = min<int64_t>(S::BM, a.m - m0), cols = min<int64_t>(S::BN, a.n - nb);
     const __amdgpu_buffer_rsrc_t xr = buffer_rsrc(a.x + m0 * a.ldx, (rows - 1) * a.ldx + a.k);
     const __amdgpu_buffer_rsrc_t sr = buffer_rsrc(a.xs + m0 * groups, rows * groups * 4);
-    const __amdgpu_buffer_rsrc_t wr = buffer_rsrc(a.w + min(n0, a.n - 1) * a.k, cols * a.k);
-    uint32_t xo[kMaxXP];
+    const __amdgpu_buffer_rsrc_t wr = buffer_rsrc(a.w + nb * a.k, cols * a.k);
+    uint32_t xo[kMaxPieces], wo[kMaxPieces];
 #pragma unroll
     for (int p = 0; p < XP; ++p) {
         const int row = 8 * (XP * wave + p) + lane / 8;
         xo[p] = uint32_t(row * a.ldx + (((lane & 7) ^ ((row >> 1) & 7)) << 4));
     }
+#pragma unroll
+    for (int p = 0; p < WP; ++p) {
+        const int row = 8 * (WP * wave + p) + lane / 8;
+        wo[p] = uint32_t(row * a.k + (((lane & 7) ^ fp8_w_turn<CB>(row)) << 4));
+    }
     const uint32_t so = uint32_t((64 * wave + lane) % S::BM * groups * 4);
-    const uint32_t wo = uint32_t((4 * CB * (r / 4) + r % 4) * a.k + 16 * kq);
     const float* wsp = a.ws + min(n0, a.n - 1) / 128 * groups;
 
-    auto load_x = [&](uint8_t* X, float* sc, int s) {
+    // load q of step s (steps past the end load the last one again, into buffers that nobody reads)
+    auto load = [&](uint8_t* X, uint8_t* W, float* sc, int s, int q) {
         const int g = g0 + min(s, ng - 1);
-#pragma unroll
-        for (int p = 0; p < XP; ++p)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(xr, (lds_ptr_t)(X + (XP * wave + p) * 1024), 16, xo[p], uniform(g * kGroup), 0, 0);
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(sr, (lds_ptr_t)(sc + 64 * wave), 4, so, uniform(g * 4), 0, 0);
-    };
-    struct Weights {
-        u32x4 w[kMaxCB][2];
-    };
-    auto load_w = [&](Weights& d, int s) {
-        const int g = g0 + min(s, ng - 1);
-#pragma unroll
-        for (int j = 0; j < CB; ++j)
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                d.w[j][h] = __builtin_amdgcn_raw_buffer_load_b128(wr, wo + 64 * h, uniform(int(4 * j * a.k) + g * kGroup), 0);
+        if (q == 0)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(sr, (lds_ptr_t)(sc + 64 * wave), 4, so, uniform(g * 4), 0, 0);
+        else if (q <= XP)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(xr, (lds_ptr_t)(X + (XP * wave + q - 1) * 1024), 16, xo[q - 1], uniform(g * kGroup), 0, 0);
+        else
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(wr, (lds_ptr_t)(W + (WP * wave + q - 1 - XP) * 1024), 16, wo[q - 1 - XP], uniform(g * kGroup), 0, 0);
     };
     float acc[RB * CB][4] = {};
-
-    Weights wa, wb;
     float ws64 = 0.f;  // lane L: W's scale of step s / 64 * 64 + L
-    // One step: buffers X, sc and the registers w hold it; the next step's weights and the x of the step after next are issued.
-    auto step = [&](const uint8_t* X, const float* sc, const Weights& w, uint8_t* Xn, float* sn, Weights& wn_, int s) {
+    // Step s from the first buffers, while step s + R - 1 is loaded into the second ones.
+    auto step = [&](const uint8_t* X, const uint8_t* W, const float* sc, uint8_t* Xn, uint8_t* Wn, float* sn, int s) {
         if (s % 64 == 0) ws64 = wsp[g0 + min(s + lane, ng - 1)];
-        // this step's x has landed: issued after it were its weights and the next step's x
-        asm volatile("" ::: "memory");
-        wait_vm<2 * CB + XP + 1>();
+        wait_vm<(R - 2) * S::LOADS>();
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
-        load_w(wn_, s + 1);
-        load_x(Xn, sn, s + 2);
         const float ws = __uint_as_float(uint32_t(__builtin_amdgcn_readlane(int(__float_as_uint(ws64)), s % 64)));
         const uint8_t* xp = X + wm * (RB * 2048);
+        const uint8_t* wp = W + wn * (CB * 2048);
         const float* scp = sc + wm * (RB * 16) + r;
         // Matrix instruction t (tile t % CB of W, rows t / CB of x), then the FMAs of the one three before it, whose
-        // result is there by then; x is read one block of rows ahead.
+        // result is there by then; x and its scales are read one block of rows ahead.
         constexpr int T = RB * CB, LAG = 3;
-        u32x4 x[2][2];
+        u32x4 x[2][2], w[kMaxCB][2];
+        float xsc[2], f[4];
         f32x4_t p[4];
-        float f[4];  // a block of rows has at least two tiles: the one three tiles back is at most two blocks back
         auto read = [&](int i) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) x[i % 2][h] = *reinterpret_cast<const u32x4*>(xp + i * 2048 + fp8_swizzle(r, 4 * h + kq));
+            xsc[i % 2] = scp[16 * i];
         };
+        auto read_w = [&](int j) {
+            const int row = 4 * CB * (r / 4) + 4 * j + r % 4;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) w[j][h] = *reinterpret_cast<const u32x4*>(wp + row * 128 + (((4 * h + kq) ^ fp8_w_turn<CB>(row)) << 4));
+        };
+        read_w(0);
         read(0);
+#pragma unroll
+        for (int j = 1; j < CB; ++j) read_w(j);
 #pragma unroll
         for (int t = 0; t < T + LAG; ++t) {
             if (t < T) {
                 if (t % CB == 0) {
+                    f[t / CB % 4] = xsc[t / CB % 2] * ws;
                     if (t / CB + 1 < RB) read(t / CB + 1);
-                    f[t / CB % 4] = scp[16 * (t / CB)] * ws;
                 }
-                p[t % 4] = fp8_mfma(w.w[t % CB], x[t / CB % 2]);
+#pragma unroll
+                for (int q = t * S::PER; q < (t + 1) * S::PER && q < S::LOADS; ++q) load(Xn, Wn, sn, s + R - 1, q);
+                p[t % 4] = fp8_mfma(w[t % CB], x[t / CB % 2]);
             }
             if (t >= LAG) {
                 const int d = t - LAG;
@@ -293,26 +352,36 @@ __global__ __launch_bounds__(64 * S::WAVES, S::WAVES / 4) void fp8_tile_kernel(F
             }
             __builtin_amdgcn_sched_barrier(0);
         }
-        // every read of X is done before the next barrier lets others overwrite it
+        // every read is done before the next barrier lets others overwrite the buffers
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     };
-    load_x(X0, S0, 0);
-    load_w(wa, 0);
-    load_x(X1, S1, 1);
-    for (int s = 0;;) {
-        step(X0, S0, wa, X2, S2, wb, s);
-        if (++s >= ng) break;
-        step(X1, S1, wb, X0, S0, wa, s);
-        if (++s >= ng) break;
-        step(X2, S2, wa, X1, S1, wb, s);
-        if (++s >= ng) break;
-        step(X0, S0, wb, X2, S2, wa, s);
-        if (++s >= ng) break;
-        step(X1, S1, wa, X0, S0, wb, s);
-        if (++s >= ng) break;
-        step(X2, S2, wb, X1, S1, wa, s);
-        if (++s >= ng) break;
+    auto whole = [&](uint8_t* X, uint8_t* W, float* sc, int s) {
+#pragma unroll
+        for (int q = 0; q < S::LOADS; ++q) load(X, W, sc, s, q);
+    };
+    whole(X0, W0, S0, 0);
+    if constexpr (R > 2) whole(X1, W1, S1, 1);
+    if constexpr (R > 3) whole(X2, W2, S2, 2);
+    if constexpr (R > 4) whole(X3, W3, S3, 3);
+    if constexpr (R > 5) whole(X4, W4, S4, 4);
+    // Buffer b of R: read by step s with s % R == b, filled again from step s + 1 on
+#define FP8_STEP(b, before)                                                                                  \
+    if constexpr (b < R) {                                                                                   \
+        if constexpr (b > 0) step(X##b, W##b, S##b, X##before, W##before, S##before, s);                      \
+        else if constexpr (R == 2) step(X0, W0, S0, X1, W1, S1, s);                                          \
+        else if constexpr (R == 3) step(X0, W0, S0, X2, W2, S2, s);                                          \
+        else if constexpr (R == 4) step(X0, W0, S0, X3, W3, S3, s);                                          \
+        else if constexpr (R == 5) step(X0, W0, S0, X4, W4, S4, s);                                          \
+        else step(X0, W0, S0, X5, W5, S5, s);                                                                \
+        if (++s >= ng) break;                                                                                \
     }
+    for (int s = 0;;) {
+        FP8_STEP(0, 0)
+        FP8_STEP(1, 0)
+        FP8_STEP(2, 1)
+        FP8_STEP(3, 2)
+            }
+#undef FP8_STEP
     // (scalars from here on: as vectors of four, which the compiler would make of them at each of the loop's exits, every
     // step's sums got registers of their own)
 #pragma unroll
@@ -321,9 +390,6 @@ __global__ __launch_bounds__(64 * S::WAVES, S::WAVES / 4) void fp8_tile_kernel(F
         for (int e = 0; e < 4; ++e) asm volatile("" : "+v"(acc[t][e]));
     // the last steps' loads write LDS: they land before it is given back
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    if (splits > 1 &&
-        !join_splits<RB * CB>(acc, a.slots + tile * splits * (RB * CB * 64 * S::WAVES * 4), a.counters + tile, split, splits, &flag))
-        return;
     const bool wide = ((reinterpret_cast<uintptr_t>(a.y) | uintptr_t(a.ldy * 2)) & 15) == 0;
 #pragma unroll
     for (int i = 0; i < RB; ++i) {
@@ -333,22 +399,26 @@ __global__ __launch_bounds__(64 * S::WAVES, S::WAVES / 4) void fp8_tile_kernel(F
         for (int j = 0; j < CB; ++j)
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[4 * j + e] = acc[i * CB + j][e];
-        if (row < a.m) store_row<ACT, 4 * CB>(a, row, n0 + 4 * CB * kq, v, wide);
+        if (row >= a.m) continue;
+        if (splits > 1) store_part(a, split, ntiles * S::BN, row, n0 + 4 * CB * kq, v);
+        else store_row<ACT, 4 * CB>(a, row, n0 + 4 * CB * kq, v, wide);
     }
 }
 
-// kind: index in shapes (below)
-using Large = Fp8Shape<8, 4, 2, 4>;   // 256 x 256
-using Middle = Fp8Shape<4, 4, 2, 2>;  // 128 x 128
-using Flat = Fp8Shape<4, 2, 1, 4>;    // 64 x 128
-using Thin = Fp8Shape<2, 2, 1, 4>;    // 32 x 128
+using Thin = Fp8Shape<2, 2, 1, 4, 4>;    // 32 x 128
+using Flat = Fp8Shape<4, 2, 1, 4, 4>;    // 64 x 128
+using Middle = Fp8Shape<4, 4, 2, 2, 4>;  // 128 x 128
+using Wide = Fp8Shape<4, 4, 2, 4, 3>;    // 128 x 256
+using Large = Fp8Shape<8, 4, 2, 4, 2>;   // 256 x 256
 
 struct Shape {
     int bm, bn, waves;
 };
 template <typename S>
 constexpr Shape shape() { return {S::BM, S::BN, S::WAVES}; }
-constexpr Shape kShapes[] = {{16, 16, kFewWaves}, shape<Thin>(), shape<Flat>(), shape<Middle>(), shape<Large>()};
+// by Fp8Plan::kind
+constexpr Shape kShapes[] = {{16, 16, kFewWaves}, shape<Thin>(), shape<Flat>(), shape<Middle>(), shape<Wide>(), shape<Large>()};
+constexpr int kKinds = int(sizeof(kShapes) / sizeof(kShapes[0]));
 
 template <int ACT, typename S>
 hipError_t run_tiles(const Fp8LinearArgs& a, const Fp8Plan& p, hipStream_t stream) {
@@ -356,15 +426,25 @@ hipError_t run_tiles(const Fp8LinearArgs& a, const Fp8Plan& p, hipStream_t strea
     return hipGetLastError();
 }
 
+template <int ACT, bool QUANTIZE, int AF>
+hipError_t run_few(const Fp8LinearArgs& a, const Fp8Plan& p, hipStream_t stream) {
+    const size_t lds = QUANTIZE ? size_t(a.m) * size_t(p.gps) * (kGroup + 4) : 0;
+    fp8_few_kernel<ACT, QUANTIZE, AF><<<dim3(unsigned(p.ntiles * p.splits)), dim3(64 * kFewWaves), lds, stream>>>(a, p.splits, p.gps);
+    return hipGetLastError();
+}
+
 template <int ACT>
-hipError_t run(const Fp8LinearArgs& a, const Fp8Plan& p, hipStream_t stream) {
+hipError_t run(const Fp8LinearArgs& a, const Fp8Plan& p, bool quantize, int act_fn, hipStream_t stream) {
     switch (p.kind) {
         case 0:
-            fp8_few_kernel<ACT><<<dim3(unsigned(p.ntiles * p.splits)), dim3(64 * kFewWaves), 0, stream>>>(a, p.splits, p.gps);
-            return hipGetLastError();
+            if (!quantize) return run_few<ACT, false, kActFnNone>(a, p, stream);
+            return act_fn == kActFnSwiglu     ? run_few<ACT, true, kActFnSwiglu>(a, p, stream)
+                   : act_fn == kActFnGeluTanh ? run_few<ACT, true, kActFnGeluTanh>(a, p, stream)
+                                              : run_few<ACT, true, kActFnNone>(a, p, stream);
         case 1: return run_tiles<ACT, Thin>(a, p, stream);
         case 2: return run_tiles<ACT, Flat>(a, p, stream);
         case 3: return run_tiles<ACT, Middle>(a, p, stream);
+        case 4: return run_tiles<ACT, Wide>(a, p, stream);
         default: return run_tiles<ACT, Large>(a, p, stream);
     }
 }
@@ -372,28 +452,66 @@ hipError_t run(const Fp8LinearArgs& a, const Fp8Plan& p, hipStream_t stream) {
 }  // namespace
 
 Fp8Plan plan_fp8_linear(int64_t m, int64_t n, int64_t k) {
-    Fp8Plan p{};
     const int64_t groups = k / kGroup;
-    p.kind = m <= 16 ? 0 : m <= 32 ? 1 : m <= 512 ? 2 : m * n < int64_t(1) << 22 ? 3 : 4;
-    p.bm = kShapes[p.kind].bm;
-    p.bn = kShapes[p.kind].bn;
-    p.waves = kShapes[p.kind].waves;
-    p.mtiles = ceil_div(m, p.bm);
-    p.ntiles = ceil_div(n, p.bn);
-    const int64_t tiles = p.mtiles * p.ntiles;
-    const int64_t room = p.kind == 0 ? 1024 : p.kind == 4 ? 256 : 512;
-    int64_t splits = tiles * 4 > int64_t(kSyncBytes) ? 1 : tiles >= room ? 1 : room / tiles;
-    const int64_t least = p.kind == 0 ? 8 : 4;
-    if (splits > groups / least) splits = groups / least;
-    if (splits < 1) splits = 1;
-    p.gps = int(ceil_div(groups, splits));
-    p.splits = int(ceil_div(groups, p.gps));
-    if (p.splits > 1) p.workspace = size_t(tiles) * size_t(p.splits) * (p.kind == 0 ? size_t(kFewWaves * 64 * 16) : size_t(p.bm) * size_t(p.bn) * 4);
-    return p;
+    auto cut = [&](int kind, int64_t splits) {
+        Fp8Plan p{};
+        p.kind = kind;
+        p.bm = kShapes[kind].bm;
+        p.bn = kShapes[kind].bn;
+        p.waves = kShapes[kind].waves;
+        p.mtiles = ceil_div(m, p.bm);
+        p.ntiles = ceil_div(n, p.bn);
+        p.gps = int(ceil_div(groups, splits));
+        p.splits = int(ceil_div(groups, p.gps));
+        return p;
+    };
+    if (m <= 16) {
+        const int64_t tiles = ceil_div(n, int64_t(16));
+        int64_t splits = tiles >= 256 ? 1 : 256 / tiles;
+        if (splits > groups / 32) splits = groups / 32;
+        Fp8Plan p = cut(0, splits < 1 ? 1 : splits);
+        if (p.splits > 1) p.workspace = size_t(tiles) * size_t(p.splits) * (kFewWaves * 64 * 16);
+        return p;
+    }
+    // Microseconds: what a launch costs, then for each round of 256 workgroups its steps, bound by their latency or by
+    // what the L2s deliver, then, for a K split, the second launch and its partial sums.
+    constexpr double kLaunch = 4.5, kL2 = 10.5e6, kJoin = 2.5, kPartial = 5e6;
+    constexpr double kStep[kKinds] = {0, 0.3, 0.36, 0.62, 0.8, 1.55};
+    Fp8Plan best{};
+    double least = 0;
+    for (int kind = 1; kind < kKinds; ++kind) {
+        int64_t before = 0;
+        for (int64_t splits = 1; splits <= 16 && splits <= groups; ++splits) {
+            Fp8Plan p = cut(kind, splits);
+            if (p.splits == before) continue;
+            before = p.splits;
+            const int64_t wgs = p.mtiles * p.ntiles * p.splits;
+            const double bytes = 128.0 * (p.bm + p.bn);
+            double t = kLaunch;
+            for (int64_t left = wgs, round = 0; left > 0 && round < 2; ++round) {
+                // all whole rounds at once, then what is left
+                const int64_t whole = left / 256, now = whole ? 256 : left;
+                const double step = now * bytes / kL2 > kStep[kind] ? now * bytes / kL2 : kStep[kind];
+                t += double(whole ? whole : 1) * p.gps * step;
+                left -= whole ? whole * 256 : left;
+            }
+            if (p.splits > 1) t += kJoin + 2.0 * p.splits * m * n * 4 / kPartial;
+            if (best.bm == 0 || t < least) {
+                best = p;
+                least = t;
+            }
+        }
+    }
+    if (best.splits > 1) best.workspace = size_t(best.splits) * size_t(m) * size_t(best.ntiles * best.bn) * 4;
+    return best;
 }
 
-hipError_t launch_fp8_linear(const Fp8LinearArgs& a, const Fp8Plan& p, int act, hipStream_t stream) {
-    return act == kActBf16 ? run<kActBf16>(a, p, stream) : run<kActF16>(a, p, stream);
+bool fp8_linear_quantizes(int64_t m, const Fp8Plan& p) { return p.kind == 0 && m <= FUSE && m * p.gps * (kGroup + 4) <= 49152; }
+
+hipError_t launch_fp8_linear(const Fp8LinearArgs& a, const Fp8Plan& p, int act, bool quantize, int act_fn, hipStream_t stream) {
+    const hipError_t e = act == kActBf16 ? run<kActBf16>(a, p, quantize, act_fn, stream) : run<kActF16>(a, p, quantize, act_fn, stream);
+    if (e != hipSuccess || p.splits == 1 || p.kind == 0) return e;
+    return launch_splitk_reduce(a.slots, p.splits, a.m, a.n, p.ntiles * p.bn, a.bias, a.y, a.ldy, act, stream);
 }
 
 }  // namespace w4a16

@@ -14,53 +14,6 @@ namespace w4a16 {
 
 namespace {
 
-constexpr uint32_t kAbs = 0x7FFFFFFFu, kInf = 0x7F800000u;
-
-// The magnitude's bits order numbers, infinities and NaNs as integers do.
-__device__ inline uint32_t magnitude(float v) { return __float_as_uint(v) & kAbs; }
-
-__device__ inline float fp8_scale(uint32_t top) { return top >= kInf ? __uint_as_float(0x7FC00000u) : __uint_as_float(top) / kFp8Max; }
-
-// four values of a group with the largest magnitude `top` and scale s as codes
-__device__ inline uint32_t fp8_codes(float a, float b, float c, float d, float s, uint32_t top) {
-    if (top >= kInf) return kFp8Nan * 0x01010101u;
-    if (s == 0.0f) return 0;
-    auto q = [&](float v) { return fminf(fmaxf(v / s, -kFp8Max), kFp8Max); };
-    int w = __builtin_amdgcn_cvt_pk_fp8_f32(q(a), q(b), 0, false);
-    return uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(q(c), q(d), w, true));
-}
-
-// Eight consecutive values from p as FP32.
-template <int DT>
-__device__ inline void load8(const void* p, int64_t at, float (&v)[8]) {
-    if constexpr (DT == 0) {
-        const float4 a = reinterpret_cast<const float4*>(static_cast<const float*>(p) + at)[0];
-        const float4 b = reinterpret_cast<const float4*>(static_cast<const float*>(p) + at)[1];
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-    } else {
-        const uint4 r = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at);
-        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[2 * i] = to_f32<DT>(uint16_t(w[i]));
-            v[2 * i + 1] = to_f32<DT>(uint16_t(w[i] >> 16));
-        }
-    }
-}
-
-__device__ inline uint32_t max8(const float (&v)[8]) {
-    uint32_t top = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) top = max(top, magnitude(v[i]));
-    return top;
-}
-
-template <int M>
-__device__ inline uint32_t max_xor(uint32_t v) {
-    return max(v, uint32_t(__builtin_amdgcn_ds_swizzle(int(v), 0x1F | (M << 10))));
-}
-
 // Rows: 16 lanes a group, 8 values a lane; GROUPS groups a lane, all loaded first.
 constexpr int kRowGroups = 4;
 
@@ -74,28 +27,14 @@ __global__ __launch_bounds__(256) void fp8_rows_kernel(Fp8QuantizeArgs a, uint32
         const uint32_t at = min(first + 16 * u, total - 1);
         const uint32_t row = at / groups, g = at - row * groups;
         const int64_t in = int64_t(row) * a.ldx + int64_t(g) * kGroup + sub * 8;
-        if constexpr (AF == kActFnNone) {
-            load8<DT>(a.x, in, v[u]);
-        } else {
-            const uint16_t* p = static_cast<const uint16_t*>(a.x) + in;
-            const uint4 x = *reinterpret_cast<const uint4*>(p);
-            const uint4 gate = AF == kActFnSwiglu ? *reinterpret_cast<const uint4*>(p + a.k) : uint4{};
-            const uint4 r = activate8<DT, AF>(x, gate);
-            const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                v[u][2 * i] = to_f32<DT>(uint16_t(w[i]));
-                v[u][2 * i + 1] = to_f32<DT>(uint16_t(w[i] >> 16));
-            }
-        }
+        fp8_load8<DT, AF>(a.x, in, a.k, v[u]);
     }
 #pragma unroll
     for (int u = 0; u < kRowGroups; ++u) {
         const uint32_t at = first + 16 * u;
-        const uint32_t top = max_xor<8>(max_xor<4>(max_xor<2>(max_xor<1>(max8(v[u])))));
+        const uint32_t top = fp8_group_top(v[u]);
         const float s = fp8_scale(top);
-        const uint2 c = make_uint2(fp8_codes(v[u][0], v[u][1], v[u][2], v[u][3], s, top),
-                                   fp8_codes(v[u][4], v[u][5], v[u][6], v[u][7], s, top));
+        const uint2 c = fp8_codes8(v[u], s, top);
         if (at < total) {
             *reinterpret_cast<uint2*>(a.codes + int64_t(at) * kGroup + sub * 8) = c;
             if (sub == 0) a.scales[at] = s;
@@ -115,10 +54,10 @@ __global__ __launch_bounds__(256) void fp8_blocks_kernel(Fp8QuantizeArgs a, uint
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
         const int64_t row = min(block * 128 + u * 16 + int64_t(threadIdx.x / 16), a.m - 1);
-        load8<DT>(a.x, row * a.ldx + g * kGroup + sub * 8, v[u]);
-        top = max(top, max8(v[u]));
+        fp8_load8<DT, kActFnNone>(a.x, row * a.ldx + g * kGroup + sub * 8, 0, v[u]);
+        top = max(top, fp8_top8(v[u]));
     }
-    top = max_xor<16>(max_xor<8>(max_xor<4>(max_xor<2>(max_xor<1>(top)))));
+    top = fp8_max_xor<16>(fp8_max_xor<8>(fp8_max_xor<4>(fp8_max_xor<2>(fp8_max_xor<1>(top)))));
     top = max(top, uint32_t(__shfl_xor(int(top), 32)));
     if (lane == 0) tops[threadIdx.x / 64] = top;
     __syncthreads();
@@ -128,8 +67,7 @@ __global__ __launch_bounds__(256) void fp8_blocks_kernel(Fp8QuantizeArgs a, uint
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
         const int64_t row = block * 128 + u * 16 + threadIdx.x / 16;
-        const uint2 c = make_uint2(fp8_codes(v[u][0], v[u][1], v[u][2], v[u][3], s, top),
-                                   fp8_codes(v[u][4], v[u][5], v[u][6], v[u][7], s, top));
+        const uint2 c = fp8_codes8(v[u], s, top);
         if (row < a.m) *reinterpret_cast<uint2*>(a.codes + row * a.k + g * kGroup + sub * 8) = c;
     }
 }
