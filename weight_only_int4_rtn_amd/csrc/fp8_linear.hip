@@ -17,9 +17,6 @@
 #include "fp8.h"
 #include "kernels.h"
 
-#ifndef FUSE
-#define FUSE 4
-#endif
 namespace w4a16 {
 
 namespace {
@@ -127,6 +124,11 @@ __device__ inline bool join_splits(float (&acc)[T][4], float* slot, unsigned* co
 // operands (rows of x from the caches); the waves' sums meet in LDS.
 // ---------------------------------------------------------------------------
 constexpr int kFewWaves = 4, kFewAhead = 4;
+// Groups of x that a workgroup may have to quantize itself (rows times groups of its part).  us a call with the quantizer
+// inside and apart, rows x K x N: 1 x 2048 x 2560 (16 groups) 4.7 and 7.7, 1 x 2048 x 32768 14.4 and 17.7, 2 x 4096 x 4096
+// (64) 9.1 and 10.6, 1 x 16384 x 2048 (64) 14.9 and 16.0, 4 x 2048 x 32768 (64) 19.9 and 21.4; with 96 and 128 groups, 3 x
+// 4096 x 4096 11.4 and 10.7, 2 x 16384 x 2048 19.4 and 16.4.
+constexpr int kFewGroups = 64;
 
 // QUANTIZE: x holds 16-bit values (of the output's type), which every workgroup quantizes for itself, activated by AF, while
 // its first rows of W are on their way.
@@ -134,7 +136,8 @@ template <int ACT, bool QUANTIZE, int AF>
 __global__ __launch_bounds__(64 * kFewWaves) void fp8_few_kernel(Fp8LinearArgs a, int splits, int gps) {
     __shared__ f32x4_t sums[kFewWaves][64];
     __shared__ int flag;
-    extern __shared__ __align__(16) uint8_t few[];  // QUANTIZE: codes [m][ng][128], scales [m][ng]
+    __shared__ __align__(16) uint8_t codes[QUANTIZE ? kFewGroups * kGroup : 16];  // [m][ng][128]
+    __shared__ float scales[QUANTIZE ? kFewGroups : 1];                           // [m][ng]
     const int lane = threadIdx.x % 64, wave = uniform(threadIdx.x / 64);
     const int r = lane % 16, kq = lane / 16;
     const int64_t groups = a.k / kGroup;
@@ -169,16 +172,26 @@ __global__ __launch_bounds__(64 * kFewWaves) void fp8_few_kernel(Fp8LinearArgs a
     for (int i = 0; i < kFewAhead; ++i)
         if (i < mine) load(ring[i], i);
     if constexpr (QUANTIZE) {
-        float* const scales = reinterpret_cast<float*>(few + a.m * ng * kGroup);
-        const int sub = threadIdx.x % 16;
-        for (int e = threadIdx.x / 16; e < int(a.m) * ng; e += 4 * kFewWaves) {
-            const int at = e / ng, g = e % ng;
-            float v[8];
-            fp8_load8<ACT, AF>(a.x, at * a.ldx + int64_t(g0 + g) * kGroup + sub * 8, a.k, v);
-            const uint32_t top = fp8_group_top(v);
+        constexpr int N = kFewGroups / (4 * kFewWaves);
+        const int sub = threadIdx.x % 16, e0 = threadIdx.x / 16, all = int(a.m) * ng;
+        float v[N][8];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if (i * 4 * kFewWaves >= all) break;
+            const int e = min(e0 + i * 4 * kFewWaves, all - 1), at = e / ng, g = e - at * ng;
+            fp8_load8<ACT, AF>(a.x, at * a.ldx + int64_t(g0 + g) * kGroup + sub * 8, a.k, v[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if (i * 4 * kFewWaves >= all) break;
+            const int e = e0 + i * 4 * kFewWaves;
+            const uint32_t top = fp8_group_top(v[i]);
             const float s = fp8_scale(top);
-            *reinterpret_cast<uint2*>(few + e * kGroup + sub * 8) = fp8_codes8(v, s, top);
-            if (sub == 0) scales[e] = s;
+            const uint2 c = fp8_codes8(v[i], s, top);
+            if (e < all) {
+                *reinterpret_cast<uint2*>(codes + e * kGroup + sub * 8) = c;
+                if (sub == 0) scales[e] = s;
+            }
         }
         lds_barrier();
     }
@@ -189,8 +202,8 @@ __global__ __launch_bounds__(64 * kFewWaves) void fp8_few_kernel(Fp8LinearArgs a
             if constexpr (QUANTIZE) {
                 const int e = row * ng + wave + (c + i) * kFewWaves;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) ring[i].x[h] = *reinterpret_cast<const u32x4*>(few + e * kGroup + 64 * h + 16 * kq);
-                ring[i].xs = reinterpret_cast<const float*>(few + a.m * ng * kGroup)[e];
+                for (int h = 0; h < 2; ++h) ring[i].x[h] = *reinterpret_cast<const u32x4*>(codes + e * kGroup + 64 * h + 16 * kq);
+                ring[i].xs = scales[e];
             }
             const f32x4_t p = fp8_mfma(ring[i].w, ring[i].x);
             const float f = ring[i].xs * ring[i].ws;
@@ -428,8 +441,7 @@ hipError_t run_tiles(const Fp8LinearArgs& a, const Fp8Plan& p, hipStream_t strea
 
 template <int ACT, bool QUANTIZE, int AF>
 hipError_t run_few(const Fp8LinearArgs& a, const Fp8Plan& p, hipStream_t stream) {
-    const size_t lds = QUANTIZE ? size_t(a.m) * size_t(p.gps) * (kGroup + 4) : 0;
-    fp8_few_kernel<ACT, QUANTIZE, AF><<<dim3(unsigned(p.ntiles * p.splits)), dim3(64 * kFewWaves), lds, stream>>>(a, p.splits, p.gps);
+    fp8_few_kernel<ACT, QUANTIZE, AF><<<dim3(unsigned(p.ntiles * p.splits)), dim3(64 * kFewWaves), 0, stream>>>(a, p.splits, p.gps);
     return hipGetLastError();
 }
 
@@ -506,7 +518,7 @@ Fp8Plan plan_fp8_linear(int64_t m, int64_t n, int64_t k) {
     return best;
 }
 
-bool fp8_linear_quantizes(int64_t m, const Fp8Plan& p) { return p.kind == 0 && m <= FUSE && m * p.gps * (kGroup + 4) <= 49152; }
+bool fp8_linear_quantizes(int64_t m, const Fp8Plan& p) { return p.kind == 0 && m * p.gps <= kFewGroups; }
 
 hipError_t launch_fp8_linear(const Fp8LinearArgs& a, const Fp8Plan& p, int act, bool quantize, int act_fn, hipStream_t stream) {
     const hipError_t e = act == kActBf16 ? run<kActBf16>(a, p, quantize, act_fn, stream) : run<kActF16>(a, p, quantize, act_fn, stream);

@@ -138,7 +138,12 @@ struct Kv4AttentionArgs {
     // of a shared prefix (below) only
     const int32_t* cu_groups;  // null: one group of all requests
     int64_t groups;
-    float* parts;  // [tokens][heads] rows: sums of dim channels, then [tokens][heads][2] references and sums of probabilities
+    const int32_t* prefix_lens;
+    int64_t prefix_room;  // tokens that a prefix's pages hold
+    int prefix_span, prefix_splits;
+    // what the splits of the prefixes' launch leave for the other: [splits][tokens][heads] rows of dim sums, then
+    // [splits][tokens][heads][2] references and sums of probabilities
+    float* parts;
 };
 
 struct Kv4Plan {
@@ -163,7 +168,7 @@ struct Kv4PrefixArgs {
 };
 struct Kv4PrefixPlan {
     Kv4Plan prefix, own;
-    size_t parts, workspace;  // after the header: the prefixes' rows, then the larger plan's
+    size_t parts, workspace;  // after the header: what the prefixes' splits leave, then the own plan's
 };
 Kv4PrefixPlan plan_kv4_prefix(int64_t tokens, int64_t batch, int64_t groups, int heads, int kv_heads, int dim,
                               int64_t prefix_capacity, int64_t capacity, bool ragged, bool causal);

@@ -62,8 +62,8 @@ struct View {
 };
 
 // What a launch computes: a whole attention, the part of it over the groups'
-// shared prefixes, or the part over the requests' own tokens, which takes the
-// other part in.
+// shared prefixes, whose splits leave their sums as they are, or the part over
+// the requests' own tokens, which begins with those sums.
 enum Part { kWhole = 0, kPrefix = 1, kOwn = 2 };
 
 // First query token of group j (a request outside the batch is its end).
@@ -172,77 +172,6 @@ struct Side {
         }
     }
 };
-
-// Where the parts of a row meet (kPrefix, kOwn): its sums over the prefix, one
-// channel a lane and register as the kernels hold them, and {reference, sum of
-// probabilities}.
-struct Meeting {
-    float *sums, *stats;
-    __device__ Meeting(const Kv4AttentionArgs& a, int64_t token, int head) {
-        const int64_t row = token * a.heads + head;
-        sums = a.parts + row * a.dim;
-        stats = a.parts + a.tokens * a.heads * a.dim + row * 2;
-    }
-};
-
-// Whether request b has a prefix's part to take in.
-__device__ inline bool in_group(const Kv4AttentionArgs& a, int b) {
-    return !a.cu_groups || (b >= a.cu_groups[0] && b < a.cu_groups[a.groups]);
-}
-
-// Takes the prefix's part into a row's sums of N consecutive channels at a time:
-// the factors of both parts.
-struct Taken {
-    float mine = 1.0f, other = 0.0f;
-    // ref, sum: of the own tokens; sum becomes that of both
-    __device__ void stats(const Meeting& m, float ref, float& sum) {
-        const float r = m.stats[0], s = m.stats[1];
-        const float top = fmaxf(ref, r);
-        mine = ref == -INFINITY ? 0.0f : exp2_fast(ref - top);
-        other = r == -INFINITY ? 0.0f : exp2_fast(r - top);
-        sum = sum * mine + s * other;
-    }
-    __device__ float operator()(float v, float prefix) const { return v * mine + prefix * other; }
-};
-
-// A row's sums over the prefix left for the own part: this lane's channels, CH
-// consecutive ones for each block and register.
-template <int D>
-__device__ inline void leave(const Meeting& m, const f32x4_t (&acc)[kv4_blocks(D)][kv4_width(D) / 16], float ref, float sum, int kq) {
-    constexpr int W = kv4_width(D), NB = kv4_blocks(D), CH = W / 16;
-#pragma unroll
-    for (int b = 0; b < NB; ++b)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int i = 0; i < CH; i += 4)
-                *reinterpret_cast<float4*>(m.sums + W * b + CH * (4 * kq + j) + i) =
-                    make_float4(acc[b][i][j], acc[b][i + 1][j], acc[b][i + 2][j], acc[b][i + 3][j]);
-    if (kq == 0) *reinterpret_cast<float2*>(m.stats) = make_float2(ref, sum);
-}
-
-// The prefix's part of a row joined to the own part's.
-template <int D>
-__device__ inline void take(const Kv4AttentionArgs& a, const Tile& t, int64_t token, int head,
-                            f32x4_t (&acc)[kv4_blocks(D)][kv4_width(D) / 16], float ref, float& sum, int kq) {
-    constexpr int W = kv4_width(D), NB = kv4_blocks(D), CH = W / 16;
-    if (!in_group(a, t.b)) return;
-    const Meeting m(a, token, head);
-    Taken f;
-    f.stats(m, ref, sum);
-#pragma unroll
-    for (int b = 0; b < NB; ++b)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int i = 0; i < CH; i += 4) {
-                const float4 v = *reinterpret_cast<const float4*>(m.sums + W * b + CH * (4 * kq + j) + i);
-                acc[b][i][j] = f(acc[b][i][j], v.x);
-                acc[b][i + 1][j] = f(acc[b][i + 1][j], v.y);
-                acc[b][i + 2][j] = f(acc[b][i + 2][j], v.z);
-                acc[b][i + 3][j] = f(acc[b][i + 3][j], v.w);
-            }
-}
 
 // Workspace of a split: per (tile, key head, split) the accumulators in lane
 // order, then the 16 rows' references and sums.
@@ -371,6 +300,83 @@ __device__ inline uint4 weights(const float (&w)[2][NB][4], int b) {
                       pack_f16(w[1][b][0], w[1][b][1]), pack_f16(w[1][b][2], w[1][b][3]));
 }
 
+// What a split of the prefixes' launch leaves of a row, and where its request's own part begins.
+struct Left {
+    float *sums, *stats;  // a lane's channels: CH consecutive ones for each block and register; {reference, sum of probabilities}
+    __device__ Left(const Kv4AttentionArgs& a, int split, int64_t token, int head) {
+        const int64_t rows = a.tokens * a.heads, row = split * rows + token * a.heads + head;
+        sums = a.parts + row * a.dim;
+        stats = a.parts + a.prefix_splits * rows * a.dim + row * 2;
+    }
+};
+
+template <int D>
+__device__ inline void leave(const Left& to, const f32x4_t (&acc)[kv4_blocks(D)][kv4_width(D) / 16], float ref, float sum, int kq) {
+    constexpr int W = kv4_width(D), NB = kv4_blocks(D), CH = W / 16;
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int i = 0; i < CH; i += 4)
+                *reinterpret_cast<float4*>(to.sums + W * b + CH * (4 * kq + j) + i) =
+                    make_float4(acc[b][i][j], acc[b][i + 1][j], acc[b][i + 2][j], acc[b][i + 3][j]);
+    if (kq == 0) *reinterpret_cast<float2*>(to.stats) = make_float2(ref, sum);
+}
+
+// Splits of the prefix that request b shares (0: it is in no group), as the prefixes' launch cut it.
+__device__ inline int prefix_splits(const Kv4AttentionArgs& a, int b) {
+    int64_t j = 0;
+    if (a.cu_groups) {
+        int lo = 0, hi = int(a.groups) - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) / 2;
+            if (a.cu_groups[mid] <= b) lo = mid;
+            else hi = mid - 1;
+        }
+        if (b < a.cu_groups[lo] || b >= a.cu_groups[lo + 1]) return 0;
+        j = lo;
+    }
+    const int64_t n = a.prefix_lens[j];
+    const int len = int(n < 0 ? 0 : n > a.prefix_room ? a.prefix_room : n);
+    return max(1, min(a.prefix_splits, (len + a.prefix_span - 1) / a.prefix_span));
+}
+
+// A wave begins its running softmax of a row with the prefix's splits first, first + step, ... < live: they are as good as
+// tokens that it has seen before its own.
+template <int D>
+__device__ inline void take(const Kv4AttentionArgs& a, int first, int live, int step, int64_t token, int head, int kq, Running& run,
+                            f32x4_t (&acc)[kv4_blocks(D)][kv4_width(D) / 16]) {
+    constexpr int W = kv4_width(D), NB = kv4_blocks(D), CH = W / 16;
+    for (int s = first; s < live; s += step) {
+        const Left from(a, s, token, head);
+        const float2 st = *reinterpret_cast<const float2*>(from.stats);
+        float4 v[NB][4][CH / 4];
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int i = 0; i < CH / 4; ++i) v[b][j][i] = *reinterpret_cast<const float4*>(from.sums + W * b + CH * (4 * kq + j) + 4 * i);
+        const float now = fmaxf(run.ref, st.x);
+        const float f0 = run.ref == -INFINITY ? 0.0f : exp2_fast(run.ref - now);
+        const float f1 = st.x == -INFINITY ? 0.0f : exp2_fast(st.x - now);
+        run.ref = now;
+        run.sum = run.sum * f0 + (kq == 0 ? st.y * f1 : 0.0f);  // the lanes of a row add theirs at the end
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int i = 0; i < CH / 4; ++i) {
+                    acc[b][4 * i][j] = acc[b][4 * i][j] * f0 + v[b][j][i].x * f1;
+                    acc[b][4 * i + 1][j] = acc[b][4 * i + 1][j] * f0 + v[b][j][i].y * f1;
+                    acc[b][4 * i + 2][j] = acc[b][4 * i + 2][j] * f0 + v[b][j][i].z * f1;
+                    acc[b][4 * i + 3][j] = acc[b][4 * i + 3][j] * f0 + v[b][j][i].w * f1;
+                }
+    }
+}
+
 constexpr uint32_t kOnes = 0x3C003C00u;  // two f16 ones
 
 // One workgroup: 16 rows of one key head over one split of the tokens.  Its
@@ -440,6 +446,9 @@ __global__ __launch_bounds__(256, D == 256 ? 2 : D == 128 ? 3 : 4) void kv4_atte
     }
     Running run;
 
+    if constexpr (PART == kOwn) {
+        if (blockIdx.z == 0) take<D>(a, wave, prefix_splits(a, t.b), WAVES, t.q0 + qi, hd, kq, run, acc);
+    }
     for (int step = 0; step < steps; ++step) {
         const int tok = first + step * 32 * WAVES;
         const uint32_t there = uint32_t(ch.there >> (2 * (step % 32))) & 3;
@@ -551,14 +560,13 @@ __global__ __launch_bounds__(256, D == 256 ? 2 : D == 128 ? 3 : 4) void kv4_atte
         __syncthreads();
     }
     uint16_t* dst = a.out + (t.q0 + qi) * a.ldo + int64_t(hd) * D;
-    if (live == 1) {
+    if (PART == kPrefix || live == 1) {
         if (wave != 0 || t.r0 + col > last) return;
         sum = row_sum(sum);
         if constexpr (PART == kPrefix) {
-            leave<D>(Meeting(a, t.q0 + qi, hd), acc, ref, sum, kq);
+            leave<D>(Left(a, int(blockIdx.z), t.q0 + qi, hd), acc, ref, sum, kq);
             return;
         }
-        if constexpr (PART == kOwn) take<D>(a, t, t.q0 + qi, hd, acc, ref, sum, kq);
         const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
 #pragma unroll
         for (int b = 0; b < NB; ++b)
@@ -650,30 +658,6 @@ __global__ __launch_bounds__(256, D == 256 ? 2 : D == 128 ? 3 : 4) void kv4_atte
         }
     }
     if (t.r0 + col > last) return;
-    if constexpr (PART == kPrefix) {
-        const Meeting m(a, t.q0 + qi, hd);
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-                for (int i = 0; i < PER; ++i) m.sums[W * b + CH * (4 * kq + j) + PER * wave + i] = out[b][i][j];
-        if (wave == 0 && kq == 0) *reinterpret_cast<float2*>(m.stats) = make_float2(ref, total);
-        return;
-    }
-    if constexpr (PART == kOwn) {
-        if (in_group(a, t.b)) {
-            const Meeting m(a, t.q0 + qi, hd);
-            Taken f;
-            f.stats(m, ref, total);
-#pragma unroll
-            for (int b = 0; b < NB; ++b)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-#pragma unroll
-                    for (int i = 0; i < PER; ++i) out[b][i][j] = f(out[b][i][j], m.sums[W * b + CH * (4 * kq + j) + PER * wave + i]);
-        }
-    }
     const float inv = total > 0.0f ? 1.0f / total : 0.0f;
 #pragma unroll
     for (int b = 0; b < NB; ++b)
@@ -850,6 +834,9 @@ __global__ __launch_bounds__(256, D == 256 ? 2 : 4) void kv4_rows_kernel(Kv4Atte
     }
     Running run;
 
+    if constexpr (PART == kOwn) {
+        if (blockIdx.y == 0) take<D>(a, 0, prefix_splits(a, t.b), 1, t.q0 + qi, hd, kq, run, acc);
+    }
     if (steps > 0) raw.store(stage[0], wave, lane);
     if (steps > 1) there[2] = load();
     for (int step = 0; step < steps; ++step) {
@@ -927,7 +914,7 @@ __global__ __launch_bounds__(256, D == 256 ? 2 : 4) void kv4_rows_kernel(Kv4Atte
 #pragma unroll
         for (int i = 0; i < CH; ++i) acc[b][i] -= kKvOffset * ps[b];
     float sum = row_sum(run.sum), ref = run.ref;
-    if (live > 1) {
+    if (PART != kPrefix && live > 1) {
         // as in the kernel above: the last split to finish joins them all
         const int mine = int(blockIdx.y) * kSlot + wave * kGroupBytes;
 #pragma unroll
@@ -979,10 +966,9 @@ __global__ __launch_bounds__(256, D == 256 ? 2 : 4) void kv4_rows_kernel(Kv4Atte
     }
     if (t.r0 + 16 * wave + col > last) return;
     if constexpr (PART == kPrefix) {
-        leave<D>(Meeting(a, t.q0 + qi, hd), acc, ref, sum, kq);
+        leave<D>(Left(a, int(blockIdx.y), t.q0 + qi, hd), acc, ref, sum, kq);
         return;
     }
-    if constexpr (PART == kOwn) take<D>(a, t, t.q0 + qi, hd, acc, ref, sum, kq);
     const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
     uint16_t* dst = a.out + (t.q0 + qi) * a.ldo + int64_t(hd) * D;
 #pragma unroll
@@ -1108,25 +1094,28 @@ Kv4PrefixPlan plan_kv4_prefix(int64_t tokens, int64_t batch, int64_t groups, int
     Kv4PrefixPlan p{};
     p.prefix = plan_kv4_attention(tokens, groups, heads, kv_heads, dim, prefix_capacity, true, false, 0);
     p.own = plan_kv4_attention(tokens, batch, heads, kv_heads, dim, capacity, ragged, causal, 0);
-    p.parts = size_t(tokens) * size_t(heads) * size_t(dim + 2) * 4;
+    p.parts = size_t(p.prefix.splits) * size_t(tokens) * size_t(heads) * size_t(dim + 2) * 4;
     p.parts = (p.parts + 15) / 16 * 16;
-    p.workspace = p.parts + (p.prefix.workspace > p.own.workspace ? p.prefix.workspace : p.own.workspace);
+    p.workspace = p.parts + p.own.workspace;
     return p;
 }
 
 hipError_t launch_kv4_prefix(const Kv4PrefixArgs& a, int act, hipStream_t stream) {
-    const Kv4AttentionArgs& o = a.own;
+    Kv4AttentionArgs o = a.own;
     const Kv4PrefixPlan p = plan_kv4_prefix(o.tokens, o.batch, o.groups, o.heads, o.kv_heads, o.dim, a.table_width * o.page,
                                             o.table_width * o.page, o.cu_q != nullptr, o.causal != 0);
-    float* const partials = after_header(o.workspace, p.parts);
+    o.prefix_lens = a.lens;
+    o.prefix_room = a.table_width * o.page;
+    o.prefix_span = int(p.prefix.span);
+    o.prefix_splits = p.prefix.splits;
     Kv4AttentionArgs f = o;
     f.table = a.table;
     f.table_width = a.table_width;
     f.ldt = a.ldt;
     f.kv_lens = a.lens;
     f.causal = 0;
-    const hipError_t e = run_by_type<kPrefix>(f, p.prefix, partials, act, stream);
-    return e == hipSuccess ? run_by_type<kOwn>(o, p.own, partials, act, stream) : e;
+    const hipError_t e = run_by_type<kPrefix>(f, p.prefix, nullptr, act, stream);
+    return e == hipSuccess ? run_by_type<kOwn>(o, p.own, after_header(o.workspace, p.parts), act, stream) : e;
 }
 
 }  // namespace w4a16
