@@ -1092,8 +1092,35 @@ hipError_t launch_kv4_attention(const Kv4AttentionArgs& a, int act, hipStream_t 
 Kv4PrefixPlan plan_kv4_prefix(int64_t tokens, int64_t batch, int64_t groups, int heads, int kv_heads, int dim,
                               int64_t prefix_capacity, int64_t capacity, bool ragged, bool causal) {
     Kv4PrefixPlan p{};
-    p.prefix = plan_kv4_attention(tokens, groups, heads, kv_heads, dim, prefix_capacity, true, false, 0);
+    const int64_t share = heads / kv_heads;
+    // Parts of `most` tokens that fill the chip once, of at least sqrt(c most) tokens.
+    auto cut = [&](Kv4Plan& q, int64_t most, int64_t c) {
+        const int64_t base = q.tiles * kv_heads, room = 256 * (dim == 256 ? 2 : dim == 64 || q.rows > 16 ? 4 : 3);
+        int64_t least = 128;
+        while (least * least < c * most) least += 64;
+        q.span = base < room ? ceil_div(ceil_div(most, room / base), 64) * 64 : most;
+        if (q.span < least) q.span = least;
+        q.splits = int(ceil_div(most, q.span));
+    };
+    // The prefixes.  Tiles of 64 rows share the codes' conversion, tiles of 16 have more workgroups and no barriers in
+    // their steps.  us on tiles of 16 against 64, requests x heads / key heads on tokens, with the pairs of a row and a token
+    // in M:  D = 128  64 x 32/8 on 8192 (17) 43 against 46, on 16384 (34) 66 against 61, 128 x 32/8 on 8192 (34) 72 against 68,
+    // 3 x 8 of 20 queries x 32/8 on 2000 (31) 72 against 60, four groups of 48 x 32/8 on 20000 to 32768 (160) 248 against
+    // 176, but 16 x 32/8 on 65536 (34) 68 against 75;  D = 256  256 x 8/1 on 4096 (8) 44 against 49;  D = 64  256 x 8/2
+    // on 8192 (17) 29 and 29.  A part leaves its sums in memory for the other launch instead of joining them, but that
+    // launch has to read them: parts of at least sqrt(48 tokens) (2 x 32/8 on 16384, D = 128: 23 us, sqrt(12 tokens) 24,
+    // sqrt(tokens) 29, sqrt(100 tokens) 26); twice as many as fill the chip 49 us for 64 x 32/8 on 8192, 43 once.
+    // (the grid of tiles of 64 is one line of tiles and key heads, which has to fit)
+    p.prefix.rows = tokens * heads * prefix_capacity < int64_t(24) << 20 || (tokens * share / 64 + groups) * kv_heads >= int64_t(1) << 23 ? 16 : 64;
+    p.prefix.tiles = tokens * share / p.prefix.rows + groups;
+    cut(p.prefix, prefix_capacity, 48);
+    // The requests' own tokens, few as a rule: once over the chip where kv4_attention goes twice (64 x 32/8 on 4096, up to
+    // 500 of their own: 35 us against 42; up to 4000: 71 and 71).
     p.own = plan_kv4_attention(tokens, batch, heads, kv_heads, dim, capacity, ragged, causal, 0);
+    if (!ragged && p.own.splits > 1) {
+        cut(p.own, capacity, 12);
+        p.own.workspace = p.own.splits > 1 ? size_t(p.own.tiles * kv_heads) * size_t(p.own.splits) * size_t(p.own.rows / 16) * size_t(16 * dim + 32) * 4 : 0;
+    }
     p.parts = size_t(p.prefix.splits) * size_t(tokens) * size_t(heads) * size_t(dim + 2) * 4;
     p.parts = (p.parts + 15) / 16 * 16;
     p.workspace = p.parts + p.own.workspace;
