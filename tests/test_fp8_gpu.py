@@ -164,3 +164,188 @@ SIZES = [(1, 1, 128), (1, 16, 128), (1, 100, 256), (1, 2560, 2048), (2, 33, 640)
 @pytest.mark.parametrize("m,n,k", SIZES)
 def test_linear(m, n, k, dtype):
     check_linear(m, n, k, dtype, (m + n) % 2 == 0, require_gpu())
+
+
+@pytest.mark.parametrize("act", ["swiglu", "gelu_tanh"])
+@pytest.mark.parametrize("m,n,k,dtype", [(1, 130, 256, BF16), (1, 300, 2048, F16), (3, 200, 640, BF16), (4, 64, 2048, F16), (9, 100, 384, BF16),
+                                         (40, 300, 1024, F16), (150, 129, 256, BF16), (300, 512, 640, F16)])
+def test_linear_activated(m, n, k, dtype, act):
+    """A fused activation is `quantize_fp8` with it and the product of those codes: the same codes whoever quantizes."""
+    dev = require_gpu()
+    cw, sw, codes, scales = layer(n, k, n + m, dev)
+    x = rows(m, 2 * k if act == "swiglu" else k, dtype, m + k, 0.4).to(dev)
+    bias = rows(1, n, dtype, 3, 0.0)[0]
+    say("linear_fp8", m, n, k, dtype, act)
+    y = w4.linear_fp8(x, codes, scales, bias.to(dev), act=ACTS[act])
+    cx, sx = w4.quantize_fp8(x, act=ACTS[act])
+    want, tol = R.linear(bytes_of(cx).reshape(m, k), sx.cpu().numpy(), cw, sw, bias)
+    R.within(y, want, tol, f"{act} {m} x {n} x {k}")
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 100, 256), (2, 64, 8192), (16, 300, 640), (20, 130, 384), (130, 300, 640), (300, 200, 2048)])
+@pytest.mark.parametrize("dtype", [None, BF16, F16])
+def test_linear_of_codes(m, n, k, dtype):
+    """x that is quantized already, in rows of a wider tensor; the same bits as the layer that quantizes for itself."""
+    dev = require_gpu()
+    cw, sw, codes, scales = layer(n, k, n, dev)
+    x = rows(m, k, dtype or BF16, m, 0.5)
+    cx, sx = w4.quantize_fp8(x.to(dev))
+    wide = torch.zeros(m, k + 48, dtype=torch.uint8, device=dev)
+    wide[:, 16:k + 16] = cx.view(torch.uint8)
+    say("linear_fp8 of codes", m, n, k, dtype)
+    y = w4.linear_fp8(wide.view(torch.float8_e4m3fn)[:, 16:k + 16], codes, scales, x_scales=sx, out_dtype=dtype)
+    assert y.dtype == (dtype or BF16)
+    want, tol = R.linear(bytes_of(cx).reshape(m, k), sx.cpu().numpy(), cw, sw)
+    R.within(y, want, tol, f"codes {m} x {n} x {k}")
+    assert torch.equal(y, w4.linear_fp8(x.to(dev), codes, scales)), "quantized in the call: other bits"
+
+
+def test_linear_exact_integers():
+    """Small integers with scales of powers of two: every product and sum is exact in FP32, in every kernel and split, so the
+    output is the exact result rounded once."""
+    dev = require_gpu()
+    g = torch.Generator().manual_seed(5)
+    for m, n, k in SIZES + [(3, 2048, 16384), (64, 256, 16384), (40, 2100, 1024)]:
+        cx = torch.randint(-4, 5, (m, k), generator=g).float()
+        cw = torch.randint(-3, 4, (n, k), generator=g).float()
+        sx = 2.0 ** torch.randint(-2, 3, (m, k // 128), generator=g)
+        sw = 2.0 ** torch.randint(-2, 3, (-(-n // 128), k // 128), generator=g)
+        # sparse: sums of some hundreds in steps of 2^-4
+        cx *= torch.rand(m, k, generator=g) < 8 / k
+        want = torch.zeros(m, n, dtype=torch.float64)
+        for i in range(k // 128):
+            c = slice(128 * i, 128 * i + 128)
+            want += (cx[:, c].double() @ cw[:, c].double().t()) * sx[:, i:i + 1].double() * sw[:, i].double().repeat_interleave(128)[:n]
+        say("exact", m, n, k)
+        y = w4.linear_fp8(cx.to(dev).to(torch.float8_e4m3fn), cw.to(dev).to(torch.float8_e4m3fn), sw.to(dev), x_scales=sx.to(dev), out_dtype=F16)
+        assert torch.equal(y.cpu(), want.to(F16)), (m, n, k)
+
+
+def test_linear_views_and_shapes():
+    """Rows at odd addresses, broadcast or permuted, more dimensions, none, rows of weights that end inside a block."""
+    dev = require_gpu()
+    n, k = 200, 256
+    cw, sw, codes, scales = layer(n, k, 9, dev)
+    base = rows(24, 1024, BF16, 17).to(dev)
+    for x in (base[:, :k], base[::2, 128:384], base[:, 4:260], base[:, 1:257], base.view(4, 6, 1024)[:, :, 256:512], base[:1, :k].expand(20, k),
+              base.view(4, 6, 1024).transpose(0, 1)[..., :k], base[3, :k]):
+        y = w4.linear_fp8(x, codes, scales)
+        assert y.shape == (*x.shape[:-1], n)
+        flat = x.reshape(-1, k)
+        assert torch.equal(y.reshape(-1, n), w4.linear_fp8(flat.contiguous(), codes, scales))
+        want, tol = R.linear(*R.quantize_rows(flat.float().cpu().numpy()), cw, sw)
+        R.within(y.reshape(-1, n), want, tol, str(tuple(x.shape)))
+    assert w4.linear_fp8(base[:0, :k], codes, scales).shape == (0, n)
+    assert w4.linear_fp8(base[:, :k], codes[:0], scales[:0]).shape == (24, 0)
+
+
+@pytest.mark.parametrize("m", [1, 3, 16, 40, 140, 300])
+def test_linear_not_finite(m):
+    """A NaN or an infinity in x makes its row NaN, one in W's block the columns of that block; the others are as without."""
+    dev = require_gpu()
+    n, k = 300, 384
+    w = torch.randn(n, k, generator=torch.Generator().manual_seed(2))
+    x = rows(m, k, BF16, m)
+    clean = w4.linear_fp8(x.to(dev), *w4.quantize_fp8_weight(w.to(dev)))
+    bad = x.clone()
+    bad[m // 2, 200] = float("inf")
+    y = w4.linear_fp8(bad.to(dev), *w4.quantize_fp8_weight(w.to(dev)))
+    keep = torch.arange(m) != m // 2
+    assert torch.isnan(y[m // 2]).all() and torch.equal(y[keep.to(dev)], clean[keep.to(dev)])
+    w[130, 5] = float("nan")
+    y = w4.linear_fp8(x.to(dev), *w4.quantize_fp8_weight(w.to(dev)))
+    assert torch.isnan(y[:, 128:256]).all()
+    assert torch.equal(y[:, :128], clean[:, :128]) and torch.equal(y[:, 256:], clean[:, 256:])
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 2560, 2048), (1, 64, 16384), (12, 64, 16384), (64, 256, 16384), (40, 300, 2048), (300, 512, 1024)])
+def test_linear_streams_graphs_and_repeats(m, n, k):
+    """Two runs, another stream, two graphs on one workspace, replays between eager calls: the same bits; the header stays zero."""
+    dev = require_gpu()
+    _, _, codes, scales = layer(n, k, 1, dev)
+    x = rows(m, k, BF16, m).to(dev)
+    say("streams and graphs", m, n, k)
+    want = w4.linear_fp8(x, codes, scales)
+    assert torch.equal(want, w4.linear_fp8(x, codes, scales))
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        got = w4.linear_fp8(x, codes, scales)
+    side.synchronize()
+    assert torch.equal(got, want)
+    need = w4.linear_fp8_workspace_bytes(m, n, k)
+    ws = torch.zeros(max(need, 16), dtype=torch.uint8, device=dev)
+    graphs, outs = [torch.cuda.CUDAGraph() for _ in range(2)], []
+    torch.cuda.synchronize()
+    for graph in graphs:
+        with torch.cuda.graph(graph):
+            outs.append(w4.linear_fp8(x, codes, scales, workspace=ws))
+    for rep in range(4):
+        out = outs[rep % 2]
+        out.fill_(float("nan"))
+        graphs[rep % 2].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want), f"replay {rep}"
+        assert torch.equal(w4.linear_fp8(x, codes, scales), want)
+    assert not ws[:1 << 20].any(), "the workspace's header is not zero"
+    if need:
+        with pytest.raises(ValueError, match="workspace"):
+            with torch.cuda.graph(torch.cuda.CUDAGraph()):
+                w4.linear_fp8(x, codes, scales)
+
+
+def test_quantize_in_a_graph():
+    dev = require_gpu()
+    x = rows(300, 1024, F16, 3).to(dev)
+    want = w4.quantize_fp8(x)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        got = w4.quantize_fp8(x)
+    for _ in range(3):
+        got[1].zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got[0].view(torch.uint8), want[0].view(torch.uint8)) and torch.equal(got[1], want[1])
+
+
+def test_linear_shares_a_workspace():
+    """One workspace serves this layer, the INT4 layer and the cache's operators in turn."""
+    dev = require_gpu()
+    _, _, codes, scales = layer(2048, 16384, 1, dev)
+    ws = torch.zeros(64 << 20, dtype=torch.uint8, device=dev)
+    x = rows(64, 16384, BF16, 3).to(dev)
+    packed = w4.pack(*w4.quantize(torch.randn(2048, 16384, device=dev) * 0.02))
+    a, b = w4.linear_fp8(x, codes, scales), w4.linear(x, packed, 2048)
+    for m in (64, 1, 12):
+        assert torch.equal(w4.linear_fp8(x[:m], codes, scales, workspace=ws), w4.linear_fp8(x[:m], codes, scales))
+        assert torch.equal(w4.linear(x, packed, 2048, workspace=ws), b)
+    assert torch.equal(w4.linear_fp8(x, codes, scales, workspace=ws), a)
+
+
+def test_linear_far_rows():
+    """Codes and outputs beyond 4 GiB of their tensors."""
+    dev = require_gpu()
+    n, k, m = 20480, 262144, 24  # 5 GiB of codes
+    codes = torch.zeros(n, k, dtype=torch.uint8, device=dev)
+    g = torch.Generator().manual_seed(1)
+    w = torch.randn(130, k, generator=g)
+    cw, sw = R.quantize_blocks(w.numpy())
+    codes[-130:] = torch.from_numpy(cw).to(dev)
+    scales = torch.zeros(n // 128, k // 128, device=dev)
+    # the last 130 rows lie in the last two blocks of 128
+    full = np.zeros((256, k), np.uint8)
+    full[-130:] = cw
+    two = np.repeat(np.float32([[0.5], [0.25]]), k // 128, 1)
+    scales[-2:] = torch.from_numpy(two).to(dev)
+    x = rows(m, k, BF16, 2, 0.2)
+    for count in (1, m):
+        y = w4.linear_fp8(x[:count].to(dev), codes.view(torch.float8_e4m3fn), scales)
+        assert not y[:, :-256].any()
+        cx, sx = R.quantize_rows(x[:count].float().numpy())
+        some = np.r_[120:130, 250:256]
+        a = torch.from_numpy(R.decode(cx) * np.repeat(sx.astype(np.float64), 128, 1))
+        b = torch.from_numpy(R.decode(full[some]) * np.repeat(two.astype(np.float64)[some // 128], 128, 1))
+        want, size = a @ b.t(), a.abs() @ b.abs().t()
+        # products cut 2^-13 below the largest of eight: at most 7 x 2^-13 of the eight's sum of sizes; 2048 groups in FP32
+        R.within(y[:, -256:].cpu()[:, some], want, size * (7 * 2.0 ** -13 + 2.0 ** -23 * (2048 + 19)), "far rows")
