@@ -11,7 +11,7 @@ import math
 import torch
 
 from ._binding import BF16, GROUP, Act, _act_tag, _check, _w_tag, lib
-from ._serving import _dense, _device_index, _meta, _no_grad, _on_device, _raw_stream, _remember, _workspace
+from ._serving import _dense, _device_index, _meta, _no_grad, _launch, _raw_stream, _remember, _workspace
 
 E4M3 = 3  # W4A16_E4M3 of include/w4a16.h
 CODES = torch.float8_e4m3fn
@@ -70,12 +70,12 @@ def _width(width: int, act: Act) -> int:
 @_remember
 def _quantize_plan(x, act):
     shape, stride, dtype = x
-    tag = _act_tag(dtype)
+    tag, act = _act_tag(dtype), Act(act)
     if len(shape) < 1:
         raise ValueError("x must have at least one dimension")
     k = _width(shape[-1], act)
     rows = _rows(shape, stride, 2)
-    return tag, k, rows, (*shape[:-1], k), (*shape[:-1], k // GROUP)
+    return tag, int(act), k, rows, (*shape[:-1], k), (*shape[:-1], k // GROUP)
 
 
 def quantize_fp8(x: torch.Tensor, act: Act = Act.NONE) -> tuple[torch.Tensor, torch.Tensor]:
@@ -84,17 +84,15 @@ def quantize_fp8(x: torch.Tensor, act: Act = Act.NONE) -> tuple[torch.Tensor, to
     max|x| / 448 per row and 128 columns.  ``act``: activation applied first, as
     in ``linear`` (SwiGLU rows hold [up | gate], 2k values).  A group with a NaN
     or an infinity becomes NaN.  See quantize_fp8_rows in include/w4a16.h."""
-    act = Act(act)
-    tag, k, rows, shape, groups = _quantize_plan(_meta(x), act)
+    tag, act, k, rows, shape, groups = _quantize_plan(_meta(x), act)
     _no_grad(x)
     index = _device_index(x)
     if rows is None or x.data_ptr() % 16:
-        x = x.contiguous() if rows is None else x.clone(memory_format=torch.contiguous_format)
+        x = x.clone(memory_format=torch.contiguous_format)
         rows = math.prod(shape[:-1]), x.shape[-1]
     codes, scales = x.new_empty(shape, dtype=CODES), x.new_empty(groups, dtype=torch.float32)
-    with _on_device(index):
-        st = _lib().quantize_fp8_rows(x.data_ptr(), tag, int(act), rows[0], k, rows[1], codes.data_ptr(), scales.data_ptr(),
-                                      _raw_stream(index))
+    st = _launch(index, _lib().quantize_fp8_rows, x.data_ptr(), tag, act, rows[0], k, rows[1], codes.data_ptr(), scales.data_ptr(),
+                 _raw_stream(index))
     if st:
         _check(st, "quantize_fp8")
     return codes, scales
@@ -114,8 +112,7 @@ def quantize_fp8_weight(w: torch.Tensor) -> tuple[torch.Tensor, torch.Tensor]:
     if rows is None or w.data_ptr() % 16:
         w, rows = w.clone(memory_format=torch.contiguous_format), (n, k)
     codes, scales = w.new_empty((n, k), dtype=CODES), w.new_empty((-(-n // GROUP), k // GROUP), dtype=torch.float32)
-    with _on_device(index):
-        st = _lib().quantize_fp8_blocks(w.data_ptr(), tag, n, k, rows[1], codes.data_ptr(), scales.data_ptr(), _raw_stream(index))
+    st = _launch(index, _lib().quantize_fp8_blocks, w.data_ptr(), tag, n, k, rows[1], codes.data_ptr(), scales.data_ptr(), _raw_stream(index))
     if st:
         _check(st, "quantize_fp8_weight")
     return codes, scales
@@ -129,6 +126,7 @@ def linear_fp8_workspace_bytes(m: int, n: int, k: int, codes: bool = False) -> i
 @_remember
 def _linear_plan(x, codes, scales, bias, x_scales, out_dtype, act):
     shape, stride, dtype = x
+    act = Act(act)
     is_codes = dtype == CODES
     if is_codes and act != Act.NONE:
         raise ValueError("x of codes takes no activation")
@@ -154,7 +152,7 @@ def _linear_plan(x, codes, scales, bias, x_scales, out_dtype, act):
         raise ValueError(f"x_scales must be a contiguous float32 {(*shape[:-1], k // GROUP)} tensor")
     rows = _rows(shape, stride, 1 if is_codes else 2)
     need = int(_lib().fp8_linear_workspace_bytes(tag, m, n, k))
-    return tag, out_tag, out_dtype, m, n, k, rows, (*shape[:-1], n), need
+    return tag, out_tag, int(act), out_dtype, m, n, k, rows, (*shape[:-1], n), need
 
 
 def linear_fp8(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, bias: torch.Tensor | None = None, act: Act = Act.NONE,
@@ -166,9 +164,8 @@ def linear_fp8(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, bias:
     or a checkpoint's).  With ``act=Act.SWIGLU`` the rows of x are [up | gate], 2k
     values.  x of float8_e4m3fn codes comes with ``x_scales`` [..., k / 128]; y is
     then of ``out_dtype`` (default bfloat16).  See fp8_linear in include/w4a16.h."""
-    act = Act(act)
-    tag, out_tag, out_dtype, m, n, k, rows, shape, need = _linear_plan(_meta(x), _meta(codes), _meta(scales), _meta(bias),
-                                                                       _meta(x_scales), out_dtype, act)
+    tag, out_tag, act, out_dtype, m, n, k, rows, shape, need = _linear_plan(_meta(x), _meta(codes), _meta(scales), _meta(bias),
+                                                                            _meta(x_scales), out_dtype, act)
     _no_grad(x, scales, bias, x_scales)
     index = _device_index(x, codes, scales, bias, x_scales, workspace)
     if rows is None or x.data_ptr() % 16:
@@ -181,10 +178,9 @@ def linear_fp8(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, bias:
         raise ValueError("codes must be 16-byte aligned")
     stream = _raw_stream(index)
     ws, ws_bytes = _workspace(workspace, need, index, stream)
-    with _on_device(index):
-        st = _lib().fp8_linear(x.data_ptr(), tag, None if x_scales is None else x_scales.data_ptr(), int(act), m, k, rows[1],
-                               codes.data_ptr(), scales.data_ptr(), n, None if bias is None else bias.data_ptr(), y.data_ptr(), out_tag,
-                               n, ws, ws_bytes, stream)
+    st = _launch(index, _lib().fp8_linear, x.data_ptr(), tag, None if x_scales is None else x_scales.data_ptr(), act, m, k, rows[1],
+                 codes.data_ptr(), scales.data_ptr(), n, None if bias is None else bias.data_ptr(), y.data_ptr(), out_tag, n, ws, ws_bytes,
+                 stream)
     if st:
         _check(st, "linear_fp8")
     return y

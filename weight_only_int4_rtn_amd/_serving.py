@@ -106,21 +106,16 @@ def _device_index(first, *others) -> int:
     return index
 
 
-class _on_device:
-    """The current device while a call launches on tensors of another one."""
-    __slots__ = ("index", "before")
-
-    def __init__(self, index):
-        self.index = index
-
-    def __enter__(self):
-        self.before = torch._C._cuda_getDevice()
-        if self.before != self.index:
-            torch.cuda.set_device(self.index)
-
-    def __exit__(self, *_):
-        if self.before != self.index:
-            torch.cuda.set_device(self.before)
+def _launch(index: int, call, *args) -> int:
+    """call(*args) with the tensors' device current."""
+    before = torch._C._cuda_getDevice()
+    if before == index:
+        return call(*args)
+    torch.cuda.set_device(index)
+    try:
+        return call(*args)
+    finally:
+        torch.cuda.set_device(before)
 
 
 def _no_grad(*ts):
@@ -416,12 +411,10 @@ def kv4_prefix_attention(q: torch.Tensor, pool: torch.Tensor, prefix_table: torc
         return out
     stream = _raw_stream(index)
     ws, ws_bytes = _workspace(workspace, need, index, stream)
-    with _on_device(index):
-        st = _lib().kv4_prefix_attention(q.data_ptr(), tag, tokens, ldq, heads, kv_heads, dim, pool.data_ptr(), pages, page,
-                                         prefix_table.data_ptr(), prefix_width, ldp, prefix_lens.data_ptr(),
-                                         None if cu_groups is None else cu_groups.data_ptr(), groups, block_table.data_ptr(), width, ldt,
-                                         kv_lens.data_ptr(), None if cu_q is None else cu_q.data_ptr(), batch, causal,
-                                         dim ** -0.5 if scale is None else scale, out.data_ptr(), heads * dim, ws, ws_bytes, stream)
+    st = _launch(index, _lib().kv4_prefix_attention, q.data_ptr(), tag, tokens, ldq, heads, kv_heads, dim, pool.data_ptr(), pages, page,
+                 prefix_table.data_ptr(), prefix_width, ldp, prefix_lens.data_ptr(), None if cu_groups is None else cu_groups.data_ptr(),
+                 groups, block_table.data_ptr(), width, ldt, kv_lens.data_ptr(), None if cu_q is None else cu_q.data_ptr(), batch, causal,
+                 dim ** -0.5 if scale is None else scale, out.data_ptr(), heads * dim, ws, ws_bytes, stream)
     if st:
         _check(st, "kv4_prefix_attention")
     return out

@@ -14,23 +14,21 @@ namespace w4a16 {
 
 namespace {
 
-// Rows: 16 lanes a group, 8 values a lane; GROUPS groups a lane, all loaded first.
-constexpr int kRowGroups = 4;
-
-template <int DT, int AF>
+// Rows: 16 lanes a group, 8 values a lane; N groups a lane, all loaded first.
+template <int DT, int AF, int N>
 __global__ __launch_bounds__(256) void fp8_rows_kernel(Fp8QuantizeArgs a, uint32_t groups, uint32_t total) {
     const int sub = threadIdx.x % 16;
-    const uint32_t first = blockIdx.x * uint32_t(16 * kRowGroups) + threadIdx.x / 16;
-    float v[kRowGroups][8];
+    const uint32_t first = blockIdx.x * uint32_t(16 * N) + threadIdx.x / 16;
+    float v[N][8];
 #pragma unroll
-    for (int u = 0; u < kRowGroups; ++u) {
+    for (int u = 0; u < N; ++u) {
         const uint32_t at = min(first + 16 * u, total - 1);
         const uint32_t row = at / groups, g = at - row * groups;
         const int64_t in = int64_t(row) * a.ldx + int64_t(g) * kGroup + sub * 8;
         fp8_load8<DT, AF>(a.x, in, a.k, v[u]);
     }
 #pragma unroll
-    for (int u = 0; u < kRowGroups; ++u) {
+    for (int u = 0; u < N; ++u) {
         const uint32_t at = first + 16 * u;
         const uint32_t top = fp8_group_top(v[u]);
         const float s = fp8_scale(top);
@@ -72,11 +70,16 @@ __global__ __launch_bounds__(256) void fp8_blocks_kernel(Fp8QuantizeArgs a, uint
     }
 }
 
+// Below so many groups a lane takes one, more waves the sooner; above it four, whose loads fill memory's queue.  us on one and
+// on four, rows x columns: 1 x 2048 2.3 and 3.7, 777 x 4096 4.7 and 6.1, 4096 x 4096 12.9 and 14.3, 4096 x 16384 (524288
+// groups) 44.6 and 45.6, 8192 x 16384 89 and 84 (4.79 TB/s, a large copy's rate); with SwiGLU 2048 x 4096 11.5 and 13.2.
+constexpr uint32_t kOneGroup = 600000;
+
 template <int DT, int AF>
 hipError_t rows(const Fp8QuantizeArgs& a, hipStream_t stream) {
     const uint32_t groups = uint32_t(a.k / kGroup), total = uint32_t(a.m) * groups;
-    const uint32_t grid = uint32_t(ceil_div(total, 16 * kRowGroups));
-    fp8_rows_kernel<DT, AF><<<dim3(grid), dim3(256), 0, stream>>>(a, groups, total);
+    if (total < kOneGroup) fp8_rows_kernel<DT, AF, 1><<<dim3(uint32_t(ceil_div(total, 16))), dim3(256), 0, stream>>>(a, groups, total);
+    else fp8_rows_kernel<DT, AF, 4><<<dim3(uint32_t(ceil_div(total, 64))), dim3(256), 0, stream>>>(a, groups, total);
     return hipGetLastError();
 }
 
