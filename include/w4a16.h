@@ -571,10 +571,20 @@ w4a16_status_t kv4_attention(const void* q, w4a16_dtype_t dtype, int64_t tokens,
                              const int32_t* cu_q, int64_t batch, int causal, int64_t window, float scale, void* out,
                              int64_t ldo, void* workspace, size_t workspace_bytes, void* stream);
 
-/* Workspace bytes of kv4_prefix_attention (0: invalid or empty sizes); header rules as above. */
+/* Workspace bytes of kv4_prefix_attention (0: none needed, or invalid or empty sizes); header rules as above. */
 size_t kv4_prefix_attention_workspace_bytes(int64_t tokens, int64_t batch, int64_t groups, int64_t heads, int64_t kv_heads,
                                             int64_t head_dim, int64_t prefix_width, int64_t table_width, int64_t page_size,
                                             int ragged, int causal);
+
+/*
+ * Rows (query tokens times the heads that share a key head) of a workgroup's
+ * tile over the prefixes in kv4_prefix_attention for these sizes: 16 or 64, each
+ * a kernel of its own; 0 where one launch takes each request's prefix and own
+ * tokens together (and for invalid sizes or no tokens).
+ */
+int kv4_prefix_attention_tile_rows(int64_t tokens, int64_t batch, int64_t groups, int64_t heads, int64_t kv_heads,
+                                   int64_t head_dim, int64_t prefix_width, int64_t table_width, int64_t page_size, int ragged,
+                                   int causal);
 
 /*
  * kv4_attention for requests that begin with the same tokens: group j's
@@ -592,8 +602,9 @@ size_t kv4_prefix_attention_workspace_bytes(int64_t tokens, int64_t batch, int64
  *   kv_lens       tokens of the request beyond the prefix, its query tokens
  *                 among them; may be 0 for a query token that is in the cache
  *                 nowhere.  table_width is at least 1 also then.
- * The other arguments, limits and roundings are kv4_attention's.  Two launches:
- * the prefixes' sums pass through the workspace in FP32.
+ * The other arguments, limits and roundings are kv4_attention's.  One launch
+ * where there is little to share; else two, between which the prefixes' sums pass
+ * through the workspace in FP32.
  */
 w4a16_status_t kv4_prefix_attention(const void* q, w4a16_dtype_t dtype, int64_t tokens, int64_t ldq, int64_t heads,
                                     int64_t kv_heads, int64_t head_dim, const void* pool, int64_t pages, int64_t page_size,

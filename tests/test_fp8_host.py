@@ -149,8 +149,8 @@ def test_linear_workspace(lib):
 
 
 def prefix(lib, **kw):
-    d = dict(q=A, dtype=B.F16, tokens=4, ldq=512, heads=4, kv_heads=1, dim=128, pool=A + GB, pages=8, page=16, ptable=A + 2 * GB, pwidth=4,
-             ldp=4, plens=A + 3 * GB, cug=None, groups=1, table=A + 4 * GB, width=4, ldt=4, lens=A + 5 * GB, cu=None, batch=4, causal=1,
+    d = dict(q=A, dtype=B.F16, tokens=4, ldq=512, heads=4, kv_heads=1, dim=128, pool=A + GB, pages=8, page=16, ptable=A + 2 * GB, pwidth=400,
+             ldp=400, plens=A + 3 * GB, cug=None, groups=1, table=A + 4 * GB, width=4, ldt=4, lens=A + 5 * GB, cu=None, batch=4, causal=1,
              scale=0.1, out=A + 6 * GB, ldo=512, ws=A + 7 * GB, ws_bytes=GB)
     d.update(kw)
     return lib.kv4_prefix_attention(*d.values(), None)
@@ -162,7 +162,7 @@ def prefix(lib, **kw):
     (dict(page=17), B.EINVAL), (dict(pages=0), B.EINVAL), (dict(width=0), B.EINVAL), (dict(pwidth=0), B.EINVAL), (dict(groups=0), B.EINVAL),
     (dict(groups=2), B.EINVAL), (dict(pwidth=1 << 24, ldp=1 << 24), B.EINVAL), (dict(pwidth=1 << 62, ldp=1 << 62), B.EINVAL),
     (dict(groups=(1 << 20) + 1, cug=A + 8 * GB), B.EINVAL), (dict(ldq=504), B.EINVAL), (dict(ldo=516), B.EINVAL), (dict(ldt=3), B.EINVAL),
-    (dict(ldp=3), B.EINVAL), (dict(scale=float("nan")), B.EINVAL), (dict(q=None), B.EINVAL), (dict(pool=None), B.EINVAL),
+    (dict(ldp=399), B.EINVAL), (dict(scale=float("nan")), B.EINVAL), (dict(q=None), B.EINVAL), (dict(pool=None), B.EINVAL),
     (dict(ptable=None), B.EINVAL), (dict(plens=None), B.EINVAL), (dict(table=None), B.EINVAL), (dict(lens=None), B.EINVAL), (dict(out=None), B.EINVAL),
     (dict(q=A + 8), B.EINVAL), (dict(out=A + 6 * GB + 8), B.EINVAL), (dict(ptable=A + 2), B.EINVAL), (dict(plens=A + 1), B.EINVAL),
     (dict(cug=A + 2, groups=1), B.EINVAL), (dict(out=A), B.EINVAL), (dict(out=A + GB), B.EINVAL), (dict(out=A + 2 * GB), B.EINVAL),
@@ -178,9 +178,14 @@ def test_prefix_workspace(lib):
     f = w4.kv4_prefix_attention_workspace_bytes
     assert f(0, 0, 1, 4, 1, 128, 10, 10, 16) == 0 and f(4, 4, 1, 4, 3, 128, 10, 10, 16) == 0 and f(4, 4, 0, 4, 1, 128, 10, 10, 16) == 0
     assert f(4, 3, 1, 4, 1, 128, 10, 10, 16) == 0 and f(4, 4, 1, 4, 1, 128, 0, 10, 16) == 0
-    # one part of the prefix: a row of sums and two statistics each
-    assert f(4, 4, 1, 4, 1, 128, 1, 1, 16) == (1 << 20) + 4 * 4 * 130 * 4
-    assert f(4, 4, 1, 4, 1, 128, 4096, 1, 16) > f(4, 4, 1, 4, 1, 128, 64, 1, 16)
+    rows = w4.kv4_prefix_attention_tile_rows
+    # little to share: one launch, which needs nothing for one part
+    assert rows(4, 4, 1, 4, 1, 128, 1, 1, 16) == 0 and f(4, 4, 1, 4, 1, 128, 1, 1, 16) == 0
+    assert rows(4, 4, 1, 4, 1, 128, 400, 1, 16) == 0 and f(4, 4, 1, 4, 1, 128, 400, 1, 16) > 1 << 20
+    # apart: at least a row of sums and two statistics of each query and head
+    assert rows(64, 64, 1, 32, 8, 128, 128, 4, 64) == 16 and rows(192, 192, 4, 32, 8, 128, 256, 8, 128) == 64
+    assert f(64, 64, 1, 32, 8, 128, 128, 4, 64) >= (1 << 20) + 64 * 32 * 130 * 4
+    assert rows(4, 3, 1, 4, 1, 128, 10, 10, 16) == 0 and rows(0, 0, 1, 4, 1, 128, 10, 10, 16) == 0
 
 
 # ---------------------------------------------------------------------------

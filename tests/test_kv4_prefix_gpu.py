@@ -51,6 +51,13 @@ class Batch:
                  b.to(self.dev), ints(self.own if own is None else own, self.dev)),
                 dict(cu_q=cu, cu_groups=None if self.one else ints(self.first, self.dev)))
 
+    def takes(self, rows):
+        """That a call runs on tiles of `rows` rows over the prefixes (0: together with the own tokens)."""
+        a, b = self.tables()
+        got = w4().kv4_prefix_attention_tile_rows(self.q.shape[0], len(self.own), len(self.prefix), self.q.shape[1], self.cache.hk,
+                                                  self.cache.d, a.shape[1], b.shape[1], self.cache.page, ragged=self.q_lens is not None)
+        assert got == rows, f"tiles of {got} rows, not {rows}"
+
     def run(self, causal=True, **kw):
         a, k = self.args(kw.pop("prefix", None), kw.pop("own", None))
         return w4().kv4_prefix_attention(*a, **k, causal=causal, **kw)
@@ -96,6 +103,22 @@ CASES = [
 ]
 
 
+# Calls with something to share take two launches: over the prefixes on tiles of 16 rows or 64, then over the own tokens.
+APART = [
+    (16, [1000], [1, 30, 0, 200, 64] * 13, [0, 65], None, 8, 8, 64, 16, True, "bf16"),
+    (16, [700, 0, 1500], [3, 1, 77] * 20, [0, 25, 30, 60], None, 16, 4, 64, 48, True, "f16"),
+    (16, [2049], [5, 0, 129, 40] * 12, [2, 47], None, 16, 8, 128, 64, True, "bf16"),        # requests of no group at both ends
+    (16, [900, 400], [1, 2, 300] * 14, [0, 20, 42], None, 24, 8, 128, 32, True, "f16"),
+    (16, [1100], [17, 9, 0, 60] * 12, [0, 48], None, 8, 8, 256, 16, True, "bf16"),
+    (16, [800, 1000], [30, 12, 9, 50] * 12, [0, 20, 48], [5, 12, 1, 8] * 12, 8, 8, 64, 16, True, "bf16"),
+    (16, [1400], [20, 12, 9, 40] * 11, [0, 44], [5, 20, 1, 8] * 11, 8, 4, 256, 32, False, "f16"),
+    (64, [1500, 900], [150, 90, 300, 40, 260, 17], [0, 3, 6], [140, 90, 280, 1, 233, 16], 32, 8, 64, 32, True, "f16"),
+    (64, [2100], [200, 333, 350, 31], [0, 4], [180, 333, 290, 31], 16, 2, 128, 64, True, "bf16"),
+    (64, [1700, 0, 60], [220, 333, 100, 7], [0, 2, 3, 4], [220, 300, 90, 9], 24, 8, 128, 16, False, "bf16"),
+    (64, [1600], [270, 1, 300, 310], [0, 4], [260, 1, 300, 301], 24, 3, 256, 16, True, "f16"),
+]
+
+
 def name(c):
     cut = lambda v: "_".join(map(str, v[:5])) + ("x" * (len(v) > 5))  # noqa: E731
     return f"p{cut(c[0])}-o{cut(c[1])}-q{cut(c[3]) if c[3] else 1}-h{c[4]}_{c[5]}-d{c[6]}-{'c' if c[8] else 'b'}-{c[9]}"
@@ -112,16 +135,54 @@ def test_prefix(dev, case):
     assert torch.equal(b.run(causal).view(torch.int16), out.view(torch.int16)), "two runs differ"
 
 
+@pytest.mark.parametrize("case", APART, ids=[f"t{c[0]}-" + name(c[1:]) for c in APART])
+def test_prefix_apart(dev, case):
+    rows, prefix, own, first, qs, h, hk, d, page, causal, dts = case
+    say("prefix apart", case)
+    b = Batch(dev, prefix, own, first, h, hk, d, page, DT[dts], qs)
+    b.takes(rows)
+    out = b.run(causal)
+    b.check(out, causal, what=str(case))
+    assert torch.equal(b.run(causal).view(torch.int16), out.view(torch.int16)), "two runs differ"
+
+
 @pytest.mark.parametrize("spread,vsize,voutlier,qsize,scale", [
     (1.0, 1e-3, 0.0, 1.5, None), (1.0, 3e4, 0.0, 1.5, None), (1.0, 1.0, 3000.0, 1.5, None), (40.0, 1.0, 0.0, 30.0, None),
     (1.0, 1.0, 0.0, 1.5, -0.3), (1e-4, 1.0, 0.0, 1e-4, 1.0), (1.0, 1.0, 0.0, 1e5, 1e-5),
 ], ids=["small_v", "large_v", "outlier_v", "one_hot", "negative_scale", "flat", "large_q"])
-@pytest.mark.parametrize("qs", [None, [70, 130, 1]], ids=["decode", "chunk"])
-def test_prefix_ranges(dev, spread, vsize, voutlier, qsize, scale, qs):
+@pytest.mark.parametrize("rows,qs", [(0, None), (0, [70, 130, 1]), (16, None), (64, [300, 450, 256])], ids=["decode", "chunk", "apart16", "apart64"])
+def test_prefix_ranges(dev, spread, vsize, voutlier, qsize, scale, rows, qs):
     say("prefix ranges", spread, vsize, voutlier, qsize, scale, qs)
-    b = Batch(dev, [600], [133, 200, 40], [0, 3], 8, 2, 128, 32, torch.bfloat16, qs, seed=3, qsize=qsize, spread=spread, vsize=vsize,
-              voutlier=voutlier)
+    if rows == 0:
+        b = Batch(dev, [600], [133, 200, 40], [0, 3], 8, 2, 128, 32, torch.bfloat16, qs, seed=3, qsize=qsize, spread=spread, vsize=vsize,
+                  voutlier=voutlier)
+    elif rows == 16:
+        b = Batch(dev, [1000], [33, 60, 1, 0] * 9, [0, 36], 8, 8, 128, 32, torch.bfloat16, qs, seed=3, qsize=qsize, spread=spread,
+                  vsize=vsize, voutlier=voutlier)
+    else:
+        b = Batch(dev, [1600], [300, 500, 260], [0, 3], 16, 4, 128, 32, torch.bfloat16, qs, seed=3, qsize=qsize, spread=spread,
+                  vsize=vsize, voutlier=voutlier)
+    b.takes(rows)
     b.check(b.run(scale=scale), scale=scale)
+
+
+@pytest.mark.parametrize("rows,qs", [(16, None), (64, [300, 450, 20, 290])], ids=["apart16", "apart64"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_prefix_apart_bad_pages_and_lengths(dev, rows, qs, d):
+    say("bad pages apart", rows, d)
+    heads, own, first = (16, [300, 500, 20, 290], [0, 1, 4]) if qs else (8, [20, 33, 1, 64] * 16, [0, 20, 64])
+    b = Batch(dev, [1500, 700], own, first, heads, 8, d, 32, torch.bfloat16, qs)
+    b.takes(rows)
+    n = 2 + len(own)
+    there = [np.ones(64, bool) for _ in range(n)]
+    for i, p, bad in ((0, 2, -1), (0, 40, b.cache.pool.shape[0]), (1, 0, 2 ** 31 - 1), (2, 0, -2 ** 31), (n - 1, 1, 10 ** 6)):
+        b.cache.table[i, p] = bad
+        there[i][p] = False
+    b.check(b.run(), there=there, what="bad pages")
+    short = [1100, 0]
+    mine = own[:]
+    mine[1] = 0 if qs is None else own[1]
+    b.check(b.run(prefix=[1100, -5], own=mine), prefix=short, own=mine, there=there, what="lengths")
 
 
 @pytest.mark.parametrize("qs", [None, [40, 9, 30]], ids=["decode", "chunk"])
@@ -186,11 +247,15 @@ def test_prefix_equals_attention_over_both(dev):
     assert ((a - c).abs() <= 2.0 ** -9 * a.abs() + 2.0 ** -9 * a.abs().amax()).all()
 
 
-@pytest.mark.parametrize("qs", [None, [40, 200, 8]], ids=["decode", "chunk"])
-def test_prefix_on_another_stream_and_in_a_graph(dev, qs):
+@pytest.mark.parametrize("rows,qs", [(0, None), (0, [40, 200, 8]), (16, None), (64, [300, 450, 256])], ids=["decode", "chunk", "apart16", "apart64"])
+def test_prefix_on_another_stream_and_in_a_graph(dev, rows, qs):
     lib = w4()
-    say("stream and graph", qs)
-    b = Batch(dev, [3000], [100, 250, 9], [0, 3], 8, 2, 128, 32, torch.bfloat16, qs)
+    say("stream and graph", rows, qs)
+    own = [100, 250, 9] if rows == 0 else [40, 33, 1] * 12 if rows == 16 else [300, 480, 260]
+    changed = [99, 210, 8] if rows == 0 else [39, 0, 1] * 12 if rows == 16 else [300, 470, 256]
+    heads = 16 if rows == 64 else 8
+    b = Batch(dev, [3000], own, [0, len(own)], heads, 2 if rows == 0 else 8, 128, 32, torch.bfloat16, qs)
+    b.takes(rows)
     want = b.run()
     args, kw = b.args()
     torch.cuda.synchronize()
@@ -199,10 +264,7 @@ def test_prefix_on_another_stream_and_in_a_graph(dev, qs):
         got = lib.kv4_prefix_attention(*args, **kw)
     side.synchronize()
     assert torch.equal(got, want)
-    with pytest.raises(ValueError, match="workspace"):
-        with torch.cuda.graph(torch.cuda.CUDAGraph()):
-            lib.kv4_prefix_attention(*args, **kw)
-    need = lib.kv4_prefix_attention_workspace_bytes(b.q.shape[0], 3, 1, 8, 2, 128, args[2].shape[1], args[4].shape[1], 32, ragged=qs is not None)
+    need = lib.kv4_prefix_attention_workspace_bytes(b.q.shape[0], len(own), 1, heads, b.cache.hk, 128, args[2].shape[1], args[4].shape[1], 32, ragged=qs is not None)
     ws, out = torch.zeros(need, dtype=torch.uint8, device=dev), torch.empty_like(args[0])
     graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
     torch.cuda.synchronize()
@@ -217,27 +279,35 @@ def test_prefix_on_another_stream_and_in_a_graph(dev, qs):
         assert torch.equal(lib.kv4_prefix_attention(*args, **kw), want)
     # other lengths in the same graph: the plan does not depend on them
     args[3].copy_(ints([1700], dev))
-    args[5].copy_(ints([99, 210, 8], dev))
+    args[5].copy_(ints(changed, dev))
     graphs[0].replay()
     torch.cuda.synchronize()
-    b.check(out, prefix=[1700], own=[99, 210, 8], what="replay with other lengths")
+    b.check(out, prefix=[1700], own=changed, what="replay with other lengths")
     assert not ws[:1 << 20].any(), "the workspace's header is not zero"
 
 
+@pytest.mark.parametrize("rows", [0, 16, 64])
 @pytest.mark.parametrize("d", [64, 128, 256])
-def test_prefix_nan_tokens(dev, d):
+def test_prefix_nan_tokens(dev, d, rows):
     """A key of the prefix that is NaN makes every row of its group and heads NaN, an own one its request's; others stay."""
     say("NaN tokens", d)
     lib = w4()
-    b = Batch(dev, [200, 90], [40, 33, 20], [0, 2, 3], 4, 2, d, 16, torch.bfloat16)
-    x = torch.full((1, 4 * d), float("nan"), dtype=torch.bfloat16, device=dev)
-    x[:, d:2 * d] = x[:, 3 * d:] = 1.0  # the second head stays a number
+    if rows == 0:
+        b = Batch(dev, [200, 90], [40, 33, 20], [0, 2, 3], 4, 2, d, 16, torch.bfloat16)
+    elif rows == 16:
+        b = Batch(dev, [1500, 900], [40, 33, 20] * 20, [0, 2, 60], 8, 8, d, 16, torch.bfloat16)
+    else:
+        b = Batch(dev, [1500, 900], [300, 433, 320], [0, 2, 3], 32, 8, d, 16, torch.bfloat16, [300, 1, 300])
+    b.takes(rows)
+    hk = b.cache.hk
+    x = torch.ones(1, 2 * hk, d, dtype=torch.bfloat16, device=dev)  # the other heads stay numbers
+    x[:, 0] = x[:, hk] = float("nan")
     page = b.cache.page
     slot = int(b.cache.table[1, 50 // page]) * page + 50 % page          # the second group's prefix
     mine = int(b.cache.table[2 + 1, 7 // page]) * page + 7 % page        # request 1's own tokens
     for s in (slot, mine):
-        lib.kv4_append(x, b.cache.pool, torch.tensor([s], device=dev), d)
-    out = b.run().cpu()
-    assert torch.isnan(out[1:, :2]).all() and torch.isfinite(out[:, 2:]).all() and torch.isfinite(out[0]).all()
-    b.counts = [1]
-    b.check(out[:1], what="the first request")
+        lib.kv4_append(x.flatten(1), b.cache.pool, torch.tensor([s], device=dev), d)
+    out, share, n = b.run().cpu(), b.q.shape[1] // hk, b.counts[0]
+    assert torch.isnan(out[n:, :share]).all() and torch.isfinite(out[:, share:]).all() and torch.isfinite(out[:n]).all()
+    b.counts = [n]
+    b.check(out[:n], what="the first request")

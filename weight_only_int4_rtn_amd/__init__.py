@@ -69,6 +69,7 @@ from ._serving import (  # noqa: F401
     kv4_page_size,
     kv4_pool,
     kv4_prefix_attention,
+    kv4_prefix_attention_tile_rows,
     kv4_prefix_attention_workspace_bytes,
     kv4_read,
     lora_add,

@@ -36,6 +36,8 @@ def _lib():
         L.kv4_attention.restype = i32
         L.kv4_prefix_attention_workspace_bytes.argtypes = [i64] * 9 + [i32, i32]
         L.kv4_prefix_attention_workspace_bytes.restype = sz
+        L.kv4_prefix_attention_tile_rows.argtypes = [i64] * 9 + [i32, i32]
+        L.kv4_prefix_attention_tile_rows.restype = i32
         L.kv4_prefix_attention.argtypes = [vp, i32, i64, i64, i64, i64, i64, vp, i64, i64, vp, i64, i64, vp, vp, i64, vp, i64, i64,
                                            vp, vp, i64, i32, ctypes.c_float, vp, i64, vp, sz, vp]
         L.kv4_prefix_attention.restype = i32
@@ -368,6 +370,14 @@ def kv4_prefix_attention_workspace_bytes(tokens: int, batch: int, groups: int, h
     """Workspace kv4_prefix_attention needs for these sizes (``ragged``: cu_q is given)."""
     return _prefix_need(tokens, batch, groups, heads, kv_heads, head_dim, prefix_width, table_width, page_size, int(bool(ragged)),
                         int(bool(causal)))
+
+
+def kv4_prefix_attention_tile_rows(tokens: int, batch: int, groups: int, heads: int, kv_heads: int, head_dim: int, prefix_width: int,
+                                   table_width: int, page_size: int, ragged: bool = False, causal: bool = True) -> int:
+    """Rows of a workgroup's tile over the prefixes in kv4_prefix_attention for these sizes: 16 or 64, each a kernel of its
+    own, or 0 where one launch takes each request's prefix and own tokens together."""
+    return _lib().kv4_prefix_attention_tile_rows(tokens, batch, groups, heads, kv_heads, head_dim, prefix_width, table_width, page_size,
+                                                 int(bool(ragged)), int(bool(causal)))
 
 
 @_remember

@@ -138,8 +138,9 @@ struct Kv4AttentionArgs {
     // of a shared prefix (below) only
     const int32_t* cu_groups;  // null: one group of all requests
     int64_t groups;
+    const int32_t* prefix_table;
+    int64_t prefix_width, ldp;
     const int32_t* prefix_lens;
-    int64_t prefix_room;  // tokens that a prefix's pages hold
     int prefix_span, prefix_splits;
     // what the splits of the prefixes' launch leave for the other: [splits][tokens][heads] rows of dim sums, then
     // [splits][tokens][heads][2] references and sums of probabilities
@@ -158,20 +159,16 @@ Kv4Plan plan_kv4_attention(int64_t tokens, int64_t batch, int heads, int kv_head
 hipError_t launch_kv4_attention(const Kv4AttentionArgs& a, int act, hipStream_t stream);
 
 // A shared prefix: one launch over the prefixes, whose "requests" are groups of
-// requests (table, table_width, ldt, kv_lens of the prefixes), then one over the
-// requests' own tokens, which joins both.
-struct Kv4PrefixArgs {
-    Kv4AttentionArgs own;
-    const int32_t* table;
-    int64_t table_width, ldt;
-    const int32_t* lens;
-};
+// requests, then one over the requests' own tokens, which takes both together;
+// or, where there is little to share, one launch over each request's prefix and
+// own tokens.
 struct Kv4PrefixPlan {
+    bool together;      // one launch, of the plan `own`
     Kv4Plan prefix, own;
     size_t parts, workspace;  // after the header: what the prefixes' splits leave, then the own plan's
 };
 Kv4PrefixPlan plan_kv4_prefix(int64_t tokens, int64_t batch, int64_t groups, int heads, int kv_heads, int dim,
                               int64_t prefix_capacity, int64_t capacity, bool ragged, bool causal);
-hipError_t launch_kv4_prefix(const Kv4PrefixArgs& a, int act, hipStream_t stream);
+hipError_t launch_kv4_prefix(const Kv4AttentionArgs& a, int act, hipStream_t stream);
 
 }  // namespace w4a16

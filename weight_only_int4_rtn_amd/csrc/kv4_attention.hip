@@ -62,15 +62,32 @@ struct View {
 };
 
 // What a launch computes: a whole attention, the part of it over the groups'
-// shared prefixes, whose splits leave their sums as they are, or the part over
-// the requests' own tokens, which begins with those sums.
-enum Part { kWhole = 0, kPrefix = 1, kOwn = 2 };
+// shared prefixes, whose splits leave their sums as they are, the part over the
+// requests' own tokens, which begins with those sums, or each request's prefix
+// and own tokens one after the other.
+enum Part { kWhole = 0, kPrefix = 1, kOwn = 2, kBoth = 3 };
 
 // First query token of group j (a request outside the batch is its end).
 __device__ inline int64_t group_start(const Kv4AttentionArgs& a, int64_t j) {
     int64_t b = a.cu_groups ? a.cu_groups[j] : j ? a.batch : 0;
     b = b < 0 ? 0 : b > a.batch ? a.batch : b;
     return a.cu_q ? a.cu_q[b] : b;
+}
+
+// The group of request b (-1: none), and how many tokens its prefix has.
+__device__ inline int group_of(const Kv4AttentionArgs& a, int b) {
+    if (!a.cu_groups) return 0;
+    int lo = 0, hi = int(a.groups) - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (a.cu_groups[mid] <= b) lo = mid;
+        else hi = mid - 1;
+    }
+    return b >= a.cu_groups[lo] && b < a.cu_groups[lo + 1] ? lo : -1;
+}
+__device__ inline int prefix_len(const Kv4AttentionArgs& a, int group) {
+    const int64_t n = a.prefix_lens[group], room = a.prefix_width * a.page;
+    return int(n < 0 ? 0 : n > room ? room : n);
 }
 
 // Tiles are numbered without a table: request b's start at
@@ -131,6 +148,22 @@ struct Chunks {
         const int in = c - p * per;
         int id = -1;
         if (c * 16 < end && p < int(a.table_width)) id = row[p];
+        place(a, id, in, region, chunk_bytes);
+    }
+    // The same along a prefix of `len` tokens, padded to `own` (a multiple of 32), and the request's tokens behind it.
+    __device__ void find_both(const Kv4AttentionArgs& a, uint32_t magic, const int32_t* prefix, int len, int own, const int32_t* row,
+                              int64_t region, int chunk_bytes, int first, int stride, int end, int lane) {
+        const int at = first + lane / 2 * stride + lane % 2;
+        const bool mine = at * 16 >= own;
+        const int c = mine ? at - own / 16 : at;
+        const int per = a.page / 16;
+        const int p = per == 1 ? c : int(__umulhi(uint32_t(c), magic));
+        const int in = c - p * per;
+        int id = -1;
+        if (mine ? at * 16 < end && p < int(a.table_width) : c * 16 < len && p < int(a.prefix_width)) id = mine ? row[p] : prefix[p];
+        place(a, id, in, region, chunk_bytes);
+    }
+    __device__ void place(const Kv4AttentionArgs& a, int id, int in, int64_t region, int chunk_bytes) {
         const bool ok = id >= 0 && id < a.pages;
         const uint64_t at = uint64_t(ok ? id : 0) * uint64_t(a.kv_heads * region);
         code = ok ? uint32_t((at + uint64_t(in) * chunk_bytes) >> 7) : 0;
@@ -326,20 +359,9 @@ __device__ inline void leave(const Left& to, const f32x4_t (&acc)[kv4_blocks(D)]
 
 // Splits of the prefix that request b shares (0: it is in no group), as the prefixes' launch cut it.
 __device__ inline int prefix_splits(const Kv4AttentionArgs& a, int b) {
-    int64_t j = 0;
-    if (a.cu_groups) {
-        int lo = 0, hi = int(a.groups) - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) / 2;
-            if (a.cu_groups[mid] <= b) lo = mid;
-            else hi = mid - 1;
-        }
-        if (b < a.cu_groups[lo] || b >= a.cu_groups[lo + 1]) return 0;
-        j = lo;
-    }
-    const int64_t n = a.prefix_lens[j];
-    const int len = int(n < 0 ? 0 : n > a.prefix_room ? a.prefix_room : n);
-    return max(1, min(a.prefix_splits, (len + a.prefix_span - 1) / a.prefix_span));
+    const int group = group_of(a, b);
+    if (group < 0) return 0;
+    return max(1, min(a.prefix_splits, (prefix_len(a, group) + a.prefix_span - 1) / a.prefix_span));
 }
 
 // A wave begins its running softmax of a row with the prefix's splits first, first + step, ... < live: they are as good as
@@ -409,19 +431,26 @@ __global__ __launch_bounds__(256, D == 256 ? 2 : D == 128 ? 3 : 4) void kv4_atte
     const View view{a.causal, int(a.window)};
     const int last = min(t.r0 + 15, t.rows - 1);
     const int p_first = t.position(t.r0 / share), p_last = t.position(last / share);
-    const int begin = view.lo(p_first) / 32 * 32, end = view.hi(p_last, t.kv);
+    // kBoth: tokens [0, len) are the prefix's, those from `own` on the request's
+    const int group = PART == kBoth ? group_of(a, t.b) : -1, len = group < 0 ? 0 : prefix_len(a, group), own = (len + 31) / 32 * 32;
+    const int begin = view.lo(p_first) / 32 * 32, end = own + view.hi(p_last, t.kv);
     const int live = max(1, min(splits, (end - begin + span - 1) / span));  // splits with tokens
     if (int(blockIdx.z) >= live) return;
     const int s0 = begin + int(blockIdx.z) * span, s1 = min(end, s0 + span);
     // every row of the tile sees [all_lo, all_hi)
-    const int all_lo = view.lo(p_last), all_hi = min(view.hi(p_first, t.kv), s1);
+    const int all_lo = view.lo(p_last), all_hi = min(own + view.hi(p_first, t.kv), s1);
 
     const int64_t region = kv4_region(a.page, D);
     const uint8_t* pool = a.pool + kh * region;
     const int32_t* row = a.table + int64_t(t.b) * a.ldt;
     const int first = s0 + 32 * wave, steps = max(0, (s1 - first + 32 * WAVES - 1) / (32 * WAVES));
     Chunks ch;
-    ch.find(a, magic, row, region, NB * 8 * W, first / 16, 2 * WAVES, s1, lane);
+    auto find = [&](int chunk) {
+        if constexpr (PART == kBoth)
+            ch.find_both(a, magic, a.prefix_table + (group < 0 ? 0 : group) * a.ldp, len, own, row, region, NB * 8 * W, chunk, 2 * WAVES, s1, lane);
+        else ch.find(a, magic, row, region, NB * 8 * W, chunk, 2 * WAVES, s1, lane);
+    };
+    find(first / 16);
     Side<D> k, v;
     if (steps > 0) {
         k.load(pool, pool, ch, 0, a.page, lane);
@@ -432,7 +461,7 @@ __global__ __launch_bounds__(256, D == 256 ? 2 : D == 128 ? 3 : 4) void kv4_atte
     const int r = min(t.r0 + col, last);
     const int qi = r / share, hd = kh * share + r % share;
     const int pos = t.position(qi);
-    const int lo = view.lo(pos), hi = min(view.hi(pos, t.kv), s1);
+    const int lo = view.lo(pos), hi = min(own + view.hi(pos, t.kv), s1);
     uint4 q[NB][W / 32];
     float offset[NB];
     const float zf = load_queries<ACT, D>(a.q + (t.q0 + qi) * a.ldq + int64_t(hd) * D + 8 * kq, a.scale, q, offset);
@@ -473,8 +502,7 @@ __global__ __launch_bounds__(256, D == 256 ? 2 : D == 128 ? 3 : 4) void kv4_atte
         }
         const bool more = step + 1 < steps;
         if (more) {
-            if ((step + 1) % 32 == 0)
-                ch.find(a, magic, row, region, NB * 8 * W, (tok + 32 * WAVES) / 16, 2 * WAVES, s1, lane);
+            if ((step + 1) % 32 == 0) find((tok + 32 * WAVES) / 16);
             k.load(pool, pool, ch, (step + 1) % 32, a.page, lane);
         }
         float vs[2][NB][4];
@@ -484,13 +512,13 @@ __global__ __launch_bounds__(256, D == 256 ? 2 : D == 128 ? 3 : 4) void kv4_atte
             for (int b = 0; b < NB; ++b) {
                 vs[c][b][0] = v.s[c][b].x; vs[c][b][1] = v.s[c][b].y; vs[c][b][2] = v.s[c][b].z; vs[c][b][3] = v.s[c][b].w;
             }
-        if (!(tok >= all_lo && tok + 32 <= all_hi && there == 3)) {
+        if (!(tok >= all_lo && tok + 32 <= all_hi && there == 3) || (PART == kBoth && tok < own && tok + 32 > len)) {
 #pragma unroll
             for (int c = 0; c < 2; ++c)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int at = tok + 16 * c + 4 * kq + i;
-                    const bool seen = (there >> c & 1) && at >= lo && at < hi;
+                    const bool seen = (there >> c & 1) && at >= lo && at < hi && (PART != kBoth || at < len || at >= own);
                     z[c][i] = seen ? z[c][i] : -INFINITY;
 #pragma unroll
                     for (int b = 0; b < NB; ++b) vs[c][b][i] = seen ? vs[c][b][i] : 0.0f;
@@ -996,13 +1024,15 @@ hipError_t run(const Kv4AttentionArgs& a, const Kv4Plan& p, float* partials, hip
     const uint32_t magic = per == 1 ? 0 : uint32_t(((uint64_t(1) << 32) + per - 1) / per);
     unsigned* counters = static_cast<unsigned*>(a.workspace);
     if (p.splits < 2) partials = nullptr;
-    if (p.rows > 16) {
-        const dim3 grid(unsigned(p.tiles * a.kv_heads), unsigned(p.splits));
-        const size_t lds = 2 * sizeof(Stage<D>);
-        const hipError_t e = allow_lds(reinterpret_cast<const void*>(&kv4_rows_kernel<ACT, D, PART>), lds);
-        if (e != hipSuccess) return e;
-        kv4_rows_kernel<ACT, D, PART><<<grid, dim3(256), lds, stream>>>(a, p.tiles, int(p.span), p.splits, magic, counters, partials);
-        return hipGetLastError();
+    if constexpr (PART != kBoth) {  // (tiles of 16 rows only)
+        if (p.rows > 16) {
+            const dim3 grid(unsigned(p.tiles * a.kv_heads), unsigned(p.splits));
+            const size_t lds = 2 * sizeof(Stage<D>);
+            const hipError_t e = allow_lds(reinterpret_cast<const void*>(&kv4_rows_kernel<ACT, D, PART>), lds);
+            if (e != hipSuccess) return e;
+            kv4_rows_kernel<ACT, D, PART><<<grid, dim3(256), lds, stream>>>(a, p.tiles, int(p.span), p.splits, magic, counters, partials);
+            return hipGetLastError();
+        }
     }
     const dim3 grid(unsigned(p.tiles), unsigned(a.kv_heads), unsigned(p.splits));
     kv4_attention_kernel<ACT, D, PART><<<grid, dim3(256), 0, stream>>>(a, int(p.span), p.splits, magic, counters, partials);
@@ -1121,25 +1151,41 @@ Kv4PrefixPlan plan_kv4_prefix(int64_t tokens, int64_t batch, int64_t groups, int
         cut(p.own, capacity, 12);
         p.own.workspace = p.own.splits > 1 ? size_t(p.own.tiles * kv_heads) * size_t(p.own.splits) * size_t(p.own.rows / 16) * size_t(16 * dim + 32) * 4 : 0;
     }
+    // One launch for both where sharing saves little: every request's tiles (of 16 rows) then walk the prefix too.  us
+    // together against apart, with the tile-tokens that sharing saves in thousands, requests x heads / key heads on tokens:
+    //   D = 64   8 x 8/1 on 1000 (3) 8.3 and 11.3, 32 x 32/8 on 1000 (184) 12.7 and 13.3, 64 x 32/8 on 1000 (376) 16.5 and 15.6,
+    //            8 x 16/16 on 1000 (112) 10.4 and 11.1, on 4000 (448) 18.8 and 13.0
+    //   D = 128  4 x 32/8 on 1000 (48) 11.2 and 15.5, 150 x 16/2 on 1000 (148) 18.3 and 20.7, 4 x 8/8 on 8000 (192) 18.6 and
+    //            17.3, 32 x 8/8 on 1000 (232) 15.5 and 13.9, but 64 x 32/8 on 1000 (376) 20.7 and 23.2
+    //   D = 256  2 x 8/1 on 800 (0) 11.2 and 18.5, 64 x 8/1 on 8000 (248) 31 and 37, 64 x 4/4 on 2000 (472) 32 and 23
+    const int64_t tiles = ragged ? tokens * share / 16 + batch : batch * ceil_div(share, int64_t(16)), shared = tokens * share / 16 + groups;
+    if (tokens * heads * prefix_capacity < int64_t(24) << 20 && (tiles - shared) * kv_heads * prefix_capacity <= 200000) {
+        p.together = true;
+        p.own = Kv4Plan{};
+        p.own.rows = 16;
+        p.own.tiles = tiles;
+        cut(p.own, prefix_capacity + 32 + capacity, 12);
+        if (p.own.splits > 1) p.workspace = size_t(tiles * kv_heads) * size_t(p.own.splits) * size_t(16 * dim + 32) * 4;
+        return p;
+    }
     p.parts = size_t(p.prefix.splits) * size_t(tokens) * size_t(heads) * size_t(dim + 2) * 4;
     p.parts = (p.parts + 15) / 16 * 16;
     p.workspace = p.parts + p.own.workspace;
     return p;
 }
 
-hipError_t launch_kv4_prefix(const Kv4PrefixArgs& a, int act, hipStream_t stream) {
-    Kv4AttentionArgs o = a.own;
-    const Kv4PrefixPlan p = plan_kv4_prefix(o.tokens, o.batch, o.groups, o.heads, o.kv_heads, o.dim, a.table_width * o.page,
+hipError_t launch_kv4_prefix(const Kv4AttentionArgs& a, int act, hipStream_t stream) {
+    Kv4AttentionArgs o = a;
+    const Kv4PrefixPlan p = plan_kv4_prefix(o.tokens, o.batch, o.groups, o.heads, o.kv_heads, o.dim, o.prefix_width * o.page,
                                             o.table_width * o.page, o.cu_q != nullptr, o.causal != 0);
-    o.prefix_lens = a.lens;
-    o.prefix_room = a.table_width * o.page;
+    if (p.together) return run_by_type<kBoth>(o, p.own, after_header(o.workspace, 0), act, stream);
     o.prefix_span = int(p.prefix.span);
     o.prefix_splits = p.prefix.splits;
     Kv4AttentionArgs f = o;
-    f.table = a.table;
-    f.table_width = a.table_width;
-    f.ldt = a.ldt;
-    f.kv_lens = a.lens;
+    f.table = a.prefix_table;
+    f.table_width = a.prefix_width;
+    f.ldt = a.ldp;
+    f.kv_lens = a.prefix_lens;
     f.causal = 0;
     const hipError_t e = run_by_type<kPrefix>(f, p.prefix, nullptr, act, stream);
     return e == hipSuccess ? run_by_type<kOwn>(o, p.own, after_header(o.workspace, p.parts), act, stream) : e;

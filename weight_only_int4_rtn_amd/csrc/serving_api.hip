@@ -228,8 +228,19 @@ size_t kv4_prefix_attention_workspace_bytes(int64_t tokens, int64_t batch, int64
     if (!valid_attention(tokens, batch, heads, kv_heads, head_dim, table_width, page_size, ragged != 0, 0) ||
         !valid_prefix(groups, prefix_width, page_size) || tokens == 0)
         return 0;
-    return kSyncBytes + plan_kv4_prefix(tokens, batch, groups, int(heads), int(kv_heads), int(head_dim), prefix_width * page_size,
-                                        table_width * page_size, ragged != 0, causal != 0).workspace;
+    const size_t w = plan_kv4_prefix(tokens, batch, groups, int(heads), int(kv_heads), int(head_dim), prefix_width * page_size,
+                                     table_width * page_size, ragged != 0, causal != 0).workspace;
+    return w ? kSyncBytes + w : 0;
+}
+
+int kv4_prefix_attention_tile_rows(int64_t tokens, int64_t batch, int64_t groups, int64_t heads, int64_t kv_heads, int64_t head_dim,
+                                   int64_t prefix_width, int64_t table_width, int64_t page_size, int ragged, int causal) {
+    if (!valid_attention(tokens, batch, heads, kv_heads, head_dim, table_width, page_size, ragged != 0, 0) ||
+        !valid_prefix(groups, prefix_width, page_size) || tokens == 0)
+        return 0;
+    const Kv4PrefixPlan p = plan_kv4_prefix(tokens, batch, groups, int(heads), int(kv_heads), int(head_dim), prefix_width * page_size,
+                                            table_width * page_size, ragged != 0, causal != 0);
+    return p.together ? 0 : p.prefix.rows;
 }
 
 w4a16_status_t kv4_prefix_attention(const void* q, w4a16_dtype_t dtype, int64_t tokens, int64_t ldq, int64_t heads, int64_t kv_heads,
@@ -254,8 +265,8 @@ w4a16_status_t kv4_prefix_attention(const void* q, w4a16_dtype_t dtype, int64_t 
     const size_t ob = span_bytes(tokens, width, ldo, 2);
     const size_t need = kv4_prefix_attention_workspace_bytes(tokens, batch, groups, heads, kv_heads, head_dim, prefix_width, table_width,
                                                              page_size, cu_q != nullptr, causal);
-    if (!workspace || workspace_bytes < need) return W4A16_EWORKSPACE;
-    if (!aligned(workspace, 16)) return W4A16_EINVAL;
+    if (need > 0 && (!workspace || workspace_bytes < need)) return W4A16_EWORKSPACE;
+    if (need > 0 && !aligned(workspace, 16)) return W4A16_EINVAL;
     const struct { const void* p; size_t n; } in[] = {
         {q, span_bytes(tokens, width, ldq, 2)}, {pool, kv4_pool_bytes(pages, page_size, kv_heads, head_dim)},
         {prefix_table, span_bytes(groups, prefix_width, ldp, 4)}, {prefix_lens, size_t(groups) * 4},
@@ -264,8 +275,7 @@ w4a16_status_t kv4_prefix_attention(const void* q, w4a16_dtype_t dtype, int64_t 
     for (const auto& i : in)
         if (overlap(out, ob, i.p, i.n) || overlap(workspace, need, i.p, i.n)) return W4A16_EINVAL;
     if (overlap(workspace, need, out, ob)) return W4A16_EINVAL;
-    Kv4PrefixArgs p{};
-    Kv4AttentionArgs& a = p.own;
+    Kv4AttentionArgs a{};
     a.q = static_cast<const uint16_t*>(q);
     a.ldq = ldq;
     a.tokens = tokens;
@@ -288,12 +298,12 @@ w4a16_status_t kv4_prefix_attention(const void* q, w4a16_dtype_t dtype, int64_t 
     a.workspace = workspace;
     a.cu_groups = cu_groups;
     a.groups = groups;
-    a.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kSyncBytes);
-    p.table = prefix_table;
-    p.table_width = prefix_width;
-    p.ldt = ldp;
-    p.lens = prefix_lens;
-    return from_hip(launch_kv4_prefix(p, act_of(dtype), static_cast<hipStream_t>(stream)));
+    a.parts = reinterpret_cast<float*>(reinterpret_cast<uintptr_t>(workspace) + kSyncBytes);
+    a.prefix_table = prefix_table;
+    a.prefix_width = prefix_width;
+    a.ldp = ldp;
+    a.prefix_lens = prefix_lens;
+    return from_hip(launch_kv4_prefix(a, act_of(dtype), static_cast<hipStream_t>(stream)));
 }
 
 size_t lora_add_workspace_bytes(int64_t m, int64_t n, int64_t k, int64_t adapters, int64_t rank) {
