@@ -81,7 +81,8 @@ struct Fp8QuantizeArgs {
     const void* x;
     int64_t m, k, ldx;  // ldx: elements between rows
     uint8_t* codes;     // [m][k]
-    float* scales;      // [m][k / 128]
+    float* scales;      // [m][k / 128], or by group [k / 128][m]
+    bool by_group;      // (16-bit x)
 };
 // dtype of x: 0 (FP32, without an activation), kActBf16, kActF16; act_fn: ActFn,
 // SwiGLU rows hold [up | gate], 2k values
@@ -91,7 +92,8 @@ hipError_t launch_fp8_quantize_blocks(const Fp8QuantizeArgs& a, int dtype, hipSt
 
 struct Fp8LinearArgs {
     const uint8_t* x;   // codes, or (few rows) 16-bit values that the kernel quantizes itself
-    const float* xs;
+    const float* xs;    // of row i, group g at i * rs + g * gs
+    int64_t rs, gs;
     int64_t m, k, ldx;  // ldx: elements
     const uint8_t* w;
     const float* ws;
@@ -105,7 +107,7 @@ struct Fp8LinearArgs {
 
 struct Fp8Plan {
     int kind;           // 0: the kernel for at most 16 rows; else an index of the tiled kernel's shapes
-    int bm, bn, waves;  // rows of x and output columns of a workgroup
+    int bm, bn;         // rows of x and output columns of a workgroup
     int64_t mtiles, ntiles;
     int splits, gps;    // parts of K, groups of 128 in each
     size_t workspace;   // FP32 tiles of a K split

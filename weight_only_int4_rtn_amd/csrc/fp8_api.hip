@@ -66,7 +66,7 @@ w4a16_status_t quantize(const void* x, w4a16_dtype_t dtype, w4a16_act_t act, boo
     const size_t xb = span_bytes(m, width, ldx, elem), cb = size_t(m) * size_t(k),
                  sb = size_t(blocks ? ceil_div(m, int64_t(128)) : m) * size_t(k / kGroup) * 4;
     if (overlap(codes, cb, x, xb) || overlap(scales, sb, x, xb) || overlap(codes, cb, scales, sb)) return W4A16_EINVAL;
-    const Fp8QuantizeArgs a{x, m, k, ldx, static_cast<uint8_t*>(codes), scales};
+    const Fp8QuantizeArgs a{x, m, k, ldx, static_cast<uint8_t*>(codes), scales, false};
     hipStream_t s = static_cast<hipStream_t>(stream);
     return from_hip(blocks ? launch_fp8_quantize_blocks(a, kernel_dtype(dtype), s) : launch_fp8_quantize(a, kernel_dtype(dtype), int(act), s));
 }
@@ -128,9 +128,14 @@ w4a16_status_t fp8_linear(const void* x, w4a16_dtype_t x_dtype, const float* x_s
     if (codes || inside) {
         a.x = static_cast<const uint8_t*>(x);
         a.xs = x_scales;
+        a.rs = groups;
+        a.gs = 1;
         a.ldx = ldx;
     } else {
-        const Fp8QuantizeArgs q{x, m, k, ldx, at, reinterpret_cast<float*>(at + codes_bytes(m, k))};
+        // group by group: a step's scales are then one run of memory (4096 x 4096 x 16384: 222 us, row by row 242)
+        a.rs = 1;
+        a.gs = m;
+        const Fp8QuantizeArgs q{x, m, k, ldx, at, reinterpret_cast<float*>(at + codes_bytes(m, k)), true};
         const hipError_t e = launch_fp8_quantize(q, kernel_dtype(x_dtype), int(act), s);
         if (e != hipSuccess) return W4A16_EHIP;
         a.x = q.codes;

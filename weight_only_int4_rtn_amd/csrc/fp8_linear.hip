@@ -72,20 +72,14 @@ __device__ inline void store_part(const Fp8LinearArgs& a, int split, int64_t npa
     for (int i = 0; i < N; i += 4) *reinterpret_cast<float4*>(to + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
 }
 
-// A K split's end: every split stores its FP32 sums past the L2 (SC1: the XCDs'
-// L2s are not coherent) and counts itself; the one that completes the count
-// gets true and all the sums, added in split order, and clears the counter for
-// the next call.  Nobody waits.  slot: this tile's slots, T * threads
-// vectors each; flag: an int of LDS that nobody uses any more.
-template <int T>
-__device__ inline bool join_splits(float (&acc)[T][4], float* slot, unsigned* counter, int split, int splits, int* flag) {
-    const int threads = blockDim.x, bytes = T * threads * 16;
+// The end of a K split of few rows: every part stores its FP32 sums past the L2 (SC1: the XCDs' L2s are not coherent) and
+// counts itself; the one that completes the count gets true and all the sums, added in the order of the parts, and clears
+// the counter for the next call.  Nobody waits.  slot: this tile's, a vector a thread and part; flag: an int of LDS that
+// nobody uses any more.
+__device__ inline bool join_parts(float (&acc)[4], float* slot, unsigned* counter, int split, int splits, int* flag) {
+    const int bytes = int(blockDim.x) * 16, at = int(threadIdx.x) * 16;
     const __amdgpu_buffer_rsrc_t sl = buffer_rsrc(slot, int64_t(splits) * bytes);
-    const int at = int(threadIdx.x) * 16;
-#pragma unroll
-    for (int t = 0; t < T; ++t)
-        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, f32x4_t{acc[t][0], acc[t][1], acc[t][2], acc[t][3]}), sl,
-                                               split * bytes + t * threads * 16 + at, 0, kCoherent);
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, f32x4_t{acc[0], acc[1], acc[2], acc[3]}), sl, split * bytes + at, 0, kCoherent);
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
     if (threadIdx.x == 0) {
@@ -96,27 +90,15 @@ __device__ inline bool join_splits(float (&acc)[T][4], float* slot, unsigned* co
     __syncthreads();
     if (!*flag) return false;
 #pragma unroll
-    for (int t = 0; t < T; ++t)
+    for (int e = 0; e < 4; ++e) acc[e] = 0.0f;
+    for (int s = 0; s < splits; s += 8) {  // eight loads in flight
+        u32x4 part[8];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[t][e] = 0.0f;
-    // eight vectors a lane in flight: of one split, or of several at a time where a split has fewer
-    constexpr int V = T < 8 ? T : 8, N = 8 / V;
-    for (int s = 0; s < splits; s += N) {
+        for (int i = 0; i < 8; ++i) part[i] = __builtin_amdgcn_raw_buffer_load_b128(sl, min(s + i, splits - 1) * bytes + at, 0, kCoherent);
 #pragma unroll
-        for (int t0 = 0; t0 < T; t0 += V) {
-            u32x4 part[N][V];
+        for (int i = 0; i < 8; ++i)
 #pragma unroll
-            for (int i = 0; i < N; ++i)
-#pragma unroll
-                for (int t = 0; t < V; ++t)
-                    part[i][t] = __builtin_amdgcn_raw_buffer_load_b128(sl, min(s + i, splits - 1) * bytes + (t0 + t) * threads * 16 + at, 0, kCoherent);
-#pragma unroll
-            for (int i = 0; i < N; ++i)
-#pragma unroll
-                for (int t = 0; t < V; ++t)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[t0 + t][e] += s + i < splits ? __uint_as_float(part[i][t][e]) : 0.0f;
-        }
+            for (int e = 0; e < 4; ++e) acc[e] += s + i < splits ? __uint_as_float(part[i][e]) : 0.0f;
     }
     return true;
 }
@@ -125,13 +107,20 @@ __device__ inline bool join_splits(float (&acc)[T][4], float* slot, unsigned* co
 // At most 16 rows of x.  A workgroup takes 16 rows of W and a part of K, its
 // waves the part's groups in turn, each straight from memory to the matrix
 // operands (rows of x from the caches); the waves' sums meet in LDS.
+//
+// Bound by the read of W: 1 row x 8192 x 28672 (235 MB) 45.2 us, 5.2 TB/s; 1 x
+// 2048 x 32768 12.4 us, 5.4 TB/s.  Smaller layers cost a launch and memory's
+// latency: 1 x 4096 x 4096 7.6 us, 2.2 TB/s.  Eight waves or eight steps ahead
+// gave nothing, nontemporal loads of W cost 5 %.
 // ---------------------------------------------------------------------------
 constexpr int kFewWaves = 4, kFewAhead = 4;
-// Groups of x that a workgroup may have to quantize itself (rows times groups of its part).  us a call with the quantizer
-// inside and apart, rows x K x N: 1 x 2048 x 2560 (16 groups) 4.7 and 7.7, 1 x 2048 x 32768 14.4 and 17.7, 2 x 4096 x 4096
-// (64) 9.1 and 10.6, 1 x 16384 x 2048 (64) 14.9 and 16.0, 4 x 2048 x 32768 (64) 19.9 and 21.4; with 96 and 128 groups, 3 x
-// 4096 x 4096 11.4 and 10.7, 2 x 16384 x 2048 19.4 and 16.4.
+// Whether the workgroups quantize x for themselves, each the groups that its part of K has (rows times groups), 16 or more
+// at a time: a launch less, but the work is done once a workgroup.  So at most kFewGroups in one and kFewInAll in all of
+// them.  us with the quantizer inside and apart, rows x K x N: 1 x 2048 x 2560 4.8 and 7.7, 1 x 2048 x 32768 14.0 and 17.7, 2 x 4096
+// x 4096 (64 groups in one) 9.7 and 10.6, 1 x 16384 x 2048 14.3 and 16.0; 3 x 4096 x 4096 (96) 11.4 and 9.7; 4 x 2048 x 32768
+// (131072 in all) 19.1 and 16.9, 8 x 1024 x 65536 28.2 and 20.6, 1 x 512 x 131072 23.0 and 17.7.
 constexpr int kFewGroups = 64;
+constexpr int64_t kFewInAll = 32768;
 
 // QUANTIZE: x holds 16-bit values (of the output's type), which every workgroup quantizes for itself, activated by AF, while
 // its first rows of W are on their way.
@@ -152,7 +141,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void fp8_few_kernel(Fp8LinearArgs a
     const int row = min<int>(r, int(a.m) - 1);
     const uint8_t* wp = a.w + min(n0 + r, a.n - 1) * a.k + int64_t(g0 + wave) * kGroup + 16 * kq;
     const uint8_t* xp = a.x + row * a.ldx + int64_t(g0 + wave) * kGroup + 16 * kq;
-    const float* xsp = a.xs + row * groups + g0 + wave;
+    const float* xsp = a.xs + row * a.rs + (g0 + wave) * a.gs;
     const float* wsp = a.ws + n0 / 128 * groups + g0 + wave;
 
     struct Chunk {
@@ -166,7 +155,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void fp8_few_kernel(Fp8LinearArgs a
             c.w[h] = *reinterpret_cast<const u32x4*>(wp + at + 64 * h);
             if constexpr (!QUANTIZE) c.x[h] = *reinterpret_cast<const u32x4*>(xp + at + 64 * h);
         }
-        if constexpr (!QUANTIZE) c.xs = xsp[i * kFewWaves];
+        if constexpr (!QUANTIZE) c.xs = xsp[i * kFewWaves * a.gs];
         c.ws = wsp[i * kFewWaves];
     };
     f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
@@ -218,14 +207,14 @@ __global__ __launch_bounds__(64 * kFewWaves) void fp8_few_kernel(Fp8LinearArgs a
     sums[wave][lane] = acc;
     __syncthreads();
     // every wave adds all four, so that a split's join has the whole workgroup's loads; the first stores
-    float tot[1][4] = {};
+    float tot[4] = {};
 #pragma unroll
     for (int w = 0; w < kFewWaves; ++w)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) tot[0][e] += sums[w][lane][e];
-    if (splits > 1 && !join_splits<1>(tot, a.slots + tile * splits * (kFewWaves * 64 * 4), a.counters + tile, split, splits, &flag)) return;
+        for (int e = 0; e < 4; ++e) tot[e] += sums[w][lane][e];
+    if (splits > 1 && !join_parts(tot, a.slots + tile * splits * (kFewWaves * 64 * 4), a.counters + tile, split, splits, &flag)) return;
     if (wave != 0 || r >= a.m) return;
-    store_row<ACT, 4>(a, r, n0 + 4 * kq, tot[0]);
+    store_row<ACT, 4>(a, r, n0 + 4 * kq, tot);
 }
 
 // Row r of 128 bytes holds them as 8 pieces of 16, piece c at c ^ (r / 2 % 8): the 16 rows that an operand's read touches
@@ -241,15 +230,25 @@ __device__ inline int fp8_swizzle(int row, int piece) { return row * 128 + ((pie
 // A wave's CB tiles of W interleave their rows: tile j's row 4 a + i is
 // column 4 CB a + 4 j + i of the wave's block, so a lane's results of all tiles
 // are 4 CB consecutive columns of one row and leave in 16-byte stores.
+//
+// 256 x 256, 4096 x 16384 x 4096: 222 us, 2.48 PFLOP/s; 4096 x 2048 x 32768, with 268
+// MB of results, 270 us, 2.04.  A step takes 1.72 us, of which its matrix
+// instructions 1.5 (2.84 PFLOP/s with the loads left out; on random values the
+// clock falls to 1.7 GHz); the rest is the path from L2 to LDS, whose return
+// side is 75 % busy (9 TB/s).  W straight to registers, 16 rows x 64 bytes an
+// instruction, made the latter 410 us; loading into the L2 ahead, a shared slice
+// of x kept in LDS and workgroups that go on to a second tile gave 0 to 5 %.
+// Few rows are bound by memory's latency: a step of 32 x 128 or 64 x 128 takes 0.48
+// us whatever it computes, hence the K splits.
 // ---------------------------------------------------------------------------
 template <int RB_, int CB_, int WM_, int WN_, int R_>
 struct Fp8Shape {
     static constexpr int RB = RB_, CB = CB_, WM = WM_, WN = WN_, R = R_, WAVES = WM * WN;
     static constexpr int BM = 16 * RB * WM, BN = 16 * CB * WN;
     static constexpr int XP = BM / 8 / WAVES, WP = BN / 8 / WAVES;  // 1 KB pieces of x and W a wave loads a step
-    static constexpr int LOADS = XP + WP + 1;                       // and one of scales
+    static constexpr int LOADS = XP + WP + 1;                       // and one of its share of the rows' scales
     static constexpr int PER = (LOADS + RB * CB - 1) / (RB * CB);   // loads beside a matrix instruction
-    static_assert(XP * WAVES * 8 == BM && WP * WAVES * 8 == BN && BM <= 64 * WAVES, "every wave loads its share");
+    static_assert(XP * WAVES * 8 == BM && WP * WAVES * 8 == BN && BM / WAVES <= 64, "every wave loads its share");
     static_assert(CB == 2 || CB == 4, "rows of W in LDS");
 };
 
@@ -258,7 +257,8 @@ template <int CB>
 __device__ inline int fp8_w_turn(int row) { return ((row >> 1) & 1) | ((row / (4 * CB) & 3) << 1); }
 
 // Tile of a workgroup: an XCD (workgroups go to the 8 of them in turn) takes a run of tiles, the run goes through bands of
-// four rows of tiles, so the tiles that an XCD computes at a time share rows of x and of W in its L2.
+// four rows of tiles, so the tiles that an XCD computes at a time share rows of x and of W in its L2 (88 % of the reads hit
+// it at 4096 x 16384 x 4096; without the bands 1.5 % slower).
 __device__ inline void fp8_tile_of(int64_t id, int64_t mtiles, int64_t ntiles, int64_t& mt, int64_t& nt) {
     const int64_t total = mtiles * ntiles, xcd = id % 8, at = xcd * (total / 8) + min(xcd, total % 8) + id / 8;
     const int64_t band = at / (4 * ntiles), in = at % (4 * ntiles), high = min<int64_t>(4, mtiles - 4 * band);
@@ -270,14 +270,11 @@ template <int ACT, typename S>
 __global__ __launch_bounds__(64 * S::WAVES, S::WAVES / 4) void fp8_tile_kernel(Fp8LinearArgs a, int64_t mtiles, int64_t ntiles, int splits, int gps) {
     constexpr int RB = S::RB, CB = S::CB, XP = S::XP, WP = S::WP, R = S::R;
     constexpr int kMaxPieces = 4, kMaxCB = 4;  // (a captured array whose bound depends on the template would drop the launch stub)
-    static_assert(XP <= kMaxPieces && WP <= kMaxPieces && CB <= kMaxCB && R >= 2 && R <= 6, "array maxima");
+    static_assert(XP <= kMaxPieces && WP <= kMaxPieces && CB <= kMaxCB && R >= 2 && R <= 4, "array maxima");
     // buffers with names of their own: the compiler then tells direct loads into one from reads of another
-    __shared__ __align__(16) uint8_t X0[S::BM * 128], X1[S::BM * 128], X2[R > 2 ? S::BM * 128 : 16], X3[R > 3 ? S::BM * 128 : 16],
-        X4[R > 4 ? S::BM * 128 : 16], X5[R > 5 ? S::BM * 128 : 16];
-    __shared__ __align__(16) uint8_t W0[S::BN * 128], W1[S::BN * 128], W2[R > 2 ? S::BN * 128 : 16], W3[R > 3 ? S::BN * 128 : 16],
-        W4[R > 4 ? S::BN * 128 : 16], W5[R > 5 ? S::BN * 128 : 16];
-    __shared__ float S0[S::WAVES * 64], S1[S::WAVES * 64], S2[R > 2 ? S::WAVES * 64 : 16], S3[R > 3 ? S::WAVES * 64 : 16], S4[R > 4 ? S::WAVES * 64 : 16],
-        S5[R > 5 ? S::WAVES * 64 : 16];
+    __shared__ __align__(16) uint8_t X0[S::BM * 128], X1[S::BM * 128], X2[R > 2 ? S::BM * 128 : 16], X3[R > 3 ? S::BM * 128 : 16];
+    __shared__ __align__(16) uint8_t W0[S::BN * 128], W1[S::BN * 128], W2[R > 2 ? S::BN * 128 : 16], W3[R > 3 ? S::BN * 128 : 16];
+    __shared__ float S0[S::BM], S1[S::BM], S2[R > 2 ? S::BM : 16], S3[R > 3 ? S::BM : 16];
     const int lane = threadIdx.x % 64, wave = uniform(threadIdx.x / 64);
     const int r = lane % 16, kq = lane / 16;
     const int wm = wave / S::WN, wn = wave % S::WN;
@@ -289,10 +286,9 @@ __global__ __launch_bounds__(64 * S::WAVES, S::WAVES / 4) void fp8_tile_kernel(F
     const int64_t groups = a.k / kGroup;
     const int g0 = split * gps, ng = int(min<int64_t>(gps, groups - g0));
 
-    // rows of x past M and of W past N read as zeros (the offset that is checked is the lane's, its row's start included)
+    // rows of x past M and of W past N lie behind their resource's end: they read as zeros
     const int64_t rows = min<int64_t>(S::BM, a.m - m0), cols = min<int64_t>(S::BN, a.n - nb);
     const __amdgpu_buffer_rsrc_t xr = buffer_rsrc(a.x + m0 * a.ldx, (rows - 1) * a.ldx + a.k);
-    const __amdgpu_buffer_rsrc_t sr = buffer_rsrc(a.xs + m0 * groups, rows * groups * 4);
     const __amdgpu_buffer_rsrc_t wr = buffer_rsrc(a.w + nb * a.k, cols * a.k);
     uint32_t xo[kMaxPieces], wo[kMaxPieces];
 #pragma unroll
@@ -305,15 +301,19 @@ __global__ __launch_bounds__(64 * S::WAVES, S::WAVES / 4) void fp8_tile_kernel(F
         const int row = 8 * (WP * wave + p) + lane / 8;
         wo[p] = uint32_t(row * a.k + (((lane & 7) ^ fp8_w_turn<CB>(row)) << 4));
     }
-    const uint32_t so = uint32_t((64 * wave + lane) % S::BM * groups * 4);
+    // scales of rows past M are the last row's: their products are zeros, and dropped
+    constexpr int SR = S::BM / S::WAVES;
+    const int64_t srow = min<int64_t>(SR * wave + lane % SR, rows - 1);
+    const __amdgpu_buffer_rsrc_t sr = buffer_rsrc(a.xs + m0 * a.rs, ((rows - 1) * a.rs + (groups - 1) * a.gs + 1) * 4);
+    const uint32_t so = uint32_t(srow * a.rs * 4), sg = uint32_t(a.gs * 4);
     const float* wsp = a.ws + min(n0, a.n - 1) / 128 * groups;
 
     // load q of step s (steps past the end load the last one again, into buffers that nobody reads)
     auto load = [&](uint8_t* X, uint8_t* W, float* sc, int s, int q) {
         const int g = g0 + min(s, ng - 1);
-        if (q == 0)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(sr, (lds_ptr_t)(sc + 64 * wave), 4, so, uniform(g * 4), 0, 0);
-        else if (q <= XP)
+        if (q == 0) {
+            if (lane < SR) __builtin_amdgcn_raw_ptr_buffer_load_lds(sr, (lds_ptr_t)(sc + SR * wave), 4, so, uniform(g * sg), 0, 0);
+        } else if (q <= XP)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(xr, (lds_ptr_t)(X + (XP * wave + q - 1) * 1024), 16, xo[q - 1], uniform(g * kGroup), 0, 0);
         else
             __builtin_amdgcn_raw_ptr_buffer_load_lds(wr, (lds_ptr_t)(W + (WP * wave + q - 1 - XP) * 1024), 16, wo[q - 1 - XP], uniform(g * kGroup), 0, 0);
@@ -378,17 +378,13 @@ __global__ __launch_bounds__(64 * S::WAVES, S::WAVES / 4) void fp8_tile_kernel(F
     whole(X0, W0, S0, 0);
     if constexpr (R > 2) whole(X1, W1, S1, 1);
     if constexpr (R > 3) whole(X2, W2, S2, 2);
-    if constexpr (R > 4) whole(X3, W3, S3, 3);
-    if constexpr (R > 5) whole(X4, W4, S4, 4);
     // Buffer b of R: read by step s with s % R == b, filled again from step s + 1 on
 #define FP8_STEP(b, before)                                                                                  \
     if constexpr (b < R) {                                                                                   \
         if constexpr (b > 0) step(X##b, W##b, S##b, X##before, W##before, S##before, s);                      \
         else if constexpr (R == 2) step(X0, W0, S0, X1, W1, S1, s);                                          \
         else if constexpr (R == 3) step(X0, W0, S0, X2, W2, S2, s);                                          \
-        else if constexpr (R == 4) step(X0, W0, S0, X3, W3, S3, s);                                          \
-        else if constexpr (R == 5) step(X0, W0, S0, X4, W4, S4, s);                                          \
-        else step(X0, W0, S0, X5, W5, S5, s);                                                                \
+        else step(X0, W0, S0, X3, W3, S3, s);                                                                \
         if (++s >= ng) break;                                                                                \
     }
     for (int s = 0;;) {
@@ -396,7 +392,7 @@ __global__ __launch_bounds__(64 * S::WAVES, S::WAVES / 4) void fp8_tile_kernel(F
         FP8_STEP(1, 0)
         FP8_STEP(2, 1)
         FP8_STEP(3, 2)
-            }
+    }
 #undef FP8_STEP
     // (scalars from here on: as vectors of four, which the compiler would make of them at each of the loop's exits, every
     // step's sums got registers of their own)
@@ -422,7 +418,8 @@ __global__ __launch_bounds__(64 * S::WAVES, S::WAVES / 4) void fp8_tile_kernel(F
 
 // ---------------------------------------------------------------------------
 // The end of a K split: the parts of four outputs of a row added in the order of the parts, four at a time in flight, then
-// the bias and the one rounding.  A row a workgroup row of the grid: no division.
+// the bias and the one rounding.  A row a workgroup row of the grid: no division.  Bound by its launch and one latency: 8
+// parts of 64 x 2048 3.8 us.
 // ---------------------------------------------------------------------------
 template <int ACT>
 __global__ __launch_bounds__(256) void fp8_join_kernel(Fp8LinearArgs a, int splits, int64_t npad) {
@@ -455,12 +452,12 @@ using Wide = Fp8Shape<4, 4, 2, 4, 3>;    // 128 x 256
 using Large = Fp8Shape<8, 4, 2, 4, 2>;   // 256 x 256
 
 struct Shape {
-    int bm, bn, waves;
+    int bm, bn;
 };
 template <typename S>
-constexpr Shape shape() { return {S::BM, S::BN, S::WAVES}; }
+constexpr Shape shape() { return {S::BM, S::BN}; }
 // by Fp8Plan::kind
-constexpr Shape kShapes[] = {{16, 16, kFewWaves}, shape<Thin>(), shape<Flat>(), shape<Middle>(), shape<Wide>(), shape<Large>()};
+constexpr Shape kShapes[] = {{16, 16}, shape<Thin>(), shape<Flat>(), shape<Middle>(), shape<Wide>(), shape<Large>()};
 constexpr int kKinds = int(sizeof(kShapes) / sizeof(kShapes[0]));
 
 template <int ACT, typename S>
@@ -500,14 +497,19 @@ Fp8Plan plan_fp8_linear(int64_t m, int64_t n, int64_t k) {
         p.kind = kind;
         p.bm = kShapes[kind].bm;
         p.bn = kShapes[kind].bn;
-        p.waves = kShapes[kind].waves;
         p.mtiles = ceil_div(m, p.bm);
         p.ntiles = ceil_div(n, p.bn);
         p.gps = int(ceil_div(groups, splits));
         p.splits = int(ceil_div(groups, p.gps));
         return p;
     };
-    if (m <= 16) {
+    // Few rows on a layer that takes memory tens of microseconds: the 16-row kernel reads the rows of x once for every 16 rows
+    // of W, the tiles once for every 128.  us with codes given, rows x K x N, 16-row kernel and tiles: 4 x 8192 x 28672 50 and 53, 8
+    // x 4096 x 16384 19.9 and 18.8, 16 x 2048 x 32768 22 and 15.6, 16 x 28672 x 8192 72 and 48; below the bound 16 x 4096 x 4096
+    // 8.0 and 10.9, 12 x 4096 x 8192 12.9 and 13.6; with four groups 8 x 512 x 131072
+    // 16.6 and 21.5.
+    const bool tiled = m > 4 && groups >= 8 && double(m) * double(n) * double(k) >= 5e8;
+    if (m <= 16 && !tiled) {
         const int64_t tiles = ceil_div(n, int64_t(16));
         int64_t splits = tiles >= 256 ? 1 : 256 / tiles;
         if (splits > groups / 32) splits = groups / 32;
@@ -516,9 +518,11 @@ Fp8Plan plan_fp8_linear(int64_t m, int64_t n, int64_t k) {
         return p;
     }
     // Microseconds: what a launch costs, then for each round of 256 workgroups its steps, bound by their latency or by
-    // what the L2s deliver, then, for a K split, the second launch and its partial sums.
-    constexpr double kLaunch = 4.5, kL2 = 10.5e6, kJoin = 2.5, kPartial = 5e6;
-    constexpr double kStep[kKinds] = {0, 0.3, 0.36, 0.62, 0.8, 1.55};
+    // what the L2s deliver, then, for a K split, the second launch and its partial sums.  The constants are fitted to all
+    // shapes and splits measured on 8 to 512 rows and layers of 768 x 4608 to 28672 x 8192 (1000 times): the plan that the
+    // model takes is 0.4 % behind the best measured on average, 11 % at most (64 rows, 4096 x 16384: 25.8 and 23.2 us).
+    constexpr double kLaunch = 4.5, kL2 = 12.8e6, kJoin = 2.7, kPart = 0.65, kPartial = 4.7e6;
+    constexpr double kStep[kKinds] = {0, 0.48, 0.49, 0.77, 0.94, 1.72};
     Fp8Plan best{};
     double least = 0;
     for (int kind = 1; kind < kKinds; ++kind) {
@@ -537,7 +541,7 @@ Fp8Plan plan_fp8_linear(int64_t m, int64_t n, int64_t k) {
                 t += double(whole ? whole : 1) * p.gps * step;
                 left -= whole ? whole * 256 : left;
             }
-            if (p.splits > 1) t += kJoin + 2.0 * p.splits * m * n * 4 / kPartial;
+            if (p.splits > 1) t += kJoin + kPart * p.splits + 2.0 * p.splits * m * n * 4 / kPartial;
             if (best.bm == 0 || t < least) {
                 best = p;
                 least = t;
@@ -548,7 +552,9 @@ Fp8Plan plan_fp8_linear(int64_t m, int64_t n, int64_t k) {
     return best;
 }
 
-bool fp8_linear_quantizes(int64_t m, const Fp8Plan& p) { return p.kind == 0 && m * p.gps <= kFewGroups; }
+bool fp8_linear_quantizes(int64_t m, const Fp8Plan& p) {
+    return p.kind == 0 && m * p.gps <= kFewGroups && (m * p.gps < 16 ? 16 : m * p.gps) * p.ntiles * p.splits <= kFewInAll;
+}
 
 hipError_t launch_fp8_linear(const Fp8LinearArgs& a, const Fp8Plan& p, int act, bool quantize, int act_fn, hipStream_t stream) {
     const hipError_t e = act == kActBf16 ? run<kActBf16>(a, p, quantize, act_fn, stream) : run<kActF16>(a, p, quantize, act_fn, stream);

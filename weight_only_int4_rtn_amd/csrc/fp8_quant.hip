@@ -15,17 +15,19 @@ namespace w4a16 {
 namespace {
 
 // Rows: 16 lanes a group, 8 values a lane; N groups a lane, all loaded first.
-template <int DT, int AF, int N>
+template <int DT, int AF, int N, bool BY_GROUP>
 __global__ __launch_bounds__(256) void fp8_rows_kernel(Fp8QuantizeArgs a, uint32_t groups, uint32_t total) {
     const int sub = threadIdx.x % 16;
     const uint32_t first = blockIdx.x * uint32_t(16 * N) + threadIdx.x / 16;
     float v[N][8];
+    uint32_t by_group[N];
 #pragma unroll
     for (int u = 0; u < N; ++u) {
         const uint32_t at = min(first + 16 * u, total - 1);
         const uint32_t row = at / groups, g = at - row * groups;
         const int64_t in = int64_t(row) * a.ldx + int64_t(g) * kGroup + sub * 8;
         fp8_load8<DT, AF>(a.x, in, a.k, v[u]);
+        by_group[u] = g * uint32_t(a.m) + row;
     }
 #pragma unroll
     for (int u = 0; u < N; ++u) {
@@ -35,7 +37,7 @@ __global__ __launch_bounds__(256) void fp8_rows_kernel(Fp8QuantizeArgs a, uint32
         const uint2 c = fp8_codes8(v[u], s, top);
         if (at < total) {
             *reinterpret_cast<uint2*>(a.codes + int64_t(at) * kGroup + sub * 8) = c;
-            if (sub == 0) a.scales[at] = s;
+            if (sub == 0) a.scales[BY_GROUP ? by_group[u] : at] = s;
         }
     }
 }
@@ -75,12 +77,17 @@ __global__ __launch_bounds__(256) void fp8_blocks_kernel(Fp8QuantizeArgs a, uint
 // groups) 44.6 and 45.6, 8192 x 16384 89 and 84 (4.79 TB/s, a large copy's rate); with SwiGLU 2048 x 4096 11.5 and 13.2.
 constexpr uint32_t kOneGroup = 600000;
 
-template <int DT, int AF>
+template <int DT, int AF, bool BY_GROUP>
 hipError_t rows(const Fp8QuantizeArgs& a, hipStream_t stream) {
     const uint32_t groups = uint32_t(a.k / kGroup), total = uint32_t(a.m) * groups;
-    if (total < kOneGroup) fp8_rows_kernel<DT, AF, 1><<<dim3(uint32_t(ceil_div(total, 16))), dim3(256), 0, stream>>>(a, groups, total);
-    else fp8_rows_kernel<DT, AF, 4><<<dim3(uint32_t(ceil_div(total, 64))), dim3(256), 0, stream>>>(a, groups, total);
+    if (total < kOneGroup) fp8_rows_kernel<DT, AF, 1, BY_GROUP><<<dim3(uint32_t(ceil_div(total, 16))), dim3(256), 0, stream>>>(a, groups, total);
+    else fp8_rows_kernel<DT, AF, 4, BY_GROUP><<<dim3(uint32_t(ceil_div(total, 64))), dim3(256), 0, stream>>>(a, groups, total);
     return hipGetLastError();
+}
+
+template <int DT, int AF>
+hipError_t rows(const Fp8QuantizeArgs& a, hipStream_t stream) {
+    return a.by_group ? rows<DT, AF, true>(a, stream) : rows<DT, AF, false>(a, stream);
 }
 
 template <int DT>
@@ -97,7 +104,7 @@ hipError_t rows_by_act(const Fp8QuantizeArgs& a, int act_fn, hipStream_t stream)
 hipError_t launch_fp8_quantize(const Fp8QuantizeArgs& a, int dtype, int act_fn, hipStream_t stream) {
     if (dtype == kActBf16) return rows_by_act<kActBf16>(a, act_fn, stream);
     if (dtype == kActF16) return rows_by_act<kActF16>(a, act_fn, stream);
-    return rows<0, kActFnNone>(a, stream);
+    return rows<0, kActFnNone, false>(a, stream);
 }
 
 hipError_t launch_fp8_quantize_blocks(const Fp8QuantizeArgs& a, int dtype, hipStream_t stream) {
