@@ -349,3 +349,43 @@ def test_linear_far_rows():
         want, size = a @ b.t(), a.abs() @ b.abs().t()
         # products cut 2^-13 below the largest of eight: at most 7 x 2^-13 of the eight's sum of sizes; 2048 groups in FP32
         R.within(y[:, -256:].cpu()[:, some], want, size * (7 * 2.0 ** -13 + 2.0 ** -23 * (2048 + 19)), "far rows")
+
+
+# x quantized by the workgroups themselves, by a launch of its own before the kernel of few rows and before tiles; tiles of
+# few rows on a large layer
+@pytest.mark.parametrize("act", ["none", "swiglu"])
+@pytest.mark.parametrize("m,n,k", [(1, 2560, 2048), (1, 131080, 512), (3, 17000, 1024), (8, 300, 2048), (2, 40, 16384), (5, 25000, 4096), (16, 33000, 1024),
+                                   (40, 300, 2048), (300, 513, 1024)])
+def test_linear_equals_linear_of_codes(m, n, k, act):
+    dev = require_gpu()
+    g = torch.Generator(device=dev).manual_seed(n + k)
+    codes = torch.randint(0, 256, (n, k), dtype=torch.uint8, device=dev, generator=g)
+    codes[(codes & 127) == 127] = 0x7E
+    codes = codes.view(torch.float8_e4m3fn)
+    scales = torch.rand(-(-n // 128), k // 128, device=dev, generator=g) * 2.0 ** -10
+    x = rows(m, 2 * k if act == "swiglu" else k, F16, 7, 0.5).to(dev)
+    say("linear of codes", m, n, k, act)
+    cx, sx = w4.quantize_fp8(x, act=ACTS[act])
+    y = w4.linear_fp8(x, codes, scales, act=ACTS[act])
+    z = w4.linear_fp8(cx, codes, scales, x_scales=sx, out_dtype=F16)
+    assert torch.equal(y, z)
+    for block in {0, n // 256, (n - 1) // 128}:
+        at = slice(128 * block, min(n, 128 * block + 128))
+        want, tol = R.linear(bytes_of(cx), sx.cpu().numpy(), bytes_of(codes[at]), scales[block:block + 1].cpu().numpy())
+        R.within(y[:, at], want, tol, f"{m} x {n} x {k} block {block}")
+
+
+def test_rows_far_apart():
+    """Rows of a view further apart than a kernel's strides reach are copied first."""
+    dev = require_gpu()
+    base = torch.zeros(3, (1 << 24) + 8, dtype=BF16, device=dev)
+    x = base[:, :256]
+    x.copy_(rows(3, 256, BF16, 3))
+    same_bits(*w4.quantize_fp8(x), R.quantize_rows(x.float().cpu().numpy()))
+    cw, sw, codes, scales = layer(200, 256, 4, dev)
+    assert torch.equal(w4.linear_fp8(x, codes, scales), w4.linear_fp8(x.contiguous(), codes, scales))
+    cx, sx = w4.quantize_fp8(x)
+    far = torch.zeros(3, (1 << 22) + 16, dtype=torch.uint8, device=dev)
+    far[:, :256] = cx.view(torch.uint8)
+    y = w4.linear_fp8(far.view(torch.float8_e4m3fn)[:, :256], codes, scales, x_scales=sx)
+    assert torch.equal(y, w4.linear_fp8(cx, codes, scales, x_scales=sx))

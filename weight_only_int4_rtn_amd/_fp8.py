@@ -16,6 +16,7 @@ from ._serving import _dense, _device_index, _meta, _no_grad, _launch, _raw_stre
 E4M3 = 3  # W4A16_E4M3 of include/w4a16.h
 CODES = torch.float8_e4m3fn
 _MAX_K = 1 << 22
+_MAX_STEP = {1: _MAX_K, 2: 1 << 24, 4: 1 << 24}  # elements between rows that a kernel takes, by their size
 
 _loaded = None
 
@@ -39,7 +40,7 @@ def _lib():
 
 def _rows(shape, stride, elem: int):
     """(rows, elements between them) of a tensor [..., width] that a kernel can walk, or None: contiguous rows at even
-    distances that are multiples of 16 bytes."""
+    distances that are multiples of 16 bytes, none too long."""
     m = math.prod(shape[:-1])
     if shape[-1] > 1 and stride[-1] != 1:
         return None
@@ -54,7 +55,7 @@ def _rows(shape, stride, elem: int):
         if st != want:
             return None
         want *= n
-    return (m, step) if step >= shape[-1] and step * elem % 16 == 0 else None
+    return (m, step) if shape[-1] <= step <= _MAX_STEP[elem] and step * elem % 16 == 0 else None
 
 
 def _width(width: int, act: Act) -> int:
