@@ -238,7 +238,7 @@ __device__ inline int fp8_swizzle(int row, int piece) { return row * 128 + ((pie
 // side is 75 % busy (9 TB/s).  W straight to registers, 16 rows x 64 bytes an
 // instruction, made the latter 410 us; loading into the L2 ahead, a shared slice
 // of x kept in LDS and workgroups that go on to a second tile gave 0 to 5 %.
-// Few rows are bound by memory's latency: a step of 32 x 128 or 64 x 128 takes 0.48
+// Few rows are bound by memory's latency: a step of 32 x 128 or 64 x 128 takes 0.46
 // us whatever it computes, hence the K splits.
 // ---------------------------------------------------------------------------
 template <int RB_, int CB_, int WM_, int WN_, int R_>
@@ -445,9 +445,12 @@ __global__ __launch_bounds__(256) void fp8_join_kernel(Fp8LinearArgs a, int spli
     }
 }
 
+// Eight waves but for the smallest, two a SIMD, so that one's matrix instructions fill the other's waits: us with eight and
+// with four waves, 128 x 128 at 1024 x 2048 x 2560 12.6 and 15.6, at 512 x 8192 x 8192 46.6 and 52.7; 64 x 128 at 333 x 4096 x 4100
+// 18.0 and 20.2.  Sixteen: 13.1, 45.4 and 18.3.
 using Thin = Fp8Shape<2, 2, 1, 4, 4>;    // 32 x 128
-using Flat = Fp8Shape<4, 2, 1, 4, 4>;    // 64 x 128
-using Middle = Fp8Shape<4, 4, 2, 2, 4>;  // 128 x 128
+using Flat = Fp8Shape<2, 2, 2, 4, 4>;    // 64 x 128
+using Middle = Fp8Shape<4, 2, 2, 4, 4>;  // 128 x 128
 using Wide = Fp8Shape<4, 4, 2, 4, 3>;    // 128 x 256
 using Large = Fp8Shape<8, 4, 2, 4, 2>;   // 256 x 256
 
@@ -520,9 +523,9 @@ Fp8Plan plan_fp8_linear(int64_t m, int64_t n, int64_t k) {
     // Microseconds: what a launch costs, then for each round of 256 workgroups its steps, bound by their latency or by
     // what the L2s deliver, then, for a K split, the second launch and its partial sums.  The constants are fitted to all
     // shapes and splits measured on 8 to 512 rows and layers of 768 x 4608 to 28672 x 8192 (1000 times): the plan that the
-    // model takes is 0.4 % behind the best measured on average, 11 % at most (64 rows, 4096 x 16384: 25.8 and 23.2 us).
-    constexpr double kLaunch = 4.5, kL2 = 12.8e6, kJoin = 2.7, kPart = 0.65, kPartial = 4.7e6;
-    constexpr double kStep[kKinds] = {0, 0.48, 0.49, 0.77, 0.94, 1.72};
+    // model takes is 0.7 % behind the best measured on average, 6 % at most (256 rows, 16384 x 2048: 26.2 and 24.7 us).
+    constexpr double kLaunch = 4.5, kL2 = 13e6, kJoin = 3.0, kPart = 0.6, kPartial = 5e6;
+    constexpr double kStep[kKinds] = {0, 0.46, 0.455, 0.61, 0.89, 1.8};
     Fp8Plan best{};
     double least = 0;
     for (int kind = 1; kind < kKinds; ++kind) {
