@@ -604,7 +604,9 @@ int kv4_prefix_attention_tile_rows(int64_t tokens, int64_t batch, int64_t groups
  *                 nowhere.  table_width is at least 1 also then.
  * The other arguments, limits and roundings are kv4_attention's.  One launch
  * where there is little to share; else two, between which the prefixes' sums pass
- * through the workspace in FP32.
+ * through the workspace in FP32.  Which, on tiles of how many rows and with how
+ * much workspace goes by the tables' widths, and so do the parts of a second
+ * launch over own tokens; the parts that a prefix is cut into go by its length.
  */
 w4a16_status_t kv4_prefix_attention(const void* q, w4a16_dtype_t dtype, int64_t tokens, int64_t ldq, int64_t heads,
                                     int64_t kv_heads, int64_t head_dim, const void* pool, int64_t pages, int64_t page_size,

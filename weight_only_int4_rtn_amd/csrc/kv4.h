@@ -141,7 +141,7 @@ struct Kv4AttentionArgs {
     const int32_t* prefix_table;
     int64_t prefix_width, ldp;
     const int32_t* prefix_lens;
-    int prefix_span, prefix_splits;
+    int prefix_splits;
     // what the splits of the prefixes' launch leave for the other: [splits][tokens][heads] rows of dim sums, then
     // [splits][tokens][heads][2] references and sums of probabilities
     float* parts;

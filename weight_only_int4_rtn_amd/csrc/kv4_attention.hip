@@ -90,6 +90,20 @@ __device__ inline int prefix_len(const Kv4AttentionArgs& a, int group) {
     return int(n < 0 ? 0 : n > room ? room : n);
 }
 
+// Tokens of a part where `tokens` are cut into at most `splits` parts (kPrefix, kBoth): even ones of at least 128 tokens and
+// sqrt(kPartRoot tokens).  The host knows how far a table reaches, the device how long a sequence is, and tables of captured
+// steps have room: parts cut from their width left 64 x 32/8 heads on 8192 tokens in a table of 131072 two parts of 25, 155
+// us, where an exact table took 48.  So the width bounds the grid and the length cuts the parts, by this function in both
+// launches alike.
+template <int PART>
+constexpr int kPartRoot = PART == kPrefix ? 48 : 12;
+template <int PART>
+__host__ __device__ inline int part_span(int tokens, int splits) {
+    const int even = (tokens + splits - 1) / splits, least = int(ceilf(sqrtf(float(kPartRoot<PART>) * float(tokens))));
+    const int span = even > least ? even : least;
+    return span <= 128 ? 128 : (span + 63) / 64 * 64;
+}
+
 // Tiles are numbered without a table: request b's start at
 // floor(cu_q[b] share / ROWS) + b, which leaves room for the ragged last tile
 // of every request (a few tiles stay empty).  Over the prefixes a group takes a
@@ -361,7 +375,8 @@ __device__ inline void leave(const Left& to, const f32x4_t (&acc)[kv4_blocks(D)]
 __device__ inline int prefix_splits(const Kv4AttentionArgs& a, int b) {
     const int group = group_of(a, b);
     if (group < 0) return 0;
-    return max(1, min(a.prefix_splits, (prefix_len(a, group) + a.prefix_span - 1) / a.prefix_span));
+    const int len = prefix_len(a, group), span = part_span<kPrefix>(len, a.prefix_splits);
+    return max(1, min(a.prefix_splits, (len + span - 1) / span));
 }
 
 // A wave begins its running softmax of a row with the prefix's splits first, first + step, ... < live: they are as good as
@@ -434,6 +449,7 @@ __global__ __launch_bounds__(256, D == 256 ? 2 : D == 128 ? 3 : 4) void kv4_atte
     // kBoth: tokens [0, len) are the prefix's, those from `own` on the request's
     const int group = PART == kBoth ? group_of(a, t.b) : -1, len = group < 0 ? 0 : prefix_len(a, group), own = (len + 31) / 32 * 32;
     const int begin = view.lo(p_first) / 32 * 32, end = own + view.hi(p_last, t.kv);
+    if constexpr (PART == kPrefix || PART == kBoth) span = part_span<PART>(end, splits);  // (no window: they begin at 0)
     const int live = max(1, min(splits, (end - begin + span - 1) / span));  // splits with tokens
     if (int(blockIdx.z) >= live) return;
     const int s0 = begin + int(blockIdx.z) * span, s1 = min(end, s0 + span);
@@ -818,6 +834,7 @@ __global__ __launch_bounds__(256, D == 256 ? 2 : 4) void kv4_rows_kernel(Kv4Atte
     const View view{a.causal, int(a.window)};
     const int last = min(t.r0 + ROWS - 1, t.rows - 1);
     const int begin = view.lo(t.position(t.r0 / share)) / STEP * STEP, end = view.hi(t.position(last / share), t.kv);
+    if constexpr (PART == kPrefix) span = part_span<PART>(end, splits);
     const int live = max(1, min(splits, (end - begin + span - 1) / span));
     if (int(blockIdx.y) >= live) return;
     const int s0 = begin + int(blockIdx.y) * span, s1 = min(end, s0 + span);
@@ -1123,13 +1140,10 @@ Kv4PrefixPlan plan_kv4_prefix(int64_t tokens, int64_t batch, int64_t groups, int
                               int64_t prefix_capacity, int64_t capacity, bool ragged, bool causal) {
     Kv4PrefixPlan p{};
     const int64_t share = heads / kv_heads;
-    // Parts of `most` tokens that fill the chip once, of at least sqrt(c most) tokens.
-    auto cut = [&](Kv4Plan& q, int64_t most, int64_t c) {
+    // Parts of `most` tokens that fill the chip once; fewer tokens are cut anew on the device (part_span).
+    auto cut = [&](Kv4Plan& q, int64_t most, auto span_of) {
         const int64_t base = q.tiles * kv_heads, room = 256 * (dim == 256 ? 2 : dim == 64 || q.rows > 16 ? 4 : 3);
-        int64_t least = 128;
-        while (least * least < c * most) least += 64;
-        q.span = base < room ? ceil_div(ceil_div(most, room / base), 64) * 64 : most;
-        if (q.span < least) q.span = least;
+        q.span = span_of(int(most), int(base < room ? room / base : 1));
         q.splits = int(ceil_div(most, q.span));
     };
     // The prefixes.  Tiles of 64 rows share the codes' conversion, tiles of 16 have more workgroups and no barriers in
@@ -1143,12 +1157,12 @@ Kv4PrefixPlan plan_kv4_prefix(int64_t tokens, int64_t batch, int64_t groups, int
     // (the grid of tiles of 64 is one line of tiles and key heads, which has to fit)
     p.prefix.rows = tokens * heads * prefix_capacity < int64_t(24) << 20 || (tokens * share / 64 + groups) * kv_heads >= int64_t(1) << 23 ? 16 : 64;
     p.prefix.tiles = tokens * share / p.prefix.rows + groups;
-    cut(p.prefix, prefix_capacity, 48);
+    cut(p.prefix, prefix_capacity, part_span<kPrefix>);
     // The requests' own tokens, few as a rule: once over the chip where kv4_attention goes twice (64 x 32/8 on 4096, up to
     // 500 of their own: 35 us against 42; up to 4000: 71 and 71).
     p.own = plan_kv4_attention(tokens, batch, heads, kv_heads, dim, capacity, ragged, causal, 0);
     if (!ragged && p.own.splits > 1) {
-        cut(p.own, capacity, 12);
+        cut(p.own, capacity, part_span<kOwn>);
         p.own.workspace = p.own.splits > 1 ? size_t(p.own.tiles * kv_heads) * size_t(p.own.splits) * size_t(p.own.rows / 16) * size_t(16 * dim + 32) * 4 : 0;
     }
     // One launch for both where sharing saves little: every request's tiles (of 16 rows) then walk the prefix too.  us
@@ -1164,7 +1178,7 @@ Kv4PrefixPlan plan_kv4_prefix(int64_t tokens, int64_t batch, int64_t groups, int
         p.own = Kv4Plan{};
         p.own.rows = 16;
         p.own.tiles = tiles;
-        cut(p.own, prefix_capacity + 32 + capacity, 12);
+        cut(p.own, prefix_capacity + 32 + capacity, part_span<kBoth>);
         if (p.own.splits > 1) p.workspace = size_t(tiles * kv_heads) * size_t(p.own.splits) * size_t(16 * dim + 32) * 4;
         return p;
     }
@@ -1179,7 +1193,6 @@ hipError_t launch_kv4_prefix(const Kv4AttentionArgs& a, int act, hipStream_t str
     const Kv4PrefixPlan p = plan_kv4_prefix(o.tokens, o.batch, o.groups, o.heads, o.kv_heads, o.dim, o.prefix_width * o.page,
                                             o.table_width * o.page, o.cu_q != nullptr, o.causal != 0);
     if (p.together) return run_by_type<kBoth>(o, p.own, after_header(o.workspace, 0), act, stream);
-    o.prefix_span = int(p.prefix.span);
     o.prefix_splits = p.prefix.splits;
     Kv4AttentionArgs f = o;
     f.table = a.prefix_table;
