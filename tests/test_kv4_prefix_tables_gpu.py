@@ -88,3 +88,23 @@ def test_parts_in_one_graph_follow_lengths(dev):
         torch.cuda.synchronize()
         b.check(out, prefix=[n], what=f"prefix of {n}")
         assert torch.equal(out, lib.kv4_prefix_attention(*args, **kw))
+
+
+# route, requests of each group, heads, kv_heads, dim, table width of a prefix in pages of 16 (so wide that tall tiles come into question)
+GROUPS = [
+    (0, [1] * 40, 32, 8, 64, 1400), (0, [1] * 24, 16, 2, 256, 4200),
+    (16, [2] * 20, 32, 8, 128, 1300), (16, [1, 2, 3, 0, 4] * 6, 32, 8, 64, 1000), (16, [8] * 6, 16, 8, 256, 2100),
+    (64, [12] * 5, 32, 4, 128, 900), (64, [60, 1, 1, 40], 16, 4, 64, 1000),
+]
+
+
+@pytest.mark.parametrize("rows,each,heads,hk,d,width", GROUPS, ids=[f"t{c[0]}-{len(c[1])}x{max(c[1])}-d{c[4]}" for c in GROUPS])
+def test_many_groups(dev, rows, each, heads, hk, d, width):
+    """Groups of one request, of few and of many, on long tables."""
+    n, batch = len(each), sum(each)
+    b = Batch(dev, [(97 * i + 61) % 400 for i in range(n)], [(31 * i) % 70 for i in range(batch)], [sum(each[:i]) for i in range(n + 1)],
+              heads, hk, d, 16, torch.float16)
+    say("many groups", rows, each, heads, hk, d)
+    out, _, route = call(b, -(-width // b.cache.table.shape[1]))
+    assert route == rows
+    b.check(out, what="many groups")

@@ -1154,8 +1154,14 @@ Kv4PrefixPlan plan_kv4_prefix(int64_t tokens, int64_t batch, int64_t groups, int
     // on 8192 (17) 29 and 29.  A part leaves its sums in memory for the other launch instead of joining them, but that
     // launch has to read them: parts of at least sqrt(48 tokens) (2 x 32/8 on 16384, D = 128: 23 us, sqrt(12 tokens) 24,
     // sqrt(tokens) 29, sqrt(100 tokens) 26); twice as many as fill the chip 49 us for 64 x 32/8 on 8192, 43 once.
+    // A group's last tile is padded: tiles of 64 need 48 rows a group.  us on tiles of 16 against 64, groups x requests on
+    // tokens, 32/8 heads of 128: 64 x 2 on 8192 (8 rows) 127 against 267, 64 x 8 on 2817 (32) 132 against 134, on 16384 502
+    // against 549, 16 x 12 on 6645 with 32/4 (96) 101 against 75.  Over 700 such calls 64 takes on average 1.13 times as
+    // long at 30 to 33 rows a group, 1.01 at 44 to 49, 0.93 at 60 to 65.
     // (the grid of tiles of 64 is one line of tiles and key heads, which has to fit)
-    p.prefix.rows = tokens * heads * prefix_capacity < int64_t(24) << 20 || (tokens * share / 64 + groups) * kv_heads >= int64_t(1) << 23 ? 16 : 64;
+    const bool tall = tokens * heads * prefix_capacity >= int64_t(24) << 20 && tokens * share >= 48 * groups &&
+                      (tokens * share / 64 + groups) * kv_heads < int64_t(1) << 23;
+    p.prefix.rows = tall ? 64 : 16;
     p.prefix.tiles = tokens * share / p.prefix.rows + groups;
     cut(p.prefix, prefix_capacity, part_span<kPrefix>);
     // The requests' own tokens, few as a rule: once over the chip where kv4_attention goes twice (64 x 32/8 on 4096, up to
@@ -1173,7 +1179,8 @@ Kv4PrefixPlan plan_kv4_prefix(int64_t tokens, int64_t batch, int64_t groups, int
     //            17.3, 32 x 8/8 on 1000 (232) 15.5 and 13.9, but 64 x 32/8 on 1000 (376) 20.7 and 23.2
     //   D = 256  2 x 8/1 on 800 (0) 11.2 and 18.5, 64 x 8/1 on 8000 (248) 31 and 37, 64 x 4/4 on 2000 (472) 32 and 23
     const int64_t tiles = ragged ? tokens * share / 16 + batch : batch * ceil_div(share, int64_t(16)), shared = tokens * share / 16 + groups;
-    if (tokens * heads * prefix_capacity < int64_t(24) << 20 && (tiles - shared) * kv_heads * prefix_capacity <= 200000) {
+    // (one request a group shares nothing: 64 x 1 on 16384, D = 128, 223 us together, 244 apart)
+    if (!tall && (tiles - shared) * kv_heads * prefix_capacity <= 200000) {
         p.together = true;
         p.own = Kv4Plan{};
         p.own.rows = 16;
