@@ -1171,16 +1171,23 @@ Kv4PrefixPlan plan_kv4_prefix(int64_t tokens, int64_t batch, int64_t groups, int
         cut(p.own, capacity, part_span<kOwn>);
         p.own.workspace = p.own.splits > 1 ? size_t(p.own.tiles * kv_heads) * size_t(p.own.splits) * size_t(p.own.rows / 16) * size_t(16 * dim + 32) * 4 : 0;
     }
-    // One launch for both where sharing saves little: every request's tiles (of 16 rows) then walk the prefix too.  us
-    // together against apart, with the tile-tokens that sharing saves in thousands, requests x heads / key heads on tokens:
-    //   D = 64   8 x 8/1 on 1000 (3) 8.3 and 11.3, 32 x 32/8 on 1000 (184) 12.7 and 13.3, 64 x 32/8 on 1000 (376) 16.5 and 15.6,
-    //            8 x 16/16 on 1000 (112) 10.4 and 11.1, on 4000 (448) 18.8 and 13.0
-    //   D = 128  4 x 32/8 on 1000 (48) 11.2 and 15.5, 150 x 16/2 on 1000 (148) 18.3 and 20.7, 4 x 8/8 on 8000 (192) 18.6 and
-    //            17.3, 32 x 8/8 on 1000 (232) 15.5 and 13.9, but 64 x 32/8 on 1000 (376) 20.7 and 23.2
-    //   D = 256  2 x 8/1 on 800 (0) 11.2 and 18.5, 64 x 8/1 on 8000 (248) 31 and 37, 64 x 4/4 on 2000 (472) 32 and 23
+    // One launch for both where sharing saves little: every request's tiles (of 16 rows) then walk the prefix too.  What two
+    // launches save are tile-tokens; what they cost, a launch and sums that pass through memory, grows with the rows, and a
+    // tile that many heads share holds more of them: with 4 heads a key head and more the bound grows with them.  us together
+    // against apart, with the saved tile-tokens in thousands, requests x heads / key heads on tokens, exact tables:
+    //   D = 64   8 x 8/1 on 1000 (3) 8.5 and 11.6, 8 x 16/16 on 1000 (115) 10.8 and 11.8, on 4000 (452) 18.1 and 14.9, 32 x 32/8
+    //            on 1000 (188) 12.9 and 13.4, 64 x 32/8 (385) 17.1 and 15.6, 20 x 16/2 on 12000 (217) 17.9 and 19.5
+    //   D = 128  4 x 32/8 on 1000 (16) 11.2 and 14.2, 150 x 16/2 on 1000 (152) 18.3 and 20.4, 4 x 8/8 on 8000 (192) 18.5 and
+    //            18.7, 32 x 8/8 on 1000 (238) 15.9 and 14.4, 64 x 32/8 on 1000 (385) 20.5 and 21.5, 64 x 8/1 on 16000 (496)
+    //            29.3 and 31.1
+    //   D = 256  2 x 8/1 on 800 (0) 11.3 and 18.8, 64 x 8/1 on 8000 (248) 30.9 and 37.1, 40 x 16/4 on 2500 (297) 28.4 and 28.1,
+    //            64 x 4/4 on 2000 (483) 30.6 and 22.4
+    // Over 17000 random calls the routes taken are 1.3 % behind the best of each; with 200000 for all of them 1.9 %.
     const int64_t tiles = ragged ? tokens * share / 16 + batch : batch * ceil_div(share, int64_t(16)), shared = tokens * share / 16 + groups;
     // (one request a group shares nothing: 64 x 1 on 16384, D = 128, 223 us together, 244 apart)
-    if (!tall && (tiles - shared) * kv_heads * prefix_capacity <= 200000) {
+    const int64_t grown = (dim == 128 ? 100000 : 65000) * share;
+    const int64_t little = share < 4 ? 200000 : grown < 500000 ? grown : 500000;
+    if (!tall && (tiles - shared) * kv_heads * prefix_capacity <= little) {
         p.together = true;
         p.own = Kv4Plan{};
         p.own.rows = 16;
