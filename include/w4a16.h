@@ -683,6 +683,14 @@ w4a16_status_t quantize_fp8_blocks(const void* w, w4a16_dtype_t dtype, int64_t n
 size_t fp8_linear_workspace_bytes(w4a16_dtype_t x_dtype, int64_t m, int64_t n, int64_t k);
 
 /*
+ * Rows of x of a workgroup's tile in fp8_linear for these sizes (0: invalid or
+ * empty ones), and, where asked for, its columns of y and the parts that k is
+ * cut into: 16 x 16 is the kernel for few rows, 32 x 128, 64 x 128, 128 x 128,
+ * 128 x 256 and 256 x 256 each one of their own.
+ */
+int fp8_linear_tile(int64_t m, int64_t n, int64_t k, int* columns, int* splits);
+
+/*
  * y = x W^T (+ bias) with W = codes w times their block's scale.
  *   x         device, [m][ldx], k columns; 16-byte aligned rows.  Of BF16 or F16:
  *             act is applied (SwiGLU rows hold [up | gate], 2k columns) and the

@@ -57,6 +57,7 @@ from ._binding import (  # noqa: F401
 )
 from ._fp8 import (  # noqa: F401
     linear_fp8,
+    linear_fp8_tile,
     linear_fp8_workspace_bytes,
     quantize_fp8,
     quantize_fp8_weight,

@@ -32,6 +32,8 @@ def _lib():
         L.quantize_fp8_blocks.restype = i32
         L.fp8_linear_workspace_bytes.argtypes = [i32, i64, i64, i64]
         L.fp8_linear_workspace_bytes.restype = sz
+        L.fp8_linear_tile.argtypes = [i64, i64, i64, ctypes.POINTER(i32), ctypes.POINTER(i32)]
+        L.fp8_linear_tile.restype = i32
         L.fp8_linear.argtypes = [vp, i32, vp, i32, i64, i64, i64, vp, vp, i64, vp, vp, i32, i64, vp, sz, vp]
         L.fp8_linear.restype = i32
         _loaded = L
@@ -122,6 +124,14 @@ def quantize_fp8_weight(w: torch.Tensor) -> tuple[torch.Tensor, torch.Tensor]:
 def linear_fp8_workspace_bytes(m: int, n: int, k: int, codes: bool = False) -> int:
     """Workspace linear_fp8 needs for these sizes (``codes``: x is quantized already)."""
     return int(_lib().fp8_linear_workspace_bytes(E4M3 if codes else BF16, m, n, k))
+
+
+def linear_fp8_tile(m: int, n: int, k: int) -> tuple[int, int, int]:
+    """Rows and columns of a workgroup's tile in linear_fp8 for these sizes, each pair a kernel of its own (16 x 16: the one for
+    few rows), and the parts that k is cut into ((0, 0, 0): invalid or empty sizes)."""
+    columns, splits = ctypes.c_int(), ctypes.c_int()
+    rows = _lib().fp8_linear_tile(m, n, k, ctypes.byref(columns), ctypes.byref(splits))
+    return rows, columns.value, splits.value
 
 
 @_remember

@@ -93,6 +93,14 @@ size_t fp8_linear_workspace_bytes(w4a16_dtype_t x_dtype, int64_t m, int64_t n, i
     return rows + p.workspace ? kSyncBytes + rows + p.workspace : 0;
 }
 
+int fp8_linear_tile(int64_t m, int64_t n, int64_t k, int* columns, int* splits) {
+    const bool valid = valid_linear(m, n, k) && m > 0 && n > 0;
+    const Fp8Plan p = valid ? plan_fp8_linear(m, n, k) : Fp8Plan{};
+    if (columns) *columns = p.bn;
+    if (splits) *splits = p.splits;
+    return p.bm;
+}
+
 w4a16_status_t fp8_linear(const void* x, w4a16_dtype_t x_dtype, const float* x_scales, w4a16_act_t act, int64_t m, int64_t k, int64_t ldx,
                           const void* w, const float* w_scales, int64_t n, const void* bias, void* y, w4a16_dtype_t y_dtype, int64_t ldy,
                           void* workspace, size_t workspace_bytes, void* stream) {

@@ -520,12 +520,14 @@ Fp8Plan plan_fp8_linear(int64_t m, int64_t n, int64_t k) {
         if (p.splits > 1) p.workspace = size_t(tiles) * size_t(p.splits) * (kFewWaves * 64 * 16);
         return p;
     }
-    // Microseconds: what a launch costs, then for each round of 256 workgroups its steps, bound by their latency or by
-    // what the L2s deliver, then, for a K split, the second launch and its partial sums.  The constants are fitted to all
-    // shapes and splits measured on 8 to 512 rows and layers of 768 x 4608 to 28672 x 8192 (1000 times): the plan that the
-    // model takes is 0.7 % behind the best measured on average, 6 % at most (256 rows, 16384 x 2048: 26.2 and 24.7 us).
-    constexpr double kLaunch = 4.5, kL2 = 13e6, kJoin = 3.0, kPart = 0.6, kPartial = 5e6;
-    constexpr double kStep[kKinds] = {0, 0.46, 0.455, 0.61, 0.89, 1.8};
+    // Microseconds: what a launch costs, then for each round of 256 workgroups its steps, bound by the rate of loads into a
+    // unit or by what the L2s deliver, and its beginning and end; then the results, or, for a K split, the second launch and
+    // its partial sums.  The constants are fitted to 6600 calls of 17 to 4096 rows, on layers of 128 x 128 to 16384 x 28672,
+    // with every shape and split measured: the plan that the model takes is 0.7 % behind the best on average (0.8 % on 3400 calls that
+    // it was not fitted to), 5 % at the 95th percentile, 20 % for one in a thousand.  (As times its sums are rougher: 4096 x
+    // 2048 x 32768 293 for 277, 512 x 16384 x 2048 38 for 41, 17 x 2048 x 2560 11.5 for 9.1.)
+    constexpr double kLaunch = 4.5, kL2 = 12.3e6, kStore = 9.5e6, kJoin = 2.7, kPart = 0.5, kPartial = 5e6;
+    constexpr double kStep[kKinds] = {0, 0.45, 0.48, 0.64, 0.91, 1.63}, kEnds[kKinds] = {0, 0.2, 0.4, 0.4, 2.0, 6.4};
     Fp8Plan best{};
     double least = 0;
     for (int kind = 1; kind < kKinds; ++kind) {
@@ -534,17 +536,15 @@ Fp8Plan plan_fp8_linear(int64_t m, int64_t n, int64_t k) {
             Fp8Plan p = cut(kind, splits);
             if (p.splits == before) continue;
             before = p.splits;
-            const int64_t wgs = p.mtiles * p.ntiles * p.splits;
+            const int64_t wgs = p.mtiles * p.ntiles * p.splits, whole = wgs / 256, rest = wgs % 256;
             const double bytes = 128.0 * (p.bm + p.bn);
-            double t = kLaunch;
-            for (int64_t left = wgs, round = 0; left > 0 && round < 2; ++round) {
-                // all whole rounds at once, then what is left
-                const int64_t whole = left / 256, now = whole ? 256 : left;
-                const double step = now * bytes / kL2 > kStep[kind] ? now * bytes / kL2 : kStep[kind];
-                t += double(whole ? whole : 1) * p.gps * step;
-                left -= whole ? whole * 256 : left;
-            }
-            if (p.splits > 1) t += kJoin + kPart * p.splits + 2.0 * p.splits * m * n * 4 / kPartial;
+            auto round = [&](int64_t now) {
+                const double rate = now * bytes / kL2;
+                return p.gps * (rate > kStep[kind] ? rate : kStep[kind]) + kEnds[kind];
+            };
+            double t = kLaunch + whole * round(256) + (rest ? round(rest) : 0.0);
+            if (p.splits == 1) t += 2.0 * m * n / kStore;
+            else t += kJoin + kPart * p.splits + 8.0 * p.splits * m * (p.ntiles * p.bn) / kPartial;
             if (best.bm == 0 || t < least) {
                 best = p;
                 least = t;
