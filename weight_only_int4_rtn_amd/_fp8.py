@@ -177,7 +177,7 @@ def linear_fp8(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, bias:
     then of ``out_dtype`` (default bfloat16).  See fp8_linear in include/w4a16.h."""
     tag, out_tag, act, out_dtype, m, n, k, rows, shape, need = _linear_plan(_meta(x), _meta(codes), _meta(scales), _meta(bias),
                                                                             _meta(x_scales), out_dtype, act)
-    _no_grad(x, scales, bias, x_scales)
+    _no_grad(x, codes, scales, bias, x_scales)
     index = _device_index(x, codes, scales, bias, x_scales, workspace)
     if rows is None or x.data_ptr() % 16:
         x = x.clone(memory_format=torch.contiguous_format)
