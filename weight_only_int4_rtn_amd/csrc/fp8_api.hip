@@ -110,11 +110,10 @@ w4a16_status_t fp8_linear(const void* x, w4a16_dtype_t x_dtype, const float* x_s
         return W4A16_EUNSUPPORTED;
     const int64_t width = width_of(act, k);
     const size_t elem = bytes_of(x_dtype);
-    if (!valid_linear(m, n, k) || ldx < width || ldx > (codes ? kMaxK : kMaxDim) || ldx * int64_t(elem) % 16 != 0 || ldy < n || ldy > kMaxDim ||
-        codes != (x_scales != nullptr))
+    if (!valid_linear(m, n, k) || ldx < width || ldx > (codes ? kMaxK : kMaxDim) || ldx * int64_t(elem) % 16 != 0 || ldy < n || ldy > kMaxDim)
         return W4A16_EINVAL;
-    if (m == 0 || n == 0) return W4A16_OK;
-    if (!x || !w || !w_scales || !y) return W4A16_EINVAL;
+    if (m == 0 || n == 0) return W4A16_OK;  // (an empty tensor's scales have no address)
+    if (!x || !w || !w_scales || !y || codes != (x_scales != nullptr)) return W4A16_EINVAL;
     if (!aligned(x, 16) || !aligned(w, 16) || !aligned(x_scales, 4) || !aligned(w_scales, 4) || !aligned(bias, 2) || !aligned(y, 2))
         return W4A16_EINVAL;
     const int64_t groups = k / kGroup;
