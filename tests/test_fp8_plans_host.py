@@ -21,3 +21,11 @@ NEAR_BEST = {
 @pytest.mark.parametrize("size", NEAR_BEST, ids=["x".join(map(str, s)) for s in NEAR_BEST])
 def test_plan_is_near_the_best(size):
     assert w4.linear_fp8_tile(*size) in NEAR_BEST[size]
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 64, 16384), (12, 64, 16384), (1, 16, 131072), (3, 2048, 16384)])
+def test_few_rows_leave_one_vector_a_lane_and_part(m, n, k):
+    """Parts of the kernel for few rows meet in 64 vectors of 16 bytes a tile and part, behind the header."""
+    rows, columns, splits = w4.linear_fp8_tile(m, n, k)
+    assert (rows, columns) == (16, 16) and splits > 1
+    assert w4.linear_fp8_workspace_bytes(m, n, k, codes=True) == (1 << 20) + -(-n // 16) * splits * 64 * 16

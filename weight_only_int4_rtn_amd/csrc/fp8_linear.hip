@@ -72,29 +72,26 @@ __device__ inline void store_part(const Fp8LinearArgs& a, int split, int64_t npa
     for (int i = 0; i < N; i += 4) *reinterpret_cast<float4*>(to + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
 }
 
-// The end of a K split of few rows: every part stores its FP32 sums past the L2 (SC1: the XCDs' L2s are not coherent) and
-// counts itself; the one that completes the count gets true and all the sums, added in the order of the parts, and clears
-// the counter for the next call.  Nobody waits.  slot: this tile's, a vector a thread and part; flag: an int of LDS that
-// nobody uses any more.
-__device__ inline bool join_parts(float (&acc)[4], float* slot, unsigned* counter, int split, int splits, int* flag) {
-    const int bytes = int(blockDim.x) * 16, at = int(threadIdx.x) * 16;
-    const __amdgpu_buffer_rsrc_t sl = buffer_rsrc(slot, int64_t(splits) * bytes);
-    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, f32x4_t{acc[0], acc[1], acc[2], acc[3]}), sl, split * bytes + at, 0, kCoherent);
+// The end of a K split of few rows, by one wave of every part: it stores the part's FP32 sums past the L2 (SC1: the XCDs' L2s
+// are not coherent) and counts the part; the one that completes the count gets true and all the sums, added in the order of
+// the parts, and clears the counter for the next call.  Nobody waits.  slot: this tile's, a vector a lane and part.
+__device__ inline bool join_parts(float (&acc)[4], float* slot, unsigned* counter, int split, int splits) {
+    constexpr int kBytes = 64 * 16;
+    const int lane = threadIdx.x % 64, at = lane * 16;
+    const __amdgpu_buffer_rsrc_t sl = buffer_rsrc(slot, int64_t(splits) * kBytes);
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, f32x4_t{acc[0], acc[1], acc[2], acc[3]}), sl, split * kBytes + at, 0, kCoherent);
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        const unsigned before = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        *flag = before == unsigned(splits - 1);
-        if (*flag) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    }
-    __syncthreads();
-    if (!*flag) return false;
+    unsigned before = 0;
+    if (lane == 0) before = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (uniform(int(before)) != splits - 1) return false;
+    if (lane == 0) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // (the sums are read behind the count)
 #pragma unroll
     for (int e = 0; e < 4; ++e) acc[e] = 0.0f;
     for (int s = 0; s < splits; s += 8) {  // eight loads in flight
         u32x4 part[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) part[i] = __builtin_amdgcn_raw_buffer_load_b128(sl, min(s + i, splits - 1) * bytes + at, 0, kCoherent);
+        for (int i = 0; i < 8; ++i) part[i] = __builtin_amdgcn_raw_buffer_load_b128(sl, min(s + i, splits - 1) * kBytes + at, 0, kCoherent);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
 #pragma unroll
@@ -127,7 +124,6 @@ constexpr int64_t kFewInAll = 32768;
 template <int ACT, bool QUANTIZE, int AF>
 __global__ __launch_bounds__(64 * kFewWaves) void fp8_few_kernel(Fp8LinearArgs a, int splits, int gps) {
     __shared__ f32x4_t sums[kFewWaves][64];
-    __shared__ int flag;
     __shared__ __align__(16) uint8_t codes[QUANTIZE ? kFewGroups * kGroup : 16];  // [m][ng][128]
     __shared__ float scales[QUANTIZE ? kFewGroups : 1];                           // [m][ng]
     const int lane = threadIdx.x % 64, wave = uniform(threadIdx.x / 64);
@@ -206,14 +202,14 @@ __global__ __launch_bounds__(64 * kFewWaves) void fp8_few_kernel(Fp8LinearArgs a
     }
     sums[wave][lane] = acc;
     __syncthreads();
-    // every wave adds all four, so that a split's join has the whole workgroup's loads; the first stores
+    if (wave != 0) return;
     float tot[4] = {};
 #pragma unroll
     for (int w = 0; w < kFewWaves; ++w)
 #pragma unroll
         for (int e = 0; e < 4; ++e) tot[e] += sums[w][lane][e];
-    if (splits > 1 && !join_parts(tot, a.slots + tile * splits * (kFewWaves * 64 * 4), a.counters + tile, split, splits, &flag)) return;
-    if (wave != 0 || r >= a.m) return;
+    if (splits > 1 && !join_parts(tot, a.slots + tile * splits * (64 * 4), a.counters + tile, split, splits)) return;
+    if (r >= a.m) return;
     store_row<ACT, 4>(a, r, n0 + 4 * kq, tot);
 }
 
@@ -517,7 +513,7 @@ Fp8Plan plan_fp8_linear(int64_t m, int64_t n, int64_t k) {
         int64_t splits = tiles >= 256 ? 1 : 256 / tiles;
         if (splits > groups / 32) splits = groups / 32;
         Fp8Plan p = cut(0, splits < 1 ? 1 : splits);
-        if (p.splits > 1) p.workspace = size_t(tiles) * size_t(p.splits) * (kFewWaves * 64 * 16);
+        if (p.splits > 1) p.workspace = size_t(tiles) * size_t(p.splits) * (64 * 16);
         return p;
     }
     // Microseconds: what a launch costs, then for each round of 256 workgroups its steps, bound by the rate of loads into a
