@@ -3,26 +3,13 @@
 // reads device memory ("Piper Kernels", section "Validation contract").
 #include "w4a16.h"
 
+#include "checks.h"
 #include "common.h"
 #include "kernels.h"
 
 using namespace w4a16;
 
 namespace {
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-// [lo, hi) byte ranges overlap?
-bool overlap(const void* a, size_t an, const void* b, size_t bn) {
-    if (!a || !b || an == 0 || bn == 0) return false;
-    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
-    return a0 < b0 + bn && b0 < a0 + an;
-}
-
-size_t span_bytes(int64_t rows, int64_t cols, int64_t ld, size_t elem) {
-    if (rows <= 0 || cols <= 0) return 0;
-    return (size_t(rows - 1) * size_t(ld) + size_t(cols)) * elem;
-}
 
 // Sizes are limited so every internal offset fits comfortably in int64 and
 // grid dimensions stay within HIP's limits.
@@ -44,8 +31,6 @@ bool is_gemm(w4a16_path_t p) { return p == W4A16_PATH_GEMM || p == W4A16_PATH_GE
 bool valid_nk(int64_t n, int64_t k) {
     return n >= 0 && n <= kMaxDim && k > 0 && k <= kMaxDim && k % kGroup == 0;
 }
-
-w4a16_status_t from_hip(hipError_t e) { return e == hipSuccess ? W4A16_OK : W4A16_EHIP; }
 
 size_t path_workspace(w4a16_path_t path, int64_t m, int64_t n, int64_t k, int bits) {
     switch (path) {

@@ -3,6 +3,7 @@
 // launches.
 #include "w4a16.h"
 
+#include "checks.h"
 #include "fp8.h"
 #include "kernels.h"
 
@@ -14,24 +15,8 @@ constexpr int64_t kMaxDim = int64_t(1) << 24;
 constexpr int64_t kMaxK = int64_t(1) << 22;       // 256 rows of codes are addressed with 31 bits
 constexpr int64_t kMaxGroups = int64_t(1) << 30;  // groups of a quantization, workgroups of a launch
 
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-bool overlap(const void* a, size_t an, const void* b, size_t bn) {
-    if (!a || !b || an == 0 || bn == 0) return false;
-    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
-    return a0 < b0 + bn && b0 < a0 + an;
-}
-
-size_t span_bytes(int64_t rows, int64_t cols, int64_t ld, size_t elem) {
-    if (rows <= 0 || cols <= 0) return 0;
-    return (size_t(rows - 1) * size_t(ld) + size_t(cols)) * elem;
-}
-
 size_t round16(size_t v) { return (v + 15) & ~size_t(15); }
 
-w4a16_status_t from_hip(hipError_t e) { return e == hipSuccess ? W4A16_OK : W4A16_EHIP; }
-
-bool act_dtype(w4a16_dtype_t t) { return t == W4A16_BF16 || t == W4A16_F16; }
 int kernel_dtype(w4a16_dtype_t t) { return t == W4A16_BF16 ? kActBf16 : t == W4A16_F16 ? kActF16 : 0; }
 size_t bytes_of(w4a16_dtype_t t) { return t == W4A16_F32 ? 4 : t == W4A16_E4M3 ? 1 : 2; }
 

@@ -5,6 +5,7 @@
 
 #include "w4a16.h"
 
+#include "checks.h"
 #include "kernels.h"
 #include "kv4.h"
 #include "lora.h"
@@ -23,22 +24,6 @@ constexpr int64_t kMaxCacheTokens = int64_t(1) << 23;         // appended or rea
 constexpr uint64_t kMaxPoolBytes = uint64_t(1) << 38;         // scales are addressed in units of 64 bytes
 constexpr int64_t kMaxLoraRank = 128;
 
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-bool overlap(const void* a, size_t an, const void* b, size_t bn) {
-    if (!a || !b || an == 0 || bn == 0) return false;
-    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
-    return a0 < b0 + bn && b0 < a0 + an;
-}
-
-size_t span_bytes(int64_t rows, int64_t cols, int64_t ld, size_t elem) {
-    if (rows <= 0 || cols <= 0) return 0;
-    return (size_t(rows - 1) * size_t(ld) + size_t(cols)) * elem;
-}
-
-w4a16_status_t from_hip(hipError_t e) { return e == hipSuccess ? W4A16_OK : W4A16_EHIP; }
-
-bool act_dtype(w4a16_dtype_t t) { return t == W4A16_BF16 || t == W4A16_F16; }
 int act_of(w4a16_dtype_t t) { return t == W4A16_BF16 ? kActBf16 : kActF16; }
 
 bool valid_pool(int64_t pages, int64_t page, int64_t kv_heads, int64_t dim) {
